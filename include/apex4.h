@@ -45,7 +45,7 @@ typedef int32_t apex4_status;
 
 #define APEX4_OK 0
 #define APEX4_ERR_INVALID_ARG 1  /* a size or pointer is out of the documented range */
-#define APEX4_ERR_UNSUPPORTED 2  /* a group-size combination this library does not run */
+#define APEX4_ERR_UNSUPPORTED 2  /* a group-size or type combination this library does not run */
 #define APEX4_ERR_ALIGNMENT 3    /* a pointer lacks the documented alignment */
 #define APEX4_ERR_WORKSPACE 4    /* workspace smaller than apex4_gemm_workspace_size() */
 #define APEX4_ERR_HIP 5          /* the HIP runtime reported an error at launch */
@@ -324,6 +324,134 @@ apex4_status apex4_gemm_w4a4_f6(const void* qa6, const float* s_a, const void* q
  */
 apex4_status apex4_select_granularity(int64_t M, int64_t N, int64_t K, double min_rel_speed,
                                       int32_t* group_a, int32_t* group_w);
+
+/*
+ * Sparse expert layers and 8-bit layers: the parts of a W4A4 model that are
+ * not one dense W4A4 product.
+ *
+ * Element types of the calls below that take one.
+ */
+#define APEX4_F32 0
+#define APEX4_F16 1
+#define APEX4_BF16 2
+/* Scores of apex4_route. */
+#define APEX4_SCORE_SOFTMAX 0
+#define APEX4_SCORE_SIGMOID 1
+
+/*
+ * Routing of M tokens to k of E experts each.
+ *     p[m,e] = softmax over e of logits[m,:], or 1 / (1 + exp(-logits[m,e]))
+ *     key[m,e] = p[m,e] + bias[e]   (bias NULL: the experts are ranked by
+ *                their logits, which the scores rise with)
+ * With n_group > 1 the experts form n_group runs of E / n_group; a group's
+ * score is the sum of its group_top (1 or 2) best keys (of fewer where fewer
+ * are live; without a bias the sum of the two best scores, or the best
+ * logit), and only the experts of the topk_group best groups can be chosen.
+ * The k experts with the largest keys are chosen, in descending order; equal
+ * keys, and equal groups, go to the lowest index.  An expert whose logit or
+ * key is -inf or NaN is masked: it takes no part in the softmax and is not
+ * chosen.  A place without a live expert left gets id -1 and gate 0 (a row of
+ * padding with all logits -inf routes nowhere; apex4_experts_w4a4 does no
+ * work for such places).  A logit of +inf counts as the largest fp32 number.
+ *     gates[m,j] = scale * p[m, ids[m,j]], divided by the sum of the chosen
+ *                  p[m, .] first when renormalize is nonzero (a sum of zero
+ *                  gives gates of zero).  The bias never enters the gates.
+ * Ranks that depend on a computed score, and the gates, are computed in 64
+ * bits.
+ *   logits [M, E] of logits_type (APEX4_F32, APEX4_F16 or APEX4_BF16),
+ *   bias [E] fp32 or NULL; ids [M, k] int32, gates [M, k] fp32 (outputs).
+ *   0 <= M <= 2^26 (0: no-op), 1 <= E <= 1024, 1 <= k <= 64; n_group >= 1 divides E,
+ *   n_group <= 64, 1 <= topk_group <= n_group, k <= topk_group * E / n_group,
+ *   group_top 1 or 2; score APEX4_SCORE_SOFTMAX or APEX4_SCORE_SIGMOID; scale
+ *   finite.  Pointers aligned to their elements.  Asynchronous on `stream`.
+ */
+apex4_status apex4_route(const void* logits, int32_t logits_type, int64_t M, int64_t E, int32_t score,
+                         const float* bias, int32_t n_group, int32_t topk_group, int32_t group_top, int32_t k,
+                         int32_t renormalize, float scale, int32_t* ids, float* gates, void* stream);
+
+/*
+ * The experts' feed-forward network over routed tokens, every product W4A4
+ * with groups of 128 (the rule of apex4_quantize_act for both activations):
+ *     for every slot (m, j) with 0 <= e = ids[m,j] < E:
+ *         [g; u] = W4A4(x[m], gate_up[e])             (I gate rows, then I up rows)
+ *         h      = fp16(silu(g) * u), kept within +-65504, silu(g) = g / (1 + exp(-g))
+ *         d      = W4A4(h, down[e])
+ *     y[m] = sum over j of gates[m,j] * d             (fp32, j ascending; then fp16)
+ * g, u and d are fp32 sums and are not rounded.  A slot with another id (-1
+ * of apex4_route, an expert that lives elsewhere) costs no product and adds
+ * nothing, whatever its gate; a token without a slot gets zeros.  A token may
+ * name an expert more than once.
+ *   x_f16 [M, H] fp16, 16-byte aligned;  ids [M, k] int32, gates [M, k] fp32.
+ *   qw_gate_up [E, 2I, H/2] and s_gate_up [E, 2I, H/128], qw_down [E, H, I/2]
+ *   and s_down [E, H, I/128]: apex4_pack_weight outputs with group 128 (of the
+ *   matrices stacked to [E * rows, columns]); codes 16-byte, scales 4-byte
+ *   aligned.
+ *   group: 128 (other groups: APEX4_ERR_UNSUPPORTED).
+ *   y_f16 [M, H] fp16, 16-byte aligned;  y_f32 [M, H] fp32 before that
+ *   rounding, or NULL.
+ *   workspace: at least apex4_experts_workspace_size() bytes (0 for invalid or
+ *   empty sizes), 256-byte aligned, caller-owned, overwritten; calls that
+ *   share one workspace race.
+ *   M >= 0 (0: no-op), 1 <= k <= 64, 1 <= E <= 1024, H and I positive
+ *   multiples of 128, M * k < 2^31, M * k * I < 2^34,
+ *   2 * I * H < 2^32, (M + k) * H < 2^32.
+ * The results do not depend on timing: no atomics, every sum in a fixed
+ * order.  Asynchronous on `stream`; every check runs on the host before
+ * anything is launched.
+ */
+size_t apex4_experts_workspace_size(int64_t M, int32_t k, int64_t E, int64_t H, int64_t I, int32_t group);
+apex4_status apex4_experts_w4a4(const void* x_f16, const int32_t* ids, const float* gates, int64_t M, int32_t k,
+                                int64_t E, int64_t H, int64_t I, int32_t group, const void* qw_gate_up,
+                                const float* s_gate_up, const void* qw_down, const float* s_down, void* y_f16,
+                                float* y_f32, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * 8-bit floating point (OCP E4M3) with a scale for each block of 128: one per
+ * row and 128 columns of the activations, one per 128 x 128 of the weights.
+ *     s = max|v| / 448 over the block (fp32, correctly rounded)
+ *     q = e4m3(clamp(v / s, -448, 448)), round to nearest even of the
+ *         correctly rounded fp32 quotient;  s == 0 gives q = 0
+ *     y[m,n] = sum_j s_a[m,j] * s_w[n/128, j] * sum_{k in block j} qa[m,k] * qw[n,k]
+ * with an fp32 sum over the blocks, in no fixed order of the additions.  The
+ * sum of a block comes from the FP8 matrix instruction, which adds 8
+ * neighbouring products aligned to the largest of them, cut below 2^-13 of
+ * it, and those sums in fp32.  These are 8-bit values of their own, unlike the INT4 codes
+ * in E4M3 bytes of apex4_quantize_f8 / apex4_gemm_w4a4_f8.
+ *
+ * apex4_quantize_e4m3: activations, x [rows, K] of x_type (APEX4_F16 or
+ * APEX4_BF16, 16-byte aligned) -> q8 [rows, K] bytes (8-byte aligned), s
+ * [rows, K/128] fp32.  apex4_pack_weight_e4m3: weights, w [N, K] of w_type ->
+ * q8 [N, K] bytes, s [ceil(N/128), K/128] fp32 (the last block of rows may be
+ * short).  0 <= rows, N <= 2^26 (0: no-op), 0 < K < 2^23, K % 128 == 0,
+ * rows * K and N * K < 2^34.
+ */
+apex4_status apex4_quantize_e4m3(const void* x, int32_t x_type, int64_t rows, int64_t K, void* q8, float* s,
+                                 void* stream);
+apex4_status apex4_pack_weight_e4m3(const void* w, int32_t w_type, int64_t N, int64_t K, void* q8, float* s,
+                                    void* stream);
+
+/*
+ * apex4_gemm_e4m3: the product above from quantized operands.
+ *   qa8 [M, K], qw8 [N, K] bytes, 16-byte aligned; s_a [M, K/128], s_w
+ *   [ceil(N/128), K/128] fp32.  y [M, N] of y_type (APEX4_F16 or APEX4_BF16,
+ *   round to nearest even), y_f32 [M, N] fp32 before that rounding, or NULL.
+ *   workspace: at least apex4_gemm_e4m3_workspace_size() bytes (NULL allowed
+ *   when that is 0), 16-byte aligned, caller-owned, overwritten; calls that
+ *   share one workspace race.
+ *   0 <= M, N <= 2^26 (either 0: no-op), 0 < K < 2^23, K % 128 == 0, M * K and N * K < 2^34.
+ *
+ * apex4_linear_e4m3: apex4_quantize_e4m3(x) into the workspace, then
+ * apex4_gemm_e4m3, with the bits of those two calls; y has the type of x.
+ *   workspace: at least apex4_linear_e4m3_workspace_size() bytes, 256-byte aligned.
+ */
+size_t apex4_gemm_e4m3_workspace_size(int64_t M, int64_t N, int64_t K);
+apex4_status apex4_gemm_e4m3(const void* qa8, const float* s_a, const void* qw8, const float* s_w, int64_t M,
+                             int64_t N, int64_t K, int32_t y_type, void* y, float* y_f32, void* workspace,
+                             size_t workspace_bytes, void* stream);
+size_t apex4_linear_e4m3_workspace_size(int64_t M, int64_t N, int64_t K);
+apex4_status apex4_linear_e4m3(const void* x, int32_t x_type, const void* qw8, const float* s_w, int64_t M,
+                               int64_t N, int64_t K, void* y, float* y_f32, void* workspace,
+                               size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -43,6 +43,17 @@ SIGNATURES = {
     "apex4_gemm_w4a4_f6": (_I32, [_P, _P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "apex4_select_granularity": (_I32, [_I64, _I64, _I64, ctypes.c_double,
                                         ctypes.POINTER(_I32), ctypes.POINTER(_I32)]),
+    "apex4_route": (_I32, [_P, _I32, _I64, _I64, _I32, _P, _I32, _I32, _I32, _I32, _I32, ctypes.c_float,
+                           _P, _P, _P]),
+    "apex4_experts_workspace_size": (ctypes.c_size_t, [_I64, _I32, _I64, _I64, _I64, _I32]),
+    "apex4_experts_w4a4": (_I32, [_P, _P, _P, _I64, _I32, _I64, _I64, _I64, _I32, _P, _P, _P, _P, _P, _P,
+                                  _P, ctypes.c_size_t, _P]),
+    "apex4_quantize_e4m3": (_I32, [_P, _I32, _I64, _I64, _P, _P, _P]),
+    "apex4_pack_weight_e4m3": (_I32, [_P, _I32, _I64, _I64, _P, _P, _P]),
+    "apex4_gemm_e4m3_workspace_size": (ctypes.c_size_t, [_I64, _I64, _I64]),
+    "apex4_gemm_e4m3": (_I32, [_P, _P, _P, _P, _I64, _I64, _I64, _I32, _P, _P, _P, ctypes.c_size_t, _P]),
+    "apex4_linear_e4m3_workspace_size": (ctypes.c_size_t, [_I64, _I64, _I64]),
+    "apex4_linear_e4m3": (_I32, [_P, _I32, _P, _P, _I64, _I64, _I64, _P, _P, _P, ctypes.c_size_t, _P]),
     "apex4_probe_mfma_i8": (_I32, [_I64, _P, ctypes.POINTER(ctypes.c_double), _P]),
     "apex4_probe_mfma_f6": (_I32, [_I64, _P, ctypes.POINTER(ctypes.c_double), _P]),
     "apex4_probe_hbm_read": (_I32, [_P, _I64, _P, ctypes.POINTER(ctypes.c_double), _P]),
@@ -357,6 +368,206 @@ def select_granularity(M: int, N: int, K: int, min_rel_speed: float = 0.75) -> t
     _check("apex4_select_granularity",
            lib().apex4_select_granularity(M, N, K, min_rel_speed, ctypes.byref(ga), ctypes.byref(gw)))
     return ga.value, gw.value
+
+
+# element types of the calls that take one (APEX4_F32, APEX4_F16, APEX4_BF16)
+_TYPE_NAMES = ("float32", "float16", "bfloat16")
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _type_code(t, name: str, allowed=_TYPE_NAMES) -> int:
+    n = str(t.dtype).replace("torch.", "")
+    if n not in allowed:
+        raise ValueError(f"{name} must be one of {', '.join(allowed)}, got {n}")
+    return _TYPE_NAMES.index(n)
+
+
+def _call(fn: str, device, *args) -> None:
+    """One library call with `device` current (a launch goes to the current
+    device, the tensors' may be another one), on torch's current stream there."""
+    import torch
+    f = getattr(lib(), fn)
+    if torch.cuda.current_device() == device.index:
+        status = f(*args, _stream(torch, device))
+    else:
+        with torch.cuda.device(device):
+            status = f(*args, _stream(torch, device))
+    _check(fn, status)
+
+
+def route(logits, k: int, *, score: str = "softmax", bias=None, n_group: int = 1, topk_group: int = 1,
+          group_top: int = 1, renormalize: bool = True, scale: float = 1.0, out=None):
+    """apex4_route: logits [M, E] (float32, float16 or bfloat16 GPU tensor) ->
+    (ids int32 [M, k], gates float32 [M, k]).  score: "softmax" or "sigmoid";
+    bias: float32 [E] added to the scores for the ranking only; the experts of
+    the topk_group best of n_group groups (a group's score: the sum of its
+    group_top best) can be chosen; ties go to the lowest index; masked places
+    (logits of -inf) get id -1 and gate 0.  `out`: (ids, gates) to write."""
+    import torch
+    _need_gpu(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be [M, E], got {tuple(logits.shape)}")
+    if score not in _SCORES:
+        raise ValueError(f"unknown score {score!r}; one of {tuple(_SCORES)}")
+    code = _type_code(logits, "logits")
+    (M, E), dev = logits.shape, logits.device
+    if bias is not None:
+        _need_gpu(bias, "bias", torch.float32, (E,), dev)
+    if out is None:
+        n = max(k, 0)
+        ids = torch.empty((M, n), dtype=torch.int32, device=dev)
+        gates = torch.empty((M, n), dtype=torch.float32, device=dev)
+    else:
+        ids, gates = out
+        _need_gpu(ids, "ids", torch.int32, (M, k), dev)
+        _need_gpu(gates, "gates", torch.float32, (M, k), dev)
+    _call("apex4_route", dev, logits.data_ptr(), code, M, E, _SCORES[score], _ptr(bias), n_group, topk_group,
+          group_top, k, int(bool(renormalize)), scale, ids.data_ptr(), gates.data_ptr())
+    return ids, gates
+
+
+def experts_workspace_size(M: int, k: int, E: int, H: int, I: int, group: int = 128) -> int:
+    return int(lib().apex4_experts_workspace_size(M, k, E, H, I, group))
+
+
+def experts(x, ids, gates, qw_gate_up, s_gate_up, qw_down, s_down, *, group: int = 128, want_y32: bool = False,
+            y16=None, y32=None, workspace=None):
+    """apex4_experts_w4a4: the experts' network y[m] = sum_j gates[m,j] *
+    down_e(silu(gate_e x) * up_e x), e = ids[m,j], on W4A4 products with groups
+    of 128.  x: fp16 [M, H]; ids int32, gates float32 [M, k] (route's outputs;
+    ids outside [0, E) add nothing); qw_gate_up uint8 [E, 2I, H/2], s_gate_up
+    float32 [E, 2I, H/128], qw_down uint8 [E, H, I/2], s_down float32
+    [E, H, I/128] (pack_weight of the stacked matrices).  Returns y16 [M, H],
+    or (y16, y32) with want_y32.  `workspace`: a uint8 GPU tensor of at least
+    experts_workspace_size() bytes (allocated here when None)."""
+    import torch
+    _need_gpu(x, "x", torch.float16)
+    if x.dim() != 2 or ids.dim() != 2 or qw_gate_up.dim() != 3 or qw_down.dim() != 3:
+        raise ValueError("experts takes x [M, H], ids [M, k] and weights [E, rows, bytes]")
+    (M, H), dev, k = x.shape, x.device, ids.shape[1]
+    E, I = qw_gate_up.shape[0], 2 * qw_down.shape[2]
+    _need_gpu(ids, "ids", torch.int32, (M, k), dev)
+    _need_gpu(gates, "gates", torch.float32, (M, k), dev)
+    _need_gpu(qw_gate_up, "qw_gate_up", torch.uint8, (E, 2 * I, H // 2), dev)
+    _need_gpu(s_gate_up, "s_gate_up", torch.float32, (E, 2 * I, _cols(H, group)), dev)
+    _need_gpu(qw_down, "qw_down", torch.uint8, (E, H, I // 2), dev)
+    _need_gpu(s_down, "s_down", torch.float32, (E, H, _cols(I, group)), dev)
+    # caller buffers are checked before anything is allocated
+    if y16 is not None:
+        _need_gpu(y16, "y16", torch.float16, (M, H), dev)
+    if y32 is not None:
+        _need_gpu(y32, "y32", torch.float32, (M, H), dev)
+    if workspace is not None:
+        _need_gpu(workspace, "workspace", torch.uint8, None, dev)
+    if y16 is None:
+        y16 = torch.empty((M, H), dtype=torch.float16, device=dev)
+    if want_y32 and y32 is None:
+        y32 = torch.empty((M, H), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(experts_workspace_size(M, k, E, H, I, group), dtype=torch.uint8, device=dev)
+    _call("apex4_experts_w4a4", dev, x.data_ptr(), ids.data_ptr(), gates.data_ptr(), M, k, E, H, I, group,
+          qw_gate_up.data_ptr(), s_gate_up.data_ptr(), qw_down.data_ptr(), s_down.data_ptr(), y16.data_ptr(),
+          _ptr(y32), workspace.data_ptr(), workspace.numel())
+    return (y16, y32) if want_y32 else y16
+
+
+_HALVES = ("float16", "bfloat16")
+
+
+def quantize_e4m3(x, out=None):
+    """x: fp16 or bf16 [rows, K] GPU tensor -> (q8 uint8 [rows, K] E4M3 bytes, s float32
+    [rows, K/128]), a scale max|x| / 448 for 128 columns of a row (apex4_quantize_e4m3)."""
+    import torch
+    _need_gpu(x, "x")
+    code = _type_code(x, "x", _HALVES)
+    rows, K = x.shape
+    if out is None:
+        q8 = torch.empty((rows, K), dtype=torch.uint8, device=x.device)
+        s = torch.empty((rows, K // 128), dtype=torch.float32, device=x.device)
+    else:
+        q8, s = out
+        _need_gpu(q8, "q8", torch.uint8, (rows, K), x.device)
+        _need_gpu(s, "s", torch.float32, (rows, K // 128), x.device)
+    _call("apex4_quantize_e4m3", x.device, _ptr(x), code, rows, K, _ptr(q8), _ptr(s))
+    return q8, s
+
+
+def pack_weight_e4m3(w):
+    """w: fp16 or bf16 [N, K] GPU tensor -> (q8 uint8 [N, K] E4M3 bytes, s float32
+    [ceil(N/128), K/128]), a scale for each 128 x 128 block (apex4_pack_weight_e4m3)."""
+    import torch
+    _need_gpu(w, "w")
+    code = _type_code(w, "w", _HALVES)
+    N, K = w.shape
+    q8 = torch.empty((N, K), dtype=torch.uint8, device=w.device)
+    s = torch.empty(((N + 127) // 128, K // 128), dtype=torch.float32, device=w.device)
+    _call("apex4_pack_weight_e4m3", w.device, _ptr(w), code, N, K, _ptr(q8), _ptr(s))
+    return q8, s
+
+
+def gemm_e4m3(qa8, sa, qw8, sw, dtype=None, *, want_y32: bool = False, y=None, y32=None, workspace=None):
+    """apex4_gemm_e4m3: y = the product of E4M3 operands with a scale for each block of 128
+    (quantize_e4m3 and pack_weight_e4m3 outputs).  dtype: torch.float16 (the default) or
+    torch.bfloat16.  Returns y [M, N], or (y, y32) with want_y32."""
+    import torch
+    dtype = torch.float16 if dtype is None else dtype
+    M, K = qa8.shape
+    N, dev = qw8.shape[0], qa8.device
+    _need_gpu(qa8, "qa8", torch.uint8, (M, K), dev)
+    _need_gpu(qw8, "qw8", torch.uint8, (N, K), dev)
+    _need_gpu(sa, "s_a", torch.float32, (M, K // 128), dev)
+    _need_gpu(sw, "s_w", torch.float32, ((N + 127) // 128, K // 128), dev)
+    # caller buffers are checked before anything is allocated
+    if y is not None:
+        _need_gpu(y, "y", dtype, (M, N), dev)
+    if y32 is not None:
+        _need_gpu(y32, "y32", torch.float32, (M, N), dev)
+    if workspace is not None:
+        _need_gpu(workspace, "workspace", torch.uint8, None, dev)
+    if y is None:
+        y = torch.empty((M, N), dtype=dtype, device=dev)
+    code = _type_code(y, "y", _HALVES)
+    if want_y32 and y32 is None:
+        y32 = torch.empty((M, N), dtype=torch.float32, device=dev)
+    if workspace is None:
+        need = int(lib().apex4_gemm_e4m3_workspace_size(M, N, K))
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    _call("apex4_gemm_e4m3", dev, _ptr(qa8), _ptr(sa), _ptr(qw8), _ptr(sw), M, N, K, code, _ptr(y), _ptr(y32),
+          _ptr(workspace), 0 if workspace is None else workspace.numel())
+    return (y, y32) if want_y32 else y
+
+
+def linear_e4m3_workspace_size(M: int, N: int, K: int) -> int:
+    return int(lib().apex4_linear_e4m3_workspace_size(M, N, K))
+
+
+def linear_e4m3(x, qw8, sw, *, want_y32: bool = False, y=None, y32=None, workspace=None):
+    """apex4_linear_e4m3: y = x W^T with x (fp16 or bf16 [M, K]) quantized on the fly to E4M3
+    and W packed by pack_weight_e4m3.  Returns y [M, N] of x's type, or (y, y32) with
+    want_y32.  `workspace`: a uint8 GPU tensor of at least linear_e4m3_workspace_size()
+    bytes (allocated here when None)."""
+    import torch
+    _need_gpu(x, "x")
+    code = _type_code(x, "x", _HALVES)
+    (M, K), N, dev = x.shape, qw8.shape[0], x.device
+    _need_gpu(qw8, "qw8", torch.uint8, (N, K), dev)
+    _need_gpu(sw, "s_w", torch.float32, ((N + 127) // 128, K // 128), dev)
+    # caller buffers are checked before anything is allocated
+    if y is not None:
+        _need_gpu(y, "y", x.dtype, (M, N), dev)
+    if y32 is not None:
+        _need_gpu(y32, "y32", torch.float32, (M, N), dev)
+    if workspace is not None:
+        _need_gpu(workspace, "workspace", torch.uint8, None, dev)
+    if y is None:
+        y = torch.empty((M, N), dtype=x.dtype, device=dev)
+    if want_y32 and y32 is None:
+        y32 = torch.empty((M, N), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(linear_e4m3_workspace_size(M, N, K), dtype=torch.uint8, device=dev)
+    _call("apex4_linear_e4m3", dev, x.data_ptr(), code, qw8.data_ptr(), sw.data_ptr(), M, N, K, y.data_ptr(),
+          _ptr(y32), workspace.data_ptr(), workspace.numel())
+    return (y, y32) if want_y32 else y
 
 
 def _probe(name: str, *args):

@@ -1,0 +1,284 @@
+// The experts' W4A4 feed-forward network over routed tokens on gfx950.
+//
+//     g, u = W4A4(x_m, gate_up_e);  h = f16(silu(g) u);  d = W4A4(h, down_e);
+//     y_m = sum_j gates[m, j] d_(m, j)        for the slots (m, j), e = ids[m, j]
+//
+// Slots are put in the order of their experts once (plan_kernel: the sorted
+// row of every slot and the first row of every expert), the activation codes
+// are quantized per token, and the products run per expert over its rows.
+#include "internal.h"
+#include "rows_stream.h"
+
+namespace apex4 {
+namespace {
+
+size_t align256(size_t b) { return (b + 255) & ~size_t(255); }
+
+// The workspace, in this order.
+struct Parts {
+    int32_t* offsets;    // [E + 1] first sorted row of every expert; [E]: the live rows
+    int32_t* order;      // [R] slot of a sorted row (rows past offsets[E]: unset)
+    int32_t* place;      // [R] sorted row of a slot, -1 for a slot without an expert
+    uint8_t* xq;         // [M, H/2] codes of x
+    float* xs;           // [M, H/128]
+    _Float16* h;         // [R, I]
+    uint8_t* hq;         // [R, I/2]
+    float* hs;           // [R, I/128]
+    float* d;            // [R, H]
+    size_t bytes;
+};
+
+Parts parts_of(void* ws, int64_t M, int32_t k, int32_t E, int32_t H, int32_t I)
+{
+    const int64_t R = M * k;
+    uint8_t* p = static_cast<uint8_t*>(ws);
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        uint8_t* q = p + at;
+        at += align256(bytes);
+        return q;
+    };
+    Parts w;
+    w.offsets = reinterpret_cast<int32_t*>(take((size_t)(E + 1) * 4));
+    w.order = reinterpret_cast<int32_t*>(take((size_t)R * 4));
+    w.place = reinterpret_cast<int32_t*>(take((size_t)R * 4));
+    w.xq = take((size_t)M * (H / 2));
+    w.xs = reinterpret_cast<float*>(take((size_t)M * (H / 128) * 4));
+    w.h = reinterpret_cast<_Float16*>(take((size_t)R * I * 2));
+    w.hq = take((size_t)R * (I / 2));
+    w.hs = reinterpret_cast<float*>(take((size_t)R * (I / 128) * 4));
+    w.d = reinterpret_cast<float*>(take((size_t)R * H * 4));
+    w.bytes = at;
+    return w;
+}
+
+// The slots in the order of their experts, and in slot order within one: a
+// counting sort without a word between workgroups.  Workgroup e reads all R
+// ids, counts those below e and those equal to e (its first row), and reads
+// them again to place its own; the ids stay in L2.  Each wave takes a
+// contiguous run of slots, so that only the waves' counts cross the barrier.
+constexpr int PLAN_WAVES = 16;
+__global__ __launch_bounds__(64 * PLAN_WAVES) void plan_kernel(const int32_t* __restrict__ ids, int32_t R, int32_t E,
+                                                               int32_t* __restrict__ offsets,
+                                                               int32_t* __restrict__ order,
+                                                               int32_t* __restrict__ place)
+{
+    __shared__ int below[PLAN_WAVES], equal[PLAN_WAVES];
+    const int e = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int per = ((R + PLAN_WAVES - 1) / PLAN_WAVES + 63) / 64 * 64;
+    const int64_t first = (int64_t)wave * per;
+    const int last = (int)min((int64_t)R, first + per);
+    int lt = 0, eq = 0;
+    for (int64_t s = first + lane; s < last; s += 64) {
+        const int id = ids[s];
+        lt += id >= 0 && id < e;
+        eq += id == e;
+        // slots without an expert: one workgroup says so
+        if (e == 0 && (id < 0 || id >= E)) place[s] = -1;
+    }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) {
+        lt += __shfl_xor(lt, o);
+        eq += __shfl_xor(eq, o);
+    }
+    if (lane == 0) {
+        below[wave] = lt;
+        equal[wave] = eq;
+    }
+    __syncthreads();
+    int row = 0, count = 0;
+    for (int w = 0; w < PLAN_WAVES; ++w) {
+        row += below[w];
+        if (w < wave) row += equal[w];
+        count += equal[w];
+    }
+    if (threadIdx.x == 0) {
+        offsets[e] = row;
+        if (e == E - 1) offsets[E] = row + count;
+    }
+    if (equal[wave] == 0) return;
+    for (int64_t s0 = first; s0 < last; s0 += 64) {
+        const int64_t s = s0 + lane;
+        const bool mine = s < last && ids[s] == e;
+        const uint64_t who = __ballot(mine);
+        if (mine) {
+            const int r = row + __popcll(who & ((1ull << lane) - 1));
+            order[r] = (int)s;
+            place[s] = r;
+        }
+        row += __popcll(who);
+    }
+}
+
+struct ProductArgs {
+    const int32_t* offsets;
+    const int32_t* order;
+    const uint8_t* qx;
+    const float* sx;
+    const uint8_t* qw;     // [E, N, K/2]
+    const float* sw;       // [E, N, K/128]
+    int32_t k, E, N, K;
+    _Float16* h;           // UP: [R, N/2]
+    float* d;              // else [R, N]
+};
+
+// The expert of launch row y: every expert in turn where there is one launch
+// row per expert, else the y-th expert that has rows (-1: there are fewer).
+__device__ inline int expert_of(const int32_t* __restrict__ offsets, int E, int y, int launched)
+{
+    if (launched == E) return y;
+    const int lane = threadIdx.x & 63;
+    for (int e0 = 0; e0 < E; e0 += 64) {
+        const int e = e0 + lane;
+        const bool some = e < E && offsets[e + 1] > offsets[e];
+        uint64_t who = __ballot(some);
+        const int n = __popcll(who);
+        if (y < n) {
+            for (; y > 0; --y) who &= who - 1;
+            return e0 + __ffsll((unsigned long long)who) - 1;
+        }
+        y -= n;
+    }
+    return -1;
+}
+
+// Few rows per expert: blockIdx.y is an expert, blockIdx.x 16 of its weight
+// rows (UP: 8 gate rows and the 8 up rows of the same columns of h, so that
+// the product silu(g) u is formed here).
+template <bool UP>
+__global__ __launch_bounds__(rows::THREADS) void experts_rows_kernel(ProductArgs a)
+{
+    using namespace rows;
+    __shared__ Shared<false> sh;
+    const int e = __builtin_amdgcn_readfirstlane(expert_of(a.offsets, a.E, blockIdx.y, gridDim.y));
+    if (e < 0) return;
+    const int first = a.offsets[e], count = a.offsets[e + 1] - first;
+    const int n0 = blockIdx.x * (UP ? 8 : 16), half = a.N / 2;
+    const int64_t rowbytes = a.K / 2, G = a.K / 128;
+    const uint8_t* qw = a.qw + (int64_t)e * a.N * rowbytes;
+    const float* sw = a.sw + (int64_t)e * a.N * G;
+    auto row_of = [&](int r) -> int64_t { return UP ? (r < 8 ? n0 + r : half + n0 + r - 8) : n0 + r; };
+    auto wrow = [&](int r) { return qw + row_of(r) * rowbytes; };
+    auto swrow = [&](int r) { return sw + row_of(r) * G; };
+    const int lane = threadIdx.x & 63;
+
+    auto pass = [&](auto tc, int m0) {
+        constexpr int TILES = decltype(tc)::value;
+        const uint8_t* xrow[TILES];
+        const float* sarow[TILES];
+#pragma unroll
+        for (int i = 0; i < TILES; ++i) {
+            const int m = m0 + 16 * i + (lane & 15);
+            xrow[i] = nullptr;
+            sarow[i] = nullptr;
+            if (m < count) {
+                const int64_t r = UP ? a.order[first + m] / a.k : first + m;
+                xrow[i] = a.qx + r * rowbytes;
+                sarow[i] = a.sx + r * G;
+            }
+        }
+        stream<false, TILES>(sh, a.K, wrow, swrow, xrow, sarow);
+        if (UP) {
+            for (int j = threadIdx.x; j < TILES * 128; j += THREADS) {
+                const int t = j >> 7, m = (j >> 3) & 15, c = j & 7;
+                if (m0 + 16 * t + m < count) {
+                    // weight row c (and 8 + c) of activation row m: lane 16 (row >> 2) + m, element row & 3
+                    const float g = sh.red[0][t][(16 * (c >> 2) + m) * 4 + (c & 3)];
+                    const float u = sh.red[0][t][(16 * (2 + (c >> 2)) + m) * 4 + (c & 3)];
+                    float v = g / (1.0f + expf(-g)) * u;
+                    v = fminf(fmaxf(v, -65504.0f), 65504.0f);
+                    a.h[(int64_t)(first + m0 + 16 * t + m) * half + n0 + c] = (_Float16)v;
+                }
+            }
+        } else {
+            for (int j = threadIdx.x; j < TILES * 256; j += THREADS) {
+                const int t = j >> 8, m = (j >> 4) & 15, c = j & 15;
+                if (m0 + 16 * t + m < count)
+                    a.d[(int64_t)(first + m0 + 16 * t + m) * a.N + n0 + c] =
+                        sh.red[0][t][(16 * (c >> 2) + m) * 4 + (c & 3)];
+            }
+        }
+        __syncthreads();   // sh.red is written again
+    };
+    for (int m0 = 0; m0 < count; m0 += 64) {
+        if (count - m0 <= 16) pass(std::integral_constant<int, 1>{}, m0);
+        else if (count - m0 <= 32) pass(std::integral_constant<int, 2>{}, m0);
+        else pass(std::integral_constant<int, 4>{}, m0);
+    }
+}
+
+// y = the sum of a token's slots, in slot order, one rounding to fp16 at the end.
+__global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ d, const int32_t* __restrict__ place,
+                                                      const float* __restrict__ gates, int32_t k, int32_t H,
+                                                      int64_t n4, _Float16* __restrict__ y16, float* __restrict__ y32)
+{
+    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (t >= n4) return;
+    const int per = H / 4;
+    const int64_t m = t / per;
+    const int c = (int)(t - m * per) * 4;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < k; ++j) {
+        const int r = place[m * k + j];
+        if (r < 0) continue;
+        const float g = gates[m * k + j];
+        const float4 v = *reinterpret_cast<const float4*>(d + (int64_t)r * H + c);
+        s[0] = fmaf(g, v.x, s[0]);
+        s[1] = fmaf(g, v.y, s[1]);
+        s[2] = fmaf(g, v.z, s[2]);
+        s[3] = fmaf(g, v.w, s[3]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float v = s[i];
+        asm volatile("" : "+v"(v));   // y16 is the fp16 rounding of y32
+        y16[m * H + c + i] = (_Float16)v;
+        if (y32) y32[m * H + c + i] = v;
+    }
+}
+
+}  // namespace
+
+size_t experts_workspace_bytes(int64_t M, int32_t k, int32_t E, int32_t H, int32_t I)
+{
+    return parts_of(nullptr, M, k, E, H, I).bytes;
+}
+
+hipError_t launch_experts(const ExpertsProblem& p, hipStream_t stream)
+{
+    const Parts w = parts_of(p.ws, p.M, p.k, p.E, p.H, p.I);
+    const int32_t R = (int32_t)(p.M * p.k);
+    plan_kernel<<<p.E, 64 * PLAN_WAVES, 0, stream>>>(p.ids, R, p.E, w.offsets, w.order, w.place);
+    hipError_t e = launch_quantize(p.x, p.M, p.H, 128, w.xq, w.xs, stream);
+    if (e != hipSuccess) return e;
+    const int launched = R < p.E ? R : p.E;
+    ProductArgs a{};
+    a.offsets = w.offsets;
+    a.order = w.order;
+    a.k = p.k;
+    a.E = p.E;
+    a.qx = w.xq;
+    a.sx = w.xs;
+    a.qw = p.qw_gu;
+    a.sw = p.s_gu;
+    a.N = 2 * p.I;
+    a.K = p.H;
+    a.h = w.h;
+    experts_rows_kernel<true><<<dim3(p.I / 8, launched), rows::THREADS, 0, stream>>>(a);
+    e = launch_quantize(w.h, R, p.I, 128, w.hq, w.hs, stream);
+    if (e != hipSuccess) return e;
+    a.qx = w.hq;
+    a.sx = w.hs;
+    a.qw = p.qw_down;
+    a.sw = p.s_down;
+    a.N = p.H;
+    a.K = p.I;
+    a.d = w.d;
+    experts_rows_kernel<false><<<dim3(p.H / 16, launched), rows::THREADS, 0, stream>>>(a);
+    const int64_t n4 = p.M * (p.H / 4);
+    combine_kernel<<<(unsigned)((n4 + 255) / 256), 256, 0, stream>>>(w.d, w.place, p.gates, p.k, p.H, n4,
+                                                                     static_cast<_Float16*>(p.y16), p.y32);
+    return hipGetLastError();
+}
+
+}  // namespace apex4
