@@ -12,28 +12,15 @@
 // about 2e-5 of the sum of |products|, a tenth of the rounding of the output to
 // fp16 and less of bf16's; widening the codes for the fp16 instruction would
 // halve the matrix rate.
+#include "gemm_e4m3.h"
 #include "internal.h"
 #include "rows_stream.h"
 
 namespace apex4 {
 namespace {
 
-template <bool BF16>
-__device__ inline float from16(uint16_t b)
-{
-    if (BF16) return __builtin_bit_cast(float, (uint32_t)b << 16);
-    return (float)__builtin_bit_cast(_Float16, b);
-}
-
-// round to nearest, ties to even; bf16 by arithmetic on the bits (a NaN keeps a mantissa bit)
-template <bool BF16>
-__device__ inline uint16_t to16(float v)
-{
-    if (!BF16) return __builtin_bit_cast(uint16_t, (_Float16)v);
-    const uint32_t b = __builtin_bit_cast(uint32_t, v);
-    if (v != v) return (uint16_t)((b >> 16) | 0x40);
-    return (uint16_t)((b + 0x7fff + ((b >> 16) & 1)) >> 16);
-}
+using e4m3::from16;
+using e4m3::to16;
 
 struct Eight {
     float v[8];
@@ -195,6 +182,7 @@ size_t e4m3_workspace_bytes(const E4m3Problem&) { return 0; }
 
 hipError_t launch_gemm_e4m3(const E4m3Problem& p, hipStream_t stream)
 {
+    if (p.M > 64) return launch_e4m3_tiled(p, stream);
     const unsigned blocks = (unsigned)((p.N + rows::ROWS - 1) / rows::ROWS);
     if (p.bf16) e4m3_rows_kernel<true><<<blocks, rows::THREADS, 0, stream>>>(p);
     else e4m3_rows_kernel<false><<<blocks, rows::THREADS, 0, stream>>>(p);

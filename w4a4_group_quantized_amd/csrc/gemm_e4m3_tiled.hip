@@ -1,0 +1,250 @@
+// The 8-bit block-scaled product (apex4_gemm_e4m3) in LDS tiles on gfx950.
+#include "gemm_e4m3.h"
+#include "internal.h"
+
+namespace apex4 {
+namespace {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void lds_void;
+
+constexpr int KB = 128;          // K values (bytes of a row) per stage: one block
+
+struct TileArgs {
+    E4m3Problem p;
+    int tiles_n, tiles_m;
+    int nparts;
+    float* part;
+};
+
+__device__ inline __amdgpu_buffer_rsrc_t buffer_of(const void* p, uint32_t bytes)
+{
+    // raw buffer: loads past `bytes` return zeros
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, 0x00020000);
+}
+
+// 16 bytes a lane from memory straight to 1 KB of LDS
+__device__ inline void copy_1k(const uint8_t* src, uint32_t bytes, uint8_t* dst, int voff, int soff)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_of(src, bytes), (lds_void*)dst, 16, voff, soff, 0, 0);
+}
+
+// Every copy of the stage has landed (vmcnt(0)) and every wave is done with
+// the other buffer; no memory access moves across.
+__device__ inline void stage_barrier()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    // (the builtin, which the compiler counts: an inline-asm wait would make
+    // it wait for the next stage's copies before the first fragment read)
+    __builtin_amdgcn_s_waitcnt(0xF70);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+template <bool BF16, int WN, int WM, int NT, int MT>
+__global__ __launch_bounds__(WN* WM * 64, 2) void e4m3_tile_kernel(TileArgs a)
+{
+    constexpr int BN = WN * NT * 16, BM = WM * MT * 16, WAVES = WN * WM;
+    constexpr int LOADS = (BN + BM) / 8 / WAVES;     // 1 KB copies per wave and stage
+    static_assert(BN % (WAVES * 8) == 0 && BM % (WAVES * 8) == 0, "a copy step is of w or of x");
+    constexpr int STAGE = (BN + BM) * KB;
+    __shared__ __attribute__((aligned(1024))) uint8_t buf0[STAGE];
+    __shared__ __attribute__((aligned(1024))) uint8_t buf1[STAGE];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = wave % WN, wm = wave / WN;
+    const E4m3Problem& p = a.p;
+
+    int lin = blockIdx.x;
+    const int per = (int)gridDim.x >> 3;
+    if (lin < per * 8) lin = (lin & 7) * per + (lin >> 3);
+    // bands of 4 row blocks, walked column by column: the 32 tiles that an XCD
+    // has in flight share 4 blocks of x and 8 of w
+    const int band = 4 * a.tiles_n, g4 = lin / band, local = lin - g4 * band;
+    const int brows = min(4, a.tiles_m - 4 * g4);
+    const int by = 4 * g4 + local % brows, bx = local / brows;
+    const int m0 = by * BM, n0 = bx * BN;
+    const int K = p.K, G = K / KB;
+    const int s0 = 0, stages = G;
+    const int rows_m = min(BM, p.M - m0), rows_n = min(BN, p.N - n0);
+    const __amdgpu_buffer_rsrc_t rSA = buffer_of(p.sa + (int64_t)m0 * G, (uint32_t)rows_m * G * 4);
+    const int nblk = n0 / 128, nblks = (rows_n + 127) / 128;
+    const __amdgpu_buffer_rsrc_t rSW = buffer_of(p.sw + (int64_t)nblk * G, (uint32_t)nblks * G * 4);
+
+    // Copy j of this wave brings rows 8 (j WAVES + wave) .. + 7 of the stage's
+    // BN rows of w and BM rows of x, 128 bytes each; lane l fetches chunk
+    // (l & 7) ^ (row & 7) of row l >> 3, so that the fragment reads of 8 rows
+    // at one column touch every bank once.  A descriptor per copy, so
+    // that one lane offset serves all of them and rows past the end read zeros.
+    const uint8_t* src[LOADS];
+    uint32_t bytes[LOADS];
+#pragma unroll
+    for (int j = 0; j < LOADS; ++j) {
+        const int r = j * WAVES * 8;
+        const bool w = r < BN;
+        const int first = w ? r : r - BN;
+        const int left = max(0, (w ? rows_n : rows_m) - first);
+        src[j] = w ? p.qw + (int64_t)(n0 + first) * K : p.qa + (int64_t)(m0 + first) * K;
+        bytes[j] = __builtin_amdgcn_readfirstlane((uint32_t)min(left, WAVES * 8) * K);
+    }
+    const int voff = (8 * wave + (lane >> 3)) * K + ((lane & 7) ^ (lane >> 3)) * 16;
+    auto copy = [&](uint8_t* dst, int t) {
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j)
+            copy_1k(src[j], bytes[j], dst + (j * WAVES + wave) * 1024, voff, (s0 + t) * KB);
+    };
+
+    // scales of four stages at a time: one register set, reloaded as soon as
+    // the last of the four stages has taken its values
+    uint32_t saoff[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) saoff[i] = (uint32_t)(wm * MT * 16 + i * 16 + (lane & 15)) * G * 4;
+    const uint32_t swoff = (uint32_t)(wn * NT * 16 / 128) * G * 4;
+    v4f sa[MT], sw;
+    auto load_scales = [&](int t) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+            sa[i] = __builtin_bit_cast(
+                v4f, __builtin_amdgcn_raw_buffer_load_b128(rSA, (int)saoff[i] + (s0 + t) * 4, 0, 0));
+        sw = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rSW, (int)swoff + (s0 + t) * 4, 0, 0));
+    };
+
+    // Fragment offsets: row lane & 15, chunks (lane >> 4) + 4 j (any split of
+    // the block's K over the lanes will do, alike for both operands).  A
+    // 16-byte LDS read serves lanes 0-3, 12-15 and 20-27 in one cycle, then
+    // the others: with neighbouring chunks in neighbouring lane groups their
+    // 16 rows lie in 16 different places of the 256 bytes (chunks 2 (lane >>
+    // 4) + j took two cycles).
+    const int row = lane & 15, key = row & 7;
+    int foff[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) foff[j] = row * KB + (((lane >> 4) + 4 * j) ^ key) * 16;
+    const int wbase = wn * NT * 16 * KB, xbase = (BN + wm * MT * 16) * KB;
+
+    v4f acc[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = v4f{};
+
+    auto frag = [&](const uint8_t* b) {
+        const v4i lo = *reinterpret_cast<const v4i*>(b + foff[0]);
+        const v4i hi = *reinterpret_cast<const v4i*>(b + foff[1]);
+        return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    };
+    auto compute = [&](const uint8_t* b, const float (&S)[MT]) {
+        v8i x[MT], w[2];
+        v4f P[2][MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) x[i] = frag(b + xbase + i * 16 * KB);
+        w[0] = frag(b + wbase);
+#pragma unroll
+        for (int j = 0; j <= NT; ++j) {
+            if (j + 1 < NT) w[(j + 1) & 1] = frag(b + wbase + (j + 1) * 16 * KB);
+            // the products of w tile j beside the fold of tile j - 1, kept in
+            // this order: left alone, the compiler folds each product at once
+            // and waits for the matrix unit
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                if (j < NT)
+                    P[j & 1][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w[j & 1], x[i], v4f{}, 0, 0, 0, 127,
+                                                                                  0, 127);
+                if (j > 0)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        acc[i][j - 1][r] = fmaf(S[i], P[(j - 1) & 1][i][r], acc[i][j - 1][r]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    };
+
+    load_scales(0);
+    copy(buf0, 0);
+    for (int t0 = 0; t0 < stages; t0 += 4) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+            const int t = t0 + h;
+            if (t >= stages) break;
+            stage_barrier();
+            if (t + 1 < stages) copy(h & 1 ? buf0 : buf1, t + 1);
+            float S[MT];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) S[i] = sa[i][h] * sw[h];
+            if (h == 3) load_scales(t + 1);
+            compute(h & 1 ? buf1 : buf0, S);
+        }
+    }
+
+    // --- epilogue: a lane holds 4 neighbouring columns of 16 rows per tile;
+    // the wave's MT*16 x NT*16 outputs go through LDS (its own part of the
+    // stage buffers, 8-byte pieces, piece c of row m at c ^ (m & 15)) and leave
+    // in 16-byte stores that cover whole rows of the tile.  (Stored from the
+    // accumulators, 2 bytes a lane, they took 30 us a tile.) ---
+    __syncthreads();
+    constexpr int ROW = NT * 16 * 2;                  // bytes of a row of the wave's tile
+    static_assert(ROW == 256 && MT * 16 * ROW * WAVES <= 2 * STAGE, "the wave's tile in LDS");
+    constexpr int PER_BUF = STAGE / (MT * 16 * ROW);  // waves per stage buffer
+    uint8_t* out = (wave < PER_BUF ? buf0 : buf1) + (wave % PER_BUF) * MT * 16 * ROW;
+    const int c0 = n0 + wn * NT * 16, r0 = m0 + wm * MT * 16;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const int lm = i * 16 + (lane & 15), m = r0 + lm;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            uint16_t h[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                float v = acc[i][j][r];
+                asm volatile("" : "+v"(v));           // y is the rounding of y32
+                h[r] = e4m3::to16<BF16>(v);
+                const int n = c0 + j * 16 + 4 * (lane >> 4) + r;
+                if (p.y32 && m < p.M && n < p.N) p.y32[(int64_t)m * p.N + n] = v;
+            }
+            *reinterpret_cast<uint2*>(out + lm * ROW + ((4 * j + (lane >> 4)) ^ (lm & 15)) * 8) =
+                make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+        }
+    }
+    uint16_t* y = static_cast<uint16_t*>(p.y);
+    if (p.N % 8 == 0 && (reinterpret_cast<uintptr_t>(y) & 15) == 0) {
+#pragma unroll 4
+        for (int q = 0; q < MT * 16 / 4; ++q) {
+            const int lm = 4 * q + (lane >> 4), c = 2 * (lane & 15);
+            const uint2 u = *reinterpret_cast<const uint2*>(out + lm * ROW + (c ^ (lm & 15)) * 8);
+            const uint2 v = *reinterpret_cast<const uint2*>(out + lm * ROW + ((c + 1) ^ (lm & 15)) * 8);
+            const int m = r0 + lm, n = c0 + 4 * c;
+            if (m < p.M && n < p.N)
+                *reinterpret_cast<uint4*>(y + (int64_t)m * p.N + n) = make_uint4(u.x, u.y, v.x, v.y);
+        }
+    } else {
+        // rows that start anywhere: 2 bytes a lane, a row's 128 columns in two steps
+        for (int q = 0; q < MT * 16 * 2; ++q) {
+            const int lm = q >> 1, c = 64 * (q & 1) + lane, m = r0 + lm, n = c0 + c;
+            if (m < p.M && n < p.N)
+                y[(int64_t)m * p.N + n] =
+                    *reinterpret_cast<const uint16_t*>(out + lm * ROW + ((c >> 2) ^ (lm & 15)) * 8 + (c & 3) * 2);
+        }
+    }
+}
+
+}  // namespace
+
+hipError_t launch_e4m3_tiled(const E4m3Problem& p, hipStream_t stream)
+{
+    TileArgs a{};
+    a.p = p;
+    a.tiles_m = (p.M + 255) / 256;
+    a.tiles_n = (p.N + 255) / 256;
+    a.nparts = 1;
+    const int tiles = a.tiles_m * a.tiles_n;
+    if (p.bf16) e4m3_tile_kernel<true, 2, 4, 8, 4><<<tiles, 512, 0, stream>>>(a);
+    else e4m3_tile_kernel<false, 2, 4, 8, 4><<<tiles, 512, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace apex4
