@@ -29,6 +29,7 @@ __device__ inline uint16_t to16(float v)
 
 }  // namespace e4m3
 
+size_t e4m3_tiled_workspace_bytes(const E4m3Problem& p);
 hipError_t launch_e4m3_tiled(const E4m3Problem& p, hipStream_t stream);
 
 }  // namespace apex4

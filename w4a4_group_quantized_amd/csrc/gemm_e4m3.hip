@@ -178,7 +178,7 @@ hipError_t launch_pack_e4m3(const void* w, bool bf16, int64_t N, int64_t K, void
     return hipGetLastError();
 }
 
-size_t e4m3_workspace_bytes(const E4m3Problem&) { return 0; }
+size_t e4m3_workspace_bytes(const E4m3Problem& p) { return p.M > 64 ? e4m3_tiled_workspace_bytes(p) : 0; }
 
 hipError_t launch_gemm_e4m3(const E4m3Problem& p, hipStream_t stream)
 {

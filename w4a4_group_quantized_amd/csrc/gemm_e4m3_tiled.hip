@@ -17,7 +17,10 @@ constexpr int KB = 128;          // K values (bytes of a row) per stage: one blo
 struct TileArgs {
     E4m3Problem p;
     int tiles_n, tiles_m;
-    int nparts;
+    // The last `tail` tiles run as `parts` parts of K each (part q: stages
+    // [q G / parts, (q + 1) G / parts)) into part[q][tile][BM][BN]; a
+    // reduction adds them in part order.
+    int tail, parts;
     float* part;
 };
 
@@ -47,8 +50,21 @@ __device__ inline void stage_barrier()
     __builtin_amdgcn_sched_barrier(0);
 }
 
-template <bool BF16, int WN, int WM, int NT, int MT>
-__global__ __launch_bounds__(WN* WM * 64, 2) void e4m3_tile_kernel(TileArgs a)
+// (row block, column block) of a tile: bands of 4 row blocks, walked column by
+// column, so that the 32 tiles that an XCD has in flight share 4 blocks of x
+// and 8 of w
+__device__ inline void tile_coords(const TileArgs& a, int tile, int& by, int& bx)
+{
+    const int band = 4 * a.tiles_n, g = tile / band, local = tile - g * band;
+    const int rows = min(4, a.tiles_m - 4 * g);
+    by = 4 * g + local % rows;
+    bx = local / rows;
+}
+
+// WN x WM waves, each NT tiles of 16 weight rows by MT tiles of 16 activation
+// rows; WPS: waves per SIMD that registers and LDS leave room for.
+template <bool BF16, int WN, int WM, int NT, int MT, int WPS>
+__global__ __launch_bounds__(WN* WM * 64, WPS) void e4m3_tile_kernel(TileArgs a)
 {
     constexpr int BN = WN * NT * 16, BM = WM * MT * 16, WAVES = WN * WM;
     constexpr int LOADS = (BN + BM) / 8 / WAVES;     // 1 KB copies per wave and stage
@@ -61,17 +77,24 @@ __global__ __launch_bounds__(WN* WM * 64, 2) void e4m3_tile_kernel(TileArgs a)
     const int wn = wave % WN, wm = wave / WN;
     const E4m3Problem& p = a.p;
 
-    int lin = blockIdx.x;
-    const int per = (int)gridDim.x >> 3;
-    if (lin < per * 8) lin = (lin & 7) * per + (lin >> 3);
-    // bands of 4 row blocks, walked column by column: the 32 tiles that an XCD
-    // has in flight share 4 blocks of x and 8 of w
-    const int band = 4 * a.tiles_n, g4 = lin / band, local = lin - g4 * band;
-    const int brows = min(4, a.tiles_m - 4 * g4);
-    const int by = 4 * g4 + local % brows, bx = local / brows;
+    // full tiles first (XCD b mod 8 walks a contiguous range of them), then
+    // the parts of the others
+    const int full = a.tiles_n * a.tiles_m - a.tail;
+    int lin = blockIdx.x, kpart = 0;
+    const bool split = lin >= full;
+    if (split) {
+        kpart = (lin - full) / a.tail;
+        lin = full + (lin - full) % a.tail;
+    } else {
+        const int per = full >> 3;
+        if (lin < per * 8) lin = (lin & 7) * per + (lin >> 3);
+    }
+    int by, bx;
+    tile_coords(a, lin, by, bx);
     const int m0 = by * BM, n0 = bx * BN;
     const int K = p.K, G = K / KB;
-    const int s0 = 0, stages = G;
+    const int s0 = split ? kpart * G / a.parts : 0;
+    const int stages = split ? (kpart + 1) * G / a.parts - s0 : G;
     const int rows_m = min(BM, p.M - m0), rows_n = min(BN, p.N - n0);
     const __amdgpu_buffer_rsrc_t rSA = buffer_of(p.sa + (int64_t)m0 * G, (uint32_t)rows_m * G * 4);
     const int nblk = n0 / 128, nblks = (rows_n + 127) / 128;
@@ -94,9 +117,9 @@ __global__ __launch_bounds__(WN* WM * 64, 2) void e4m3_tile_kernel(TileArgs a)
         bytes[j] = __builtin_amdgcn_readfirstlane((uint32_t)min(left, WAVES * 8) * K);
     }
     const int voff = (8 * wave + (lane >> 3)) * K + ((lane & 7) ^ (lane >> 3)) * 16;
-    auto copy = [&](uint8_t* dst, int t) {
+    auto copy = [&](uint8_t* dst, int t, int j0, int j1) {
 #pragma unroll
-        for (int j = 0; j < LOADS; ++j)
+        for (int j = j0; j < j1; ++j)
             copy_1k(src[j], bytes[j], dst + (j * WAVES + wave) * 1024, voff, (s0 + t) * KB);
     };
 
@@ -138,7 +161,7 @@ __global__ __launch_bounds__(WN* WM * 64, 2) void e4m3_tile_kernel(TileArgs a)
         const v4i hi = *reinterpret_cast<const v4i*>(b + foff[1]);
         return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
     };
-    auto compute = [&](const uint8_t* b, const float (&S)[MT]) {
+    auto compute = [&](const uint8_t* b, const float (&S)[MT], uint8_t* next, int t_next) {
         v8i x[MT], w[2];
         v4f P[2][MT];
 #pragma unroll
@@ -146,6 +169,9 @@ __global__ __launch_bounds__(WN* WM * 64, 2) void e4m3_tile_kernel(TileArgs a)
         w[0] = frag(b + wbase);
 #pragma unroll
         for (int j = 0; j <= NT; ++j) {
+            // the next stage's copies, two beside each of the first w tiles
+            // (past the last stage: stage 0 again, into a buffer that is not read)
+            if (2 * j < LOADS) copy(next, t_next, 2 * j, min(2 * j + 2, LOADS));
             if (j + 1 < NT) w[(j + 1) & 1] = frag(b + wbase + (j + 1) * 16 * KB);
             // the products of w tile j beside the fold of tile j - 1, kept in
             // this order: left alone, the compiler folds each product at once
@@ -165,30 +191,41 @@ __global__ __launch_bounds__(WN* WM * 64, 2) void e4m3_tile_kernel(TileArgs a)
     };
 
     load_scales(0);
-    copy(buf0, 0);
+    copy(buf0, 0, 0, LOADS);
     for (int t0 = 0; t0 < stages; t0 += 4) {
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
             const int t = t0 + h;
             if (t >= stages) break;
             stage_barrier();
-            if (t + 1 < stages) copy(h & 1 ? buf0 : buf1, t + 1);
             float S[MT];
 #pragma unroll
             for (int i = 0; i < MT; ++i) S[i] = sa[i][h] * sw[h];
             if (h == 3) load_scales(t + 1);
-            compute(h & 1 ? buf1 : buf0, S);
+            compute(h & 1 ? buf1 : buf0, S, h & 1 ? buf0 : buf1, t + 1 < stages ? t + 1 : 0);
         }
+    }
+
+    stage_barrier();      // the copies in flight land before this LDS is used for anything else
+    if (split) {
+        float* out = a.part + ((size_t)kpart * a.tail + lin - full) * (BM * BN);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+                *reinterpret_cast<v4f*>(out + (size_t)(wm * MT * 16 + i * 16 + (lane & 15)) * BN + wn * NT * 16 +
+                                        j * 16 + 4 * (lane >> 4)) = acc[i][j];
+        return;
     }
 
     // --- epilogue: a lane holds 4 neighbouring columns of 16 rows per tile;
     // the wave's MT*16 x NT*16 outputs go through LDS (its own part of the
-    // stage buffers, 8-byte pieces, piece c of row m at c ^ (m & 15)) and leave
+    // stage buffers, 8-byte pieces, piece c of row m at c ^ m modulo the pieces) and leave
     // in 16-byte stores that cover whole rows of the tile.  (Stored from the
     // accumulators, 2 bytes a lane, they took 30 us a tile.) ---
-    __syncthreads();
     constexpr int ROW = NT * 16 * 2;                  // bytes of a row of the wave's tile
-    static_assert(ROW == 256 && MT * 16 * ROW * WAVES <= 2 * STAGE, "the wave's tile in LDS");
+    constexpr int PM = ROW / 8 < 16 ? ROW / 8 - 1 : 15;   // pieces that a row's place is spread over
+    static_assert(MT * 16 * ROW * WAVES <= 2 * STAGE, "the waves' tiles in LDS");
     constexpr int PER_BUF = STAGE / (MT * 16 * ROW);  // waves per stage buffer
     uint8_t* out = (wave < PER_BUF ? buf0 : buf1) + (wave % PER_BUF) * MT * 16 * ROW;
     const int c0 = n0 + wn * NT * 16, r0 = m0 + wm * MT * 16;
@@ -206,45 +243,138 @@ __global__ __launch_bounds__(WN* WM * 64, 2) void e4m3_tile_kernel(TileArgs a)
                 const int n = c0 + j * 16 + 4 * (lane >> 4) + r;
                 if (p.y32 && m < p.M && n < p.N) p.y32[(int64_t)m * p.N + n] = v;
             }
-            *reinterpret_cast<uint2*>(out + lm * ROW + ((4 * j + (lane >> 4)) ^ (lm & 15)) * 8) =
+            *reinterpret_cast<uint2*>(out + lm * ROW + ((4 * j + (lane >> 4)) ^ (lm & PM)) * 8) =
                 make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
         }
     }
     uint16_t* y = static_cast<uint16_t*>(p.y);
     if (p.N % 8 == 0 && (reinterpret_cast<uintptr_t>(y) & 15) == 0) {
 #pragma unroll 4
-        for (int q = 0; q < MT * 16 / 4; ++q) {
-            const int lm = 4 * q + (lane >> 4), c = 2 * (lane & 15);
-            const uint2 u = *reinterpret_cast<const uint2*>(out + lm * ROW + (c ^ (lm & 15)) * 8);
-            const uint2 v = *reinterpret_cast<const uint2*>(out + lm * ROW + ((c + 1) ^ (lm & 15)) * 8);
+        for (int q = 0; q < MT * 16 * ROW / 1024; ++q) {
+            constexpr int LPR = ROW / 16;             // lanes per row
+            const int lm = 64 / LPR * q + lane / LPR, c = 2 * (lane % LPR);
+            const uint2 u = *reinterpret_cast<const uint2*>(out + lm * ROW + (c ^ (lm & PM)) * 8);
+            const uint2 v = *reinterpret_cast<const uint2*>(out + lm * ROW + ((c + 1) ^ (lm & PM)) * 8);
             const int m = r0 + lm, n = c0 + 4 * c;
             if (m < p.M && n < p.N)
                 *reinterpret_cast<uint4*>(y + (int64_t)m * p.N + n) = make_uint4(u.x, u.y, v.x, v.y);
         }
     } else {
-        // rows that start anywhere: 2 bytes a lane, a row's 128 columns in two steps
-        for (int q = 0; q < MT * 16 * 2; ++q) {
-            const int lm = q >> 1, c = 64 * (q & 1) + lane, m = r0 + lm, n = c0 + c;
+        // rows that start anywhere: 2 bytes a lane
+        for (int q = lane; q < MT * 16 * NT * 16; q += 64) {
+            const int lm = q / (NT * 16), c = q % (NT * 16), m = r0 + lm, n = c0 + c;
             if (m < p.M && n < p.N)
                 y[(int64_t)m * p.N + n] =
-                    *reinterpret_cast<const uint16_t*>(out + lm * ROW + ((c >> 2) ^ (lm & 15)) * 8 + (c & 3) * 2);
+                    *reinterpret_cast<const uint16_t*>(out + lm * ROW + ((c >> 2) ^ (lm & PM)) * 8 + (c & 3) * 2);
         }
     }
 }
 
+// y of the tiles that ran in parts of K: the parts' sums in part order.  One
+// thread per 4 columns of a tile row.
+template <bool BF16, int BN, int BM>
+__global__ __launch_bounds__(256) void e4m3_reduce_kernel(TileArgs a)
+{
+    const int64_t idx = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    constexpr int PER = BM * BN / 4;
+    if (idx >= (int64_t)a.tail * PER) return;
+    const int t = (int)(idx / PER), rem = (int)(idx - (int64_t)t * PER);
+    const int row = rem / (BN / 4), col = (rem - row * (BN / 4)) * 4;
+    const E4m3Problem& p = a.p;
+    int by, bx;
+    tile_coords(a, a.tiles_n * a.tiles_m - a.tail + t, by, bx);
+    const int m = by * BM + row, n0 = bx * BN + col;
+    if (m >= p.M || n0 >= p.N) return;
+    const float* src = a.part + (size_t)t * (BM * BN) + row * BN + col;
+    v4f s = *reinterpret_cast<const v4f*>(src);
+    for (int q = 1; q < a.parts; ++q) s += *reinterpret_cast<const v4f*>(src + (size_t)q * a.tail * (BM * BN));
+    uint16_t* y = static_cast<uint16_t*>(p.y) + (int64_t)m * p.N + n0;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        float v = s[r];
+        asm volatile("" : "+v"(v));                   // y is the rounding of y32
+        if (n0 + r < p.N) {
+            y[r] = e4m3::to16<BF16>(v);
+            if (p.y32) p.y32[(int64_t)m * p.N + n0 + r] = v;
+        }
+    }
+}
+
+// The tile shapes, and how a call is cut.
+struct Shape {
+    int bn, bm, per_cu;
+    double stage_us;      // one stage of all the workgroups a CU holds
+};
+constexpr Shape kShapes[3] = {{256, 256, 1, 1.75}, {128, 128, 2, 1.1}, {128, 64, 3, 0.9}};
+
+struct Cut {
+    int shape, tail, parts;
+    size_t bytes;
+};
+
+Cut choose(const E4m3Problem& p, int cus)
+{
+    const int G = p.K / KB;
+    Cut best{0, 0, 1, 0};
+    double best_us = 0.0;
+    for (int c = 0; c < 3; ++c) {
+        const Shape& s = kShapes[c];
+        const int64_t tiles = (int64_t)((p.M + s.bm - 1) / s.bm) * ((p.N + s.bn - 1) / s.bn);
+        const int64_t slots = (int64_t)(cus > 0 ? cus : 256) * s.per_cu;
+        const int64_t tail = tiles % slots;
+        for (int parts = 1; parts <= 8 && parts <= (G + 3) / 4; ++parts) {
+            const int64_t mb = tail * parts * s.bm * s.bn * 4;
+            double us = (double)(tiles / slots) * G * s.stage_us;
+            if (tail) us += (double)((tail * parts + slots - 1) / slots) * ((G + parts - 1) / parts) * s.stage_us + 4.0;
+            if (parts > 1) {
+                if (tail == 0 || cus <= 0) break;
+                us += 5.0 + (double)mb / 2.5e6;
+            }
+            if (best_us == 0.0 || us < best_us) {
+                best_us = us;
+                best = Cut{c, parts > 1 ? (int)tail : 0, parts, parts > 1 ? (size_t)mb : 0};
+            }
+        }
+    }
+    return best;
+}
+
+template <bool BF16, int WN, int WM, int NT, int MT, int WPS>
+hipError_t launch_shape(TileArgs a, hipStream_t stream)
+{
+    constexpr int BN = WN * NT * 16, BM = WM * MT * 16;
+    a.tiles_m = (a.p.M + BM - 1) / BM;
+    a.tiles_n = (a.p.N + BN - 1) / BN;
+    const int64_t grid = (int64_t)a.tiles_m * a.tiles_n + (int64_t)a.tail * (a.parts - 1);
+    e4m3_tile_kernel<BF16, WN, WM, NT, MT, WPS><<<(unsigned)grid, WN * WM * 64, 0, stream>>>(a);
+    if (a.tail) {
+        const int64_t n = (int64_t)a.tail * (BM * BN / 4);
+        e4m3_reduce_kernel<BF16, BN, BM><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(a);
+    }
+    return hipGetLastError();
+}
+
+template <bool BF16>
+hipError_t launch_cut(const TileArgs& a, int shape, hipStream_t stream)
+{
+    if (shape == 0) return launch_shape<BF16, 2, 4, 8, 4, 2>(a, stream);
+    if (shape == 1) return launch_shape<BF16, 2, 2, 4, 4, 2>(a, stream);
+    return launch_shape<BF16, 4, 1, 2, 4, 3>(a, stream);
+}
+
 }  // namespace
+
+size_t e4m3_tiled_workspace_bytes(const E4m3Problem& p) { return choose(p, cu_count()).bytes; }
 
 hipError_t launch_e4m3_tiled(const E4m3Problem& p, hipStream_t stream)
 {
+    const Cut cut = choose(p, cu_count());
     TileArgs a{};
     a.p = p;
-    a.tiles_m = (p.M + 255) / 256;
-    a.tiles_n = (p.N + 255) / 256;
-    a.nparts = 1;
-    const int tiles = a.tiles_m * a.tiles_n;
-    if (p.bf16) e4m3_tile_kernel<true, 2, 4, 8, 4><<<tiles, 512, 0, stream>>>(a);
-    else e4m3_tile_kernel<false, 2, 4, 8, 4><<<tiles, 512, 0, stream>>>(a);
-    return hipGetLastError();
+    a.tail = cut.tail;
+    a.parts = cut.parts;
+    a.part = static_cast<float*>(p.ws);
+    return p.bf16 ? launch_cut<true>(a, cut.shape, stream) : launch_cut<false>(a, cut.shape, stream);
 }
 
 }  // namespace apex4

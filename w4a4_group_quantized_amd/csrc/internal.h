@@ -48,6 +48,9 @@ struct GemmProblem {
     size_t ws_bytes;
 };
 
+// Compute units of the current device (0 where that cannot be asked).
+int cu_count();
+
 // The ping-pong kernel's K split of a partial last round of tiles: the last
 // `tail` tiles (0: no split) run as `nparts` parts of K into an fp32
 // workspace of `bytes`, then a reduction writes their Y.
