@@ -372,27 +372,40 @@ def select_granularity(M: int, N: int, K: int, min_rel_speed: float = 0.75) -> t
 
 # element types of the calls that take one (APEX4_F32, APEX4_F16, APEX4_BF16)
 _TYPE_NAMES = ("float32", "float16", "bfloat16")
+_TYPE_CODES = {}
 _SCORES = {"softmax": 0, "sigmoid": 1}
 
 
-def _type_code(t, name: str, allowed=_TYPE_NAMES) -> int:
-    n = str(t.dtype).replace("torch.", "")
-    if n not in allowed:
-        raise ValueError(f"{name} must be one of {', '.join(allowed)}, got {n}")
-    return _TYPE_NAMES.index(n)
+def _type_code(t, name: str, allowed=(0, 1, 2)) -> int:
+    if not _TYPE_CODES:
+        import torch
+        _TYPE_CODES.update({getattr(torch, n): i for i, n in enumerate(_TYPE_NAMES)})
+    code = _TYPE_CODES.get(t.dtype)
+    if code not in allowed:
+        raise ValueError(f"{name} must be one of {', '.join(_TYPE_NAMES[i] for i in allowed)}, got {t.dtype}")
+    return code
+
+
+def _need(t, name: str, dtype, shape, device) -> None:
+    """_need_gpu with its checks in one line for the calls whose time is their host time."""
+    if not (t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device):
+        _need_gpu(t, name, dtype, shape, device)
 
 
 def _call(fn: str, device, *args) -> None:
     """One library call with `device` current (a launch goes to the current
-    device, the tensors' may be another one), on torch's current stream there."""
+    device, the tensors' may be another one), on torch's current stream there
+    (read as the bare handle: a torch Stream object costs 2 us)."""
     import torch
     f = getattr(lib(), fn)
-    if torch.cuda.current_device() == device.index:
-        status = f(*args, _stream(torch, device))
+    index = device.index
+    if torch.cuda.current_device() == index:
+        status = f(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
-            status = f(*args, _stream(torch, device))
-    _check(fn, status)
+            status = f(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != OK:
+        raise Apex4Error(fn, status)
 
 
 def route(logits, k: int, *, score: str = "softmax", bias=None, n_group: int = 1, topk_group: int = 1,
@@ -412,15 +425,15 @@ def route(logits, k: int, *, score: str = "softmax", bias=None, n_group: int = 1
     code = _type_code(logits, "logits")
     (M, E), dev = logits.shape, logits.device
     if bias is not None:
-        _need_gpu(bias, "bias", torch.float32, (E,), dev)
+        _need(bias, "bias", torch.float32, (E,), dev)
     if out is None:
         n = max(k, 0)
         ids = torch.empty((M, n), dtype=torch.int32, device=dev)
         gates = torch.empty((M, n), dtype=torch.float32, device=dev)
     else:
         ids, gates = out
-        _need_gpu(ids, "ids", torch.int32, (M, k), dev)
-        _need_gpu(gates, "gates", torch.float32, (M, k), dev)
+        _need(ids, "ids", torch.int32, (M, k), dev)
+        _need(gates, "gates", torch.float32, (M, k), dev)
     _call("apex4_route", dev, logits.data_ptr(), code, M, E, _SCORES[score], _ptr(bias), n_group, topk_group,
           group_top, k, int(bool(renormalize)), scale, ids.data_ptr(), gates.data_ptr())
     return ids, gates
@@ -446,17 +459,17 @@ def experts(x, ids, gates, qw_gate_up, s_gate_up, qw_down, s_down, *, group: int
         raise ValueError("experts takes x [M, H], ids [M, k] and weights [E, rows, bytes]")
     (M, H), dev, k = x.shape, x.device, ids.shape[1]
     E, I = qw_gate_up.shape[0], 2 * qw_down.shape[2]
-    _need_gpu(ids, "ids", torch.int32, (M, k), dev)
-    _need_gpu(gates, "gates", torch.float32, (M, k), dev)
-    _need_gpu(qw_gate_up, "qw_gate_up", torch.uint8, (E, 2 * I, H // 2), dev)
-    _need_gpu(s_gate_up, "s_gate_up", torch.float32, (E, 2 * I, _cols(H, group)), dev)
-    _need_gpu(qw_down, "qw_down", torch.uint8, (E, H, I // 2), dev)
-    _need_gpu(s_down, "s_down", torch.float32, (E, H, _cols(I, group)), dev)
+    _need(ids, "ids", torch.int32, (M, k), dev)
+    _need(gates, "gates", torch.float32, (M, k), dev)
+    _need(qw_gate_up, "qw_gate_up", torch.uint8, (E, 2 * I, H // 2), dev)
+    _need(s_gate_up, "s_gate_up", torch.float32, (E, 2 * I, _cols(H, group)), dev)
+    _need(qw_down, "qw_down", torch.uint8, (E, H, I // 2), dev)
+    _need(s_down, "s_down", torch.float32, (E, H, _cols(I, group)), dev)
     # caller buffers are checked before anything is allocated
     if y16 is not None:
-        _need_gpu(y16, "y16", torch.float16, (M, H), dev)
+        _need(y16, "y16", torch.float16, (M, H), dev)
     if y32 is not None:
-        _need_gpu(y32, "y32", torch.float32, (M, H), dev)
+        _need(y32, "y32", torch.float32, (M, H), dev)
     if workspace is not None:
         _need_gpu(workspace, "workspace", torch.uint8, None, dev)
     if y16 is None:
@@ -471,7 +484,7 @@ def experts(x, ids, gates, qw_gate_up, s_gate_up, qw_down, s_down, *, group: int
     return (y16, y32) if want_y32 else y16
 
 
-_HALVES = ("float16", "bfloat16")
+_HALVES = (1, 2)
 
 
 def quantize_e4m3(x, out=None):
@@ -513,15 +526,15 @@ def gemm_e4m3(qa8, sa, qw8, sw, dtype=None, *, want_y32: bool = False, y=None, y
     dtype = torch.float16 if dtype is None else dtype
     M, K = qa8.shape
     N, dev = qw8.shape[0], qa8.device
-    _need_gpu(qa8, "qa8", torch.uint8, (M, K), dev)
-    _need_gpu(qw8, "qw8", torch.uint8, (N, K), dev)
-    _need_gpu(sa, "s_a", torch.float32, (M, K // 128), dev)
-    _need_gpu(sw, "s_w", torch.float32, ((N + 127) // 128, K // 128), dev)
+    _need(qa8, "qa8", torch.uint8, (M, K), dev)
+    _need(qw8, "qw8", torch.uint8, (N, K), dev)
+    _need(sa, "s_a", torch.float32, (M, K // 128), dev)
+    _need(sw, "s_w", torch.float32, ((N + 127) // 128, K // 128), dev)
     # caller buffers are checked before anything is allocated
     if y is not None:
-        _need_gpu(y, "y", dtype, (M, N), dev)
+        _need(y, "y", dtype, (M, N), dev)
     if y32 is not None:
-        _need_gpu(y32, "y32", torch.float32, (M, N), dev)
+        _need(y32, "y32", torch.float32, (M, N), dev)
     if workspace is not None:
         _need_gpu(workspace, "workspace", torch.uint8, None, dev)
     if y is None:
@@ -550,13 +563,13 @@ def linear_e4m3(x, qw8, sw, *, want_y32: bool = False, y=None, y32=None, workspa
     _need_gpu(x, "x")
     code = _type_code(x, "x", _HALVES)
     (M, K), N, dev = x.shape, qw8.shape[0], x.device
-    _need_gpu(qw8, "qw8", torch.uint8, (N, K), dev)
-    _need_gpu(sw, "s_w", torch.float32, ((N + 127) // 128, K // 128), dev)
+    _need(qw8, "qw8", torch.uint8, (N, K), dev)
+    _need(sw, "s_w", torch.float32, ((N + 127) // 128, K // 128), dev)
     # caller buffers are checked before anything is allocated
     if y is not None:
-        _need_gpu(y, "y", x.dtype, (M, N), dev)
+        _need(y, "y", x.dtype, (M, N), dev)
     if y32 is not None:
-        _need_gpu(y32, "y32", torch.float32, (M, N), dev)
+        _need(y32, "y32", torch.float32, (M, N), dev)
     if workspace is not None:
         _need_gpu(workspace, "workspace", torch.uint8, None, dev)
     if y is None:

@@ -300,12 +300,24 @@ __global__ __launch_bounds__(256) void e4m3_reduce_kernel(TileArgs a)
     }
 }
 
-// The tile shapes, and how a call is cut.
+// The tile shapes, and how a call is cut: the shape and the number of K parts
+// of the last tiles with the least modelled time.  The model's numbers are
+// measured on 256 compute units: a stage (128 of K) of a CU that holds all the
+// workgroups it can, and of one that holds a single one, which waits for its
+// copies; 5.9 TB/s for the operands, 12 TB/s for weights read again by another
+// row of tiles; the shorter of the two times hides to two thirds under the
+// longer; 4 TB/s for writing the partial sums and reading them again, and 1 us
+// for that launch.  E.g. 64 x 28672 x 8192: 128 x 64 tiles (weight rows x rows)
+// in two parts 46 us, in one 53, 256 x 256 163; 16 x 28672 x 8192: 128 x 32 in
+// two parts 39, 128 x 64 in one 49; 4096 x 8192 x 8192: 256 x 256 260, 128 x 128
+// 321, 128 x 64 419.
 struct Shape {
-    int bn, bm, per_cu;
-    double stage_us;      // one stage of all the workgroups a CU holds
+    int bn, bm, per_cu;          // weight rows, activation rows, workgroups that fit a CU
+    double loaded_us, alone_us;  // one stage
 };
-constexpr Shape kShapes[3] = {{256, 256, 1, 1.75}, {128, 128, 2, 1.1}, {128, 64, 3, 0.9}};
+constexpr int SHAPES = 4;
+constexpr Shape kShapes[SHAPES] = {
+    {256, 256, 1, 2.0, 1.6}, {128, 128, 2, 1.25, 0.78}, {128, 64, 3, 1.09, 0.6}, {128, 32, 4, 1.1, 0.5}};
 
 struct Cut {
     int shape, tail, parts;
@@ -315,24 +327,32 @@ struct Cut {
 Cut choose(const E4m3Problem& p, int cus)
 {
     const int G = p.K / KB;
+    const bool can_split = cus > 0;
+    if (!can_split) cus = 256;
     Cut best{0, 0, 1, 0};
     double best_us = 0.0;
-    for (int c = 0; c < 3; ++c) {
+    for (int c = 0; c < SHAPES; ++c) {
         const Shape& s = kShapes[c];
         const int64_t tiles = (int64_t)((p.M + s.bm - 1) / s.bm) * ((p.N + s.bn - 1) / s.bn);
-        const int64_t slots = (int64_t)(cus > 0 ? cus : 256) * s.per_cu;
+        const int64_t slots = (int64_t)cus * s.per_cu;
         const int64_t tail = tiles % slots;
         for (int parts = 1; parts <= 8 && parts <= (G + 3) / 4; ++parts) {
-            const int64_t mb = tail * parts * s.bm * s.bn * 4;
-            double us = (double)(tiles / slots) * G * s.stage_us;
-            if (tail) us += (double)((tail * parts + slots - 1) / slots) * ((G + parts - 1) / parts) * s.stage_us + 4.0;
-            if (parts > 1) {
-                if (tail == 0 || cus <= 0) break;
-                us += 5.0 + (double)mb / 2.5e6;
+            if (parts > 1 && (tail == 0 || !can_split)) break;
+            const int64_t per = (tail * parts + cus - 1) / cus, rest = per % s.per_cu;   // last workgroups per CU
+            double last = (double)(per / s.per_cu) * s.loaded_us;
+            if (rest) {
+                const double share = s.loaded_us * (double)rest / s.per_cu;
+                last += share > s.alone_us ? share : s.alone_us;
             }
+            double us = (double)(tiles / slots) * G * s.loaded_us + last * ((G + parts - 1) / parts);
+            const double w = (double)p.N * p.K, rows = (p.M + s.bm - 1) / s.bm;
+            const double read = (w + (double)p.M * p.K + 2.0 * p.M * p.N) / 5.9e6 + (rows - 1) * w / 12e6;
+            us = us > read ? us + 0.35 * read : read + 0.35 * us;
+            const int64_t mem = parts > 1 ? tail * parts * s.bm * s.bn * 4 : 0;
+            if (mem) us += 1.0 + (double)mem / 4e6;
             if (best_us == 0.0 || us < best_us) {
                 best_us = us;
-                best = Cut{c, parts > 1 ? (int)tail : 0, parts, parts > 1 ? (size_t)mb : 0};
+                best = Cut{c, parts > 1 ? (int)tail : 0, parts, (size_t)mem};
             }
         }
     }
@@ -359,7 +379,8 @@ hipError_t launch_cut(const TileArgs& a, int shape, hipStream_t stream)
 {
     if (shape == 0) return launch_shape<BF16, 2, 4, 8, 4, 2>(a, stream);
     if (shape == 1) return launch_shape<BF16, 2, 2, 4, 4, 2>(a, stream);
-    return launch_shape<BF16, 4, 1, 2, 4, 3>(a, stream);
+    if (shape == 2) return launch_shape<BF16, 4, 1, 2, 4, 3>(a, stream);
+    return launch_shape<BF16, 4, 1, 2, 2, 4>(a, stream);
 }
 
 }  // namespace
