@@ -6,6 +6,7 @@
 // Slots are put in the order of their experts once (plan_kernel: the sorted
 // row of every slot and the first row of every expert), the activation codes
 // are quantized per token, and the products run per expert over its rows.
+#include "experts.h"
 #include "internal.h"
 #include "rows_stream.h"
 
@@ -110,18 +111,6 @@ __global__ __launch_bounds__(64 * PLAN_WAVES) void plan_kernel(const int32_t* __
     }
 }
 
-struct ProductArgs {
-    const int32_t* offsets;
-    const int32_t* order;
-    const uint8_t* qx;
-    const float* sx;
-    const uint8_t* qw;     // [E, N, K/2]
-    const float* sw;       // [E, N, K/128]
-    int32_t k, E, N, K;
-    _Float16* h;           // UP: [R, N/2]
-    float* d;              // else [R, N]
-};
-
 // The expert of launch row y: every expert in turn where there is one launch
 // row per expert, else the y-th expert that has rows (-1: there are fewer).
 __device__ inline int expert_of(const int32_t* __restrict__ offsets, int E, int y, int launched)
@@ -146,7 +135,7 @@ __device__ inline int expert_of(const int32_t* __restrict__ offsets, int E, int 
 // rows (UP: 8 gate rows and the 8 up rows of the same columns of h, so that
 // the product silu(g) u is formed here).
 template <bool UP>
-__global__ __launch_bounds__(rows::THREADS) void experts_rows_kernel(ProductArgs a)
+__global__ __launch_bounds__(rows::THREADS) void experts_rows_kernel(ExpertsProduct a)
 {
     using namespace rows;
     __shared__ Shared<false> sh;
@@ -185,9 +174,7 @@ __global__ __launch_bounds__(rows::THREADS) void experts_rows_kernel(ProductArgs
                     // weight row c (and 8 + c) of activation row m: lane 16 (row >> 2) + m, element row & 3
                     const float g = sh.red[0][t][(16 * (c >> 2) + m) * 4 + (c & 3)];
                     const float u = sh.red[0][t][(16 * (2 + (c >> 2)) + m) * 4 + (c & 3)];
-                    float v = g / (1.0f + expf(-g)) * u;
-                    v = fminf(fmaxf(v, -65504.0f), 65504.0f);
-                    a.h[(int64_t)(first + m0 + 16 * t + m) * half + n0 + c] = (_Float16)v;
+                    a.h[(int64_t)(first + m0 + 16 * t + m) * half + n0 + c] = experts_h(g, u);
                 }
             }
         } else {
@@ -252,7 +239,7 @@ hipError_t launch_experts(const ExpertsProblem& p, hipStream_t stream)
     hipError_t e = launch_quantize(p.x, p.M, p.H, 128, w.xq, w.xs, stream);
     if (e != hipSuccess) return e;
     const int launched = R < p.E ? R : p.E;
-    ProductArgs a{};
+    ExpertsProduct a{};
     a.offsets = w.offsets;
     a.order = w.order;
     a.k = p.k;
@@ -264,7 +251,10 @@ hipError_t launch_experts(const ExpertsProblem& p, hipStream_t stream)
     a.N = 2 * p.I;
     a.K = p.H;
     a.h = w.h;
-    experts_rows_kernel<true><<<dim3(p.I / 8, launched), rows::THREADS, 0, stream>>>(a);
+    a.rows = p.M;
+    const bool few = R <= 2 * launched;
+    if (few) experts_rows_kernel<true><<<dim3(p.I / 8, launched), rows::THREADS, 0, stream>>>(a);
+    else launch_experts_tiled(a, true, R, stream);
     e = launch_quantize(w.h, R, p.I, 128, w.hq, w.hs, stream);
     if (e != hipSuccess) return e;
     a.qx = w.hq;
@@ -274,7 +264,8 @@ hipError_t launch_experts(const ExpertsProblem& p, hipStream_t stream)
     a.N = p.H;
     a.K = p.I;
     a.d = w.d;
-    experts_rows_kernel<false><<<dim3(p.H / 16, launched), rows::THREADS, 0, stream>>>(a);
+    if (few) experts_rows_kernel<false><<<dim3(p.H / 16, launched), rows::THREADS, 0, stream>>>(a);
+    else launch_experts_tiled(a, false, R, stream);
     const int64_t n4 = p.M * (p.H / 4);
     combine_kernel<<<(unsigned)((n4 + 255) / 256), 256, 0, stream>>>(w.d, w.place, p.gates, p.k, p.H, n4,
                                                                      static_cast<_Float16*>(p.y16), p.y32);
