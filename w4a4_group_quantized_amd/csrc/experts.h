@@ -4,6 +4,8 @@
 
 #include <cstdint>
 
+#include "internal.h"
+
 namespace apex4 {
 
 // One of the network's two products, over the rows sorted by expert.
@@ -26,6 +28,10 @@ __device__ inline _Float16 experts_h(float g, float u)
     const float v = g / (1.0f + expf(-g)) * u;
     return (_Float16)fminf(fmaxf(v, -65504.0f), 65504.0f);
 }
+
+// A few tokens (experts_token.hip): the whole network in two launches; h: [R, I].
+bool experts_token_supports(const ExpertsProblem& p);
+hipError_t launch_experts_token(const ExpertsProblem& p, _Float16* h, hipStream_t stream);
 
 void launch_experts_tiled(const ExpertsProduct& a, bool up, int64_t R, hipStream_t stream);
 

@@ -8,7 +8,6 @@
 // are quantized per token, and the products run per expert over its rows.
 #include "experts.h"
 #include "internal.h"
-#include "rows_stream.h"
 
 namespace apex4 {
 namespace {
@@ -111,89 +110,6 @@ __global__ __launch_bounds__(64 * PLAN_WAVES) void plan_kernel(const int32_t* __
     }
 }
 
-// The expert of launch row y: every expert in turn where there is one launch
-// row per expert, else the y-th expert that has rows (-1: there are fewer).
-__device__ inline int expert_of(const int32_t* __restrict__ offsets, int E, int y, int launched)
-{
-    if (launched == E) return y;
-    const int lane = threadIdx.x & 63;
-    for (int e0 = 0; e0 < E; e0 += 64) {
-        const int e = e0 + lane;
-        const bool some = e < E && offsets[e + 1] > offsets[e];
-        uint64_t who = __ballot(some);
-        const int n = __popcll(who);
-        if (y < n) {
-            for (; y > 0; --y) who &= who - 1;
-            return e0 + __ffsll((unsigned long long)who) - 1;
-        }
-        y -= n;
-    }
-    return -1;
-}
-
-// Few rows per expert: blockIdx.y is an expert, blockIdx.x 16 of its weight
-// rows (UP: 8 gate rows and the 8 up rows of the same columns of h, so that
-// the product silu(g) u is formed here).
-template <bool UP>
-__global__ __launch_bounds__(rows::THREADS) void experts_rows_kernel(ExpertsProduct a)
-{
-    using namespace rows;
-    __shared__ Shared<false> sh;
-    const int e = __builtin_amdgcn_readfirstlane(expert_of(a.offsets, a.E, blockIdx.y, gridDim.y));
-    if (e < 0) return;
-    const int first = a.offsets[e], count = a.offsets[e + 1] - first;
-    const int n0 = blockIdx.x * (UP ? 8 : 16), half = a.N / 2;
-    const int64_t rowbytes = a.K / 2, G = a.K / 128;
-    const uint8_t* qw = a.qw + (int64_t)e * a.N * rowbytes;
-    const float* sw = a.sw + (int64_t)e * a.N * G;
-    auto row_of = [&](int r) -> int64_t { return UP ? (r < 8 ? n0 + r : half + n0 + r - 8) : n0 + r; };
-    auto wrow = [&](int r) { return qw + row_of(r) * rowbytes; };
-    auto swrow = [&](int r) { return sw + row_of(r) * G; };
-    const int lane = threadIdx.x & 63;
-
-    auto pass = [&](auto tc, int m0) {
-        constexpr int TILES = decltype(tc)::value;
-        const uint8_t* xrow[TILES];
-        const float* sarow[TILES];
-#pragma unroll
-        for (int i = 0; i < TILES; ++i) {
-            const int m = m0 + 16 * i + (lane & 15);
-            xrow[i] = nullptr;
-            sarow[i] = nullptr;
-            if (m < count) {
-                const int64_t r = UP ? a.order[first + m] / a.k : first + m;
-                xrow[i] = a.qx + r * rowbytes;
-                sarow[i] = a.sx + r * G;
-            }
-        }
-        stream<false, TILES>(sh, a.K, wrow, swrow, xrow, sarow);
-        if (UP) {
-            for (int j = threadIdx.x; j < TILES * 128; j += THREADS) {
-                const int t = j >> 7, m = (j >> 3) & 15, c = j & 7;
-                if (m0 + 16 * t + m < count) {
-                    // weight row c (and 8 + c) of activation row m: lane 16 (row >> 2) + m, element row & 3
-                    const float g = sh.red[0][t][(16 * (c >> 2) + m) * 4 + (c & 3)];
-                    const float u = sh.red[0][t][(16 * (2 + (c >> 2)) + m) * 4 + (c & 3)];
-                    a.h[(int64_t)(first + m0 + 16 * t + m) * half + n0 + c] = experts_h(g, u);
-                }
-            }
-        } else {
-            for (int j = threadIdx.x; j < TILES * 256; j += THREADS) {
-                const int t = j >> 8, m = (j >> 4) & 15, c = j & 15;
-                if (m0 + 16 * t + m < count)
-                    a.d[(int64_t)(first + m0 + 16 * t + m) * a.N + n0 + c] =
-                        sh.red[0][t][(16 * (c >> 2) + m) * 4 + (c & 3)];
-            }
-        }
-        __syncthreads();   // sh.red is written again
-    };
-    for (int m0 = 0; m0 < count; m0 += 64) {
-        if (count - m0 <= 16) pass(std::integral_constant<int, 1>{}, m0);
-        else if (count - m0 <= 32) pass(std::integral_constant<int, 2>{}, m0);
-        else pass(std::integral_constant<int, 4>{}, m0);
-    }
-}
-
 // y = the sum of a token's slots, in slot order, one rounding to fp16 at the end.
 __global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ d, const int32_t* __restrict__ place,
                                                       const float* __restrict__ gates, int32_t k, int32_t H,
@@ -235,10 +151,10 @@ hipError_t launch_experts(const ExpertsProblem& p, hipStream_t stream)
 {
     const Parts w = parts_of(p.ws, p.M, p.k, p.E, p.H, p.I);
     const int32_t R = (int32_t)(p.M * p.k);
+    if (experts_token_supports(p)) return launch_experts_token(p, w.h, stream);
     plan_kernel<<<p.E, 64 * PLAN_WAVES, 0, stream>>>(p.ids, R, p.E, w.offsets, w.order, w.place);
     hipError_t e = launch_quantize(p.x, p.M, p.H, 128, w.xq, w.xs, stream);
     if (e != hipSuccess) return e;
-    const int launched = R < p.E ? R : p.E;
     ExpertsProduct a{};
     a.offsets = w.offsets;
     a.order = w.order;
@@ -252,9 +168,7 @@ hipError_t launch_experts(const ExpertsProblem& p, hipStream_t stream)
     a.K = p.H;
     a.h = w.h;
     a.rows = p.M;
-    const bool few = R <= 2 * launched;
-    if (few) experts_rows_kernel<true><<<dim3(p.I / 8, launched), rows::THREADS, 0, stream>>>(a);
-    else launch_experts_tiled(a, true, R, stream);
+    launch_experts_tiled(a, true, R, stream);
     e = launch_quantize(w.h, R, p.I, 128, w.hq, w.hs, stream);
     if (e != hipSuccess) return e;
     a.qx = w.hq;
@@ -264,8 +178,7 @@ hipError_t launch_experts(const ExpertsProblem& p, hipStream_t stream)
     a.N = p.H;
     a.K = p.I;
     a.d = w.d;
-    if (few) experts_rows_kernel<false><<<dim3(p.H / 16, launched), rows::THREADS, 0, stream>>>(a);
-    else launch_experts_tiled(a, false, R, stream);
+    launch_experts_tiled(a, false, R, stream);
     const int64_t n4 = p.M * (p.H / 4);
     combine_kernel<<<(unsigned)((n4 + 255) / 256), 256, 0, stream>>>(w.d, w.place, p.gates, p.k, p.H, n4,
                                                                      static_cast<_Float16*>(p.y16), p.y32);

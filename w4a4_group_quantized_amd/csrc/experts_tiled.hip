@@ -319,7 +319,7 @@ void launch_experts_tiled(const ExpertsProduct& a, bool up, int64_t R, hipStream
 #ifdef EXPERTS_SHAPE
     const int shape = EXPERTS_SHAPE;
 #else
-    const int shape = mean <= 24 ? 3 : mean <= 80 ? 2 : mean <= 160 ? 1 : 0;
+    const int shape = mean <= 12 ? 3 : 2;
 #endif
     if (shape == 0) launch_shape<2, 4, 8, 4, 2>(a, up, R, stream);
     else if (shape == 1) launch_shape<2, 2, 4, 4, 2>(a, up, R, stream);

@@ -1,0 +1,415 @@
+// The experts' W4A4 network for a few tokens (decoding) on gfx950, in two
+// launches: gate and up of every chosen expert, then all the down products of
+// a column block with the weighted sum over the experts.
+//
+// Such a call is the stream of the chosen experts' weights and the chain of
+// small steps around it.  The six launches of the general path (order of the
+// slots, codes of x, product, codes of h, product, sum) took 50 us for one
+// token and 8 of 64 experts (4096 x 1408; 74 MB of weights, 14 us at the rate
+// of a large copy), of which the two products were 36.  Here
+//   - no plan: a wave looks at the at most 64 ids itself.  An entry is an
+//     expert with the tokens that name it, one slot a token (a token that names
+//     it again gives another entry); the matrix instruction's 16 activation
+//     rows are the tokens;
+//   - every workgroup quantizes the activations it needs (x, or h of all
+//     slots) into LDS while its weights are on their way: a few dozen values
+//     a thread, from L2;
+//   - weights come by direct-to-LDS copies into a buffer of each wave's own,
+//     16 rows by 512 bytes (1024 codes) at a time, so that no barrier stands
+//     between a wave and its stream;
+//   - the down launch walks all entries for its 16 columns and adds them in
+//     one accumulator, with the gate in the activation's scale; the waves'
+//     sums are added in wave order.
+// LDS: piece c (16 bytes) of a row sits at c ^ row, so that the 16 rows' reads
+// of one column touch every bank once.
+#include "experts.h"
+#include "internal.h"
+#include "quant_rule.h"
+
+namespace apex4 {
+namespace {
+
+using qrule::half8;
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void lds_void;
+
+constexpr int TOKENS = 16;           // tokens of a call at most
+constexpr int SLOTS = 64;            // and slots
+constexpr int ITEM = 512;            // bytes of a row per item
+constexpr int PIECE = 16 * ITEM;     // bytes of an item
+constexpr int GPI = ITEM / 64;       // groups per item
+constexpr int UP_WAVES = 4, DOWN_WAVES = 8;
+constexpr int BUFS = 2;              // items in flight per wave
+constexpr int OOB = (int)0x80000000; // past every buffer: reads zeros
+constexpr int PAD = 16;              // bytes between activation rows: their reads fall on different banks
+
+struct Entries {
+    signed char slot[SLOTS][TOKENS];  // of an entry's token, -1 for none
+    signed char entry[SLOTS];         // of a slot, -1 for none
+};
+
+// The entries, found by every wave for itself (lane s is slot s), so that it
+// can ask for its weights before any barrier.
+struct Found {
+    int id;               // of this lane's slot, below 0 for a dead one
+    int entry;            // of this lane's slot
+    uint64_t leads;       // the first slots of the entries
+    int n;
+    __device__ int expert(int y) const
+    {
+        uint64_t l = leads;
+        for (; y > 0; --y) l &= l - 1;
+        return __builtin_amdgcn_readlane(id, __builtin_ctzll(l));
+    }
+};
+
+__device__ inline Found find_entries(const int32_t* __restrict__ ids, int R, int k, int E)
+{
+    const int lane = threadIdx.x & 63;
+    Found f;
+    f.id = lane < R ? ids[lane] : -1;
+    const bool live = f.id >= 0 && f.id < E;
+    if (!live) f.id = -1 - lane;      // like no other
+    int rank = 0;                     // this token's earlier slots of the same expert
+    int lead = lane;                  // the first slot of the entry
+    if (R > 1) {
+        // slots of one token, back from this one
+        const int at = lane % k;
+        for (int d = 1; d < k; ++d) rank += __shfl(f.id, lane - d) == f.id && d <= at;
+        if (R > k)
+            for (int s = R - 1; s >= 0; --s)
+                if (__builtin_amdgcn_readlane(f.id, s) == f.id && __builtin_amdgcn_readlane(rank, s) == rank) lead = s;
+    }
+    f.leads = __ballot(live && lead == lane);
+    f.entry = live ? __popcll(f.leads & ((1ull << lead) - 1)) : -1;
+    f.n = __popcll(f.leads);
+    return f;
+}
+
+// the tables that the products look into (one wave)
+__device__ inline void write_entries(Entries& t, const Found& f, int k)
+{
+    const int lane = threadIdx.x & 63;
+    *reinterpret_cast<int4*>(t.slot[lane]) = make_int4(-1, -1, -1, -1);
+    t.entry[lane] = (signed char)f.entry;
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (f.entry >= 0) t.slot[f.entry][lane / k] = (signed char)lane;
+}
+
+__device__ inline v4i widen_lo(v4i w)
+{
+    return v4i{(int)(((uint32_t)w[0] << 4) & 0xF0F0F0F0u), (int)((uint32_t)w[0] & 0xF0F0F0F0u),
+               (int)(((uint32_t)w[1] << 4) & 0xF0F0F0F0u), (int)((uint32_t)w[1] & 0xF0F0F0F0u)};
+}
+__device__ inline v4i widen_hi(v4i w)
+{
+    return v4i{(int)(((uint32_t)w[2] << 4) & 0xF0F0F0F0u), (int)((uint32_t)w[2] & 0xF0F0F0F0u),
+               (int)(((uint32_t)w[3] << 4) & 0xF0F0F0F0u), (int)((uint32_t)w[3] & 0xF0F0F0F0u)};
+}
+
+// Item `it` (bytes it ITEM .. of 16 weight rows) into a wave's buffer: copy j
+// brings rows 2 j and 2 j + 1.  `rows`: the first row of each run of 8 rows
+// (gate and up rows lie apart).
+__device__ inline void copy_item(uint8_t* dst, const uint8_t* rows0, const uint8_t* rows8, int rowbytes, int it)
+{
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int r = 2 * j + (lane >> 5);
+        const int pos = it * ITEM + (((lane & 31) ^ r) * 16);
+        const uint8_t* base = j < 4 ? rows0 : rows8;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), (short)0, 8 * rowbytes, 0x00020000),
+            (lds_void*)(dst + j * 1024), 16, pos < rowbytes ? (r & 7) * rowbytes + pos : OOB, 0, 0, 0);
+    }
+}
+
+// This lane's 8 scales of an item (weight row lane & 15).  Always 8 loads, so
+// that the wait counts are exact; past the row the last one again, which meets
+// codes that are zeros.
+__device__ inline void load_scales(float (&s)[GPI], const float* row, int G, int it)
+{
+#pragma unroll
+    for (int q = 0; q < GPI; ++q) s[q] = row[min(it * GPI + q, G - 1)];
+}
+
+// Workgroup barrier for what was stored to LDS; copies in flight stay in flight.
+__device__ inline void lds_barrier()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// A thread's values to quantize, asked for before anything else: chunks of 8
+// at tid, tid + threads, ..
+template <int NX>
+__device__ inline void load_chunks(half8 (&v)[NX], const half8* x, int n8, int threads)
+{
+#pragma unroll
+    for (int c = 0; c < NX; ++c) v[c] = x[min((int)threadIdx.x + c * threads, n8 - 1)];
+}
+
+// acc[r] += sum over the item's groups of sa4(q)[r] s_w[q] P, P of activation row 4 (lane >> 4) + r and weight row
+// lane & 15.  `x`: the codes of this lane's activation row lane & 15 at the item's first byte; `left`: bytes of the
+// row from there (reads stop at the row's end: the weights' codes past it are zeros).
+template <typename Scale>
+__device__ inline void item_products(v4f& acc, const uint8_t* buf, const uint8_t* x, int left, const float (&sw)[GPI],
+                                     Scale sa4)
+{
+    const int lane = threadIdx.x & 63, row = lane & 15, kg = lane >> 4;
+#pragma unroll
+    for (int q = 0; q < GPI; ++q) {
+        if (64 * q >= left) break;
+        const v4i w = *reinterpret_cast<const v4i*>(buf + row * ITEM + ((4 * q + kg) ^ row) * 16);
+        const v4i a = *reinterpret_cast<const v4i*>(x + 64 * q + 16 * kg);
+        v4i P = __builtin_amdgcn_mfma_i32_16x16x64_i8(widen_lo(a), widen_lo(w), v4i{}, 0, 0, 0);
+        P = __builtin_amdgcn_mfma_i32_16x16x64_i8(widen_hi(a), widen_hi(w), P, 0, 0, 0);
+        const v4f s = sa4(q);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[r] = fmaf(s[r] * sw[q], (float)P[r], acc[r]);
+    }
+}
+
+// This item's copies and scales have landed: all but the operations of the
+// next item, where one is in flight (8 copies and GPI scales).
+__device__ inline void wait_copies(bool next)
+{
+    asm volatile("" ::: "memory");
+    if (next) __builtin_amdgcn_s_waitcnt(((8 + GPI) & 15) | (((8 + GPI) >> 4) << 14) | 0xF70);
+    else __builtin_amdgcn_s_waitcnt(0xF70);
+    asm volatile("" ::: "memory");
+}
+
+struct TokenArgs {
+    ExpertsProblem p;
+    int G;                // groups of the launch's K
+    int M4;               // tokens, in fours
+};
+
+// LDS of the gate-and-up launch beside the waves' buffers: the codes of x
+// (rows of H/2 + PAD bytes), their scales as [G][16].
+__host__ __device__ inline int up_lds(const TokenArgs& a)
+{
+    return (int)a.p.M * (a.p.H / 2 + PAD) + a.G * 64;
+}
+
+// A wave walks all of K for 8 gate rows and the 8 up rows of the same columns
+// of h: no sum crosses waves, and the codes of x are made once for 4 of them.
+template <int NX>
+__global__ __launch_bounds__(UP_WAVES * 64) void token_up_kernel(TokenArgs a, _Float16* __restrict__ h)
+{
+    // (buffers of their own: the compiler then keeps the stores of the codes
+    // apart from the copies in flight)
+    __shared__ __attribute__((aligned(1024))) uint8_t bufs[UP_WAVES * BUFS * PIECE];
+    extern __shared__ __attribute__((aligned(16))) uint8_t xq[];
+    __shared__ Entries t;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int M = (int)a.p.M, k = a.p.k, H = a.p.H, I = a.p.I, G = a.G, R = M * k;
+    uint8_t* buf = bufs + wave * BUFS * PIECE;
+    const int stride = H / 2 + PAD;
+    float* xs = reinterpret_cast<float*>(xq + M * stride);
+
+    const int n8 = M * (H / 8);
+    half8 v[NX];
+    load_chunks(v, static_cast<const half8*>(a.p.x), n8, UP_WAVES * 64);
+    const Found f = find_entries(a.p.ids, R, k, a.p.E);
+    const int blocks = I / 8, block = blockIdx.x * UP_WAVES + wave, y = block / blocks;
+    if (blockIdx.x * UP_WAVES >= f.n * blocks) return;
+    const bool live = y < f.n;
+    const int e = live ? f.expert(y) : 0, n0 = (block - y * blocks) * 8;
+    const int rowbytes = H / 2, items = live ? (rowbytes + ITEM - 1) / ITEM : 0;
+    const uint8_t* gate = a.p.qw_gu + ((int64_t)e * 2 * I + n0) * rowbytes;
+    const uint8_t* up = gate + (int64_t)I * rowbytes;
+    const int wr = lane & 15;
+    const float* srow = a.p.s_gu + ((int64_t)e * 2 * I + n0 + (wr < 8 ? wr : I + wr - 8)) * G;
+    float sw[BUFS][GPI];
+    auto fetch = [&](int b, int it) {
+        copy_item(buf + b * PIECE, gate, up, rowbytes, it);
+        load_scales(sw[b], srow, G, it);
+    };
+#pragma unroll
+    for (int b = 0; b < BUFS; ++b)
+        if (b < items) fetch(b, b);
+
+    // the codes of x beside them
+#pragma unroll
+    for (int j = 0; j < NX; ++j) {
+        const int i = tid + j * UP_WAVES * 64;
+        if (i >= n8) break;
+        const float amax = qrule::group_max<16>(qrule::absmax8(v[j]));
+        const float scale = amax / 7.0f;
+        const int m = i / (H / 8), c = i - m * (H / 8);
+        *reinterpret_cast<uint32_t*>(xq + m * stride + 4 * c) = qrule::quantize8(v[j], scale, amax != 0.0f);
+        if ((c & 15) == 0) xs[(c >> 4) * 16 + m] = amax != 0.0f ? scale : 0.0f;
+    }
+    for (int i = tid; i < G * 16; i += UP_WAVES * 64)
+        if ((i & 15) >= M) xs[i] = 0.0f;
+    if (wave == 0) write_entries(t, f, k);
+    lds_barrier();
+
+    v4f acc = {};
+    const uint8_t* xrow = xq + (wr < M ? wr : 0) * stride;
+    for (int i0 = 0; i0 < items; i0 += BUFS) {
+#pragma unroll
+        for (int b = 0; b < BUFS; ++b) {
+            const int it = i0 + b;
+            if (it >= items) break;
+            wait_copies(it + 1 < items);
+            item_products(acc, buf + b * PIECE, xrow + it * ITEM, rowbytes - it * ITEM, sw[b], [&](int q) {
+                return *reinterpret_cast<const v4f*>(xs + (it * GPI + q) * 16 + 4 * (lane >> 4));
+            });
+            asm volatile("" ::: "memory");
+            if (it + BUFS < items) fetch(b, it + BUFS);
+        }
+    }
+    if (!live) return;
+    // lane 16 (m >> 2) + n, register m & 3: activation row m and weight row n (gate rows 0..7, up rows 8..15)
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const float u = __shfl(acc[r], lane + 8);
+        const int m = 4 * (lane >> 4) + r;
+        const int s = m < M && wr < 8 ? t.slot[y][m] : -1;
+        if (s >= 0) h[(int64_t)s * I + n0 + wr] = experts_h(acc[r] * 0.00390625f, u * 0.00390625f);
+    }
+}
+
+// LDS of the down launch beside the waves' buffers: the codes of h (rows of
+// I/2 + PAD bytes by slot), the scales times the gates as [entry][G][M4].
+__host__ __device__ inline int down_lds(const TokenArgs& a)
+{
+    const int R = (int)a.p.M * a.p.k;
+    return R * (a.p.I / 2 + PAD) + R * a.G * a.M4 * 4;
+}
+
+template <int NX>
+__global__ __launch_bounds__(DOWN_WAVES * 64) void token_down_kernel(TokenArgs a, const _Float16* __restrict__ h)
+{
+    __shared__ __attribute__((aligned(1024))) uint8_t bufs[DOWN_WAVES * BUFS * PIECE];
+    extern __shared__ __attribute__((aligned(16))) uint8_t hq[];
+    __shared__ Entries t;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int M = (int)a.p.M, k = a.p.k, H = a.p.H, I = a.p.I, G = a.G, R = M * k, M4 = a.M4;
+    uint8_t* buf = bufs + wave * BUFS * PIECE;
+    const int stride = I / 2 + PAD;
+    float* tab = reinterpret_cast<float*>(hq + R * stride);
+
+    const int n8 = R * (I / 8);
+    half8 v[NX];
+    load_chunks(v, reinterpret_cast<const half8*>(h), n8, DOWN_WAVES * 64);
+    const Found f = find_entries(a.p.ids, R, k, a.p.E);
+    const int n0 = blockIdx.x * 16, rowbytes = I / 2, per = (rowbytes + ITEM - 1) / ITEM, items = f.n * per;
+    const int wr = lane & 15;
+    float sw[BUFS][GPI];
+    auto fetch = [&](int b, int item) {
+        const int en = item / per, it = item - en * per;
+        const int64_t first = (int64_t)f.expert(en) * H + n0;
+        const uint8_t* w = a.p.qw_down + first * rowbytes;
+        copy_item(buf + b * PIECE, w, w + 8 * (int64_t)rowbytes, rowbytes, it);
+        load_scales(sw[b], a.p.s_down + (first + wr) * G, G, it);
+    };
+#pragma unroll
+    for (int b = 0; b < BUFS; ++b)
+        if (wave + b * DOWN_WAVES < items) fetch(b, wave + b * DOWN_WAVES);
+
+    if (wave == 0) write_entries(t, f, k);
+    for (int i = tid; i < R * G * M4; i += DOWN_WAVES * 64) tab[i] = 0.0f;
+    lds_barrier();
+
+    // the codes of h, and its scales with the gates
+#pragma unroll
+    for (int j = 0; j < NX; ++j) {
+        const int i = tid + j * DOWN_WAVES * 64;
+        if (i >= n8) break;
+        const int s = i / (I / 8), c = i - s * (I / 8), en = t.entry[s];
+        if (en < 0) continue;                    // (16 neighbouring lanes share a slot; its h is not set)
+        const float amax = qrule::group_max<16>(qrule::absmax8(v[j]));
+        const float scale = amax / 7.0f;
+        *reinterpret_cast<uint32_t*>(hq + s * stride + 4 * c) = qrule::quantize8(v[j], scale, amax != 0.0f);
+        if ((c & 15) == 0) tab[(en * G + (c >> 4)) * M4 + s / k] = amax != 0.0f ? scale * a.p.gates[s] : 0.0f;
+    }
+    lds_barrier();
+
+    v4f acc = {};
+    for (int i0 = wave; i0 < items; i0 += BUFS * DOWN_WAVES) {
+#pragma unroll
+        for (int b = 0; b < BUFS; ++b) {
+            const int item = i0 + b * DOWN_WAVES;
+            if (item >= items) break;
+            wait_copies(item + DOWN_WAVES < items);
+            const int en = item / per, it = item - en * per;
+            const int s = wr < TOKENS ? t.slot[en][wr] : -1;
+            item_products(acc, buf + b * PIECE, hq + (s < 0 ? 0 : s) * stride + it * ITEM, rowbytes - it * ITEM, sw[b],
+                          [&](int q) {
+                              v4f v = {};
+                              if (4 * (lane >> 4) < M4)
+                                  v = *reinterpret_cast<const v4f*>(tab + (en * G + it * GPI + q) * M4 +
+                                                                    4 * (lane >> 4));
+                              return v;
+                          });
+            asm volatile("" ::: "memory");
+            const int next = item + BUFS * DOWN_WAVES;
+            if (next < items) fetch(b, next);
+        }
+    }
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(bufs);  // the buffers are done with
+    *reinterpret_cast<v4f*>(red + (wave * 64 + lane) * 4) = acc;
+    __syncthreads();
+    if (tid < 16 * TOKENS) {
+        const int m = tid >> 4, c = tid & 15;
+        if (m < M) {
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < DOWN_WAVES; ++w) v += red[(w * 64 + 16 * (m >> 2) + c) * 4 + (m & 3)];
+            v *= 0.00390625f;
+            asm volatile("" : "+v"(v));          // y16 is the fp16 rounding of y32
+            const int64_t o = (int64_t)m * H + n0 + c;
+            static_cast<_Float16*>(a.p.y16)[o] = (_Float16)v;
+            if (a.p.y32) a.p.y32[o] = v;
+        }
+    }
+}
+
+}  // namespace
+
+static TokenArgs token_args(const ExpertsProblem& p, int K)
+{
+    TokenArgs a{};
+    a.p = p;
+    a.G = K / 128;
+    a.M4 = ((int)p.M + 3) / 4 * 4;
+    return a;
+}
+
+bool experts_token_supports(const ExpertsProblem& p)
+{
+    if (p.M > TOKENS || p.M * p.k > SLOTS || p.H > 16384 || p.I > 16384) return false;
+    // what a workgroup quantizes, and its LDS beside buffers and entries: two workgroups of the first launch on a CU, one of the second
+    if (p.M * p.H > 32768 || p.M * p.k * p.I > 32768) return false;
+    return up_lds(token_args(p, p.H)) <= 14 * 1024 && down_lds(token_args(p, p.I)) <= 30 * 1024;
+}
+
+template <int NX_UP, int NX_DOWN>
+static hipError_t launch_token(const ExpertsProblem& p, _Float16* h, hipStream_t stream)
+{
+    const TokenArgs up = token_args(p, p.H), down = token_args(p, p.I);
+    const unsigned blocks = (unsigned)(p.M * p.k * (p.I / 8));
+    token_up_kernel<NX_UP><<<(blocks + UP_WAVES - 1) / UP_WAVES, UP_WAVES * 64, up_lds(up), stream>>>(up, h);
+    token_down_kernel<NX_DOWN><<<p.H / 16, DOWN_WAVES * 64, down_lds(down), stream>>>(down, h);
+    return hipGetLastError();
+}
+
+hipError_t launch_experts_token(const ExpertsProblem& p, _Float16* h, hipStream_t stream)
+{
+    // chunks of 8 values that a thread quantizes
+    const bool small_x = p.M * p.H <= 2 * 8 * UP_WAVES * 64, small_h = p.M * p.k * p.I <= 3 * 8 * DOWN_WAVES * 64;
+    if (small_x) return small_h ? launch_token<2, 3>(p, h, stream) : launch_token<2, 8>(p, h, stream);
+    return small_h ? launch_token<16, 3>(p, h, stream) : launch_token<16, 8>(p, h, stream);
+}
+
+}  // namespace apex4
