@@ -39,8 +39,9 @@ constexpr int SLOTS = 64;            // and slots
 constexpr int ITEM = 512;            // bytes of a row per item
 constexpr int PIECE = 16 * ITEM;     // bytes of an item
 constexpr int GPI = ITEM / 64;       // groups per item
+constexpr int BUF = PIECE + GPI * 64; // an item in LDS: its codes, its scales
 constexpr int UP_WAVES = 4, DOWN_WAVES = 8;
-constexpr int BUFS = 2;              // items in flight per wave
+constexpr int BUFS = 2;              // buffers of a wave
 constexpr int OOB = (int)0x80000000; // past every buffer: reads zeros
 constexpr int PAD = 16;              // bytes between activation rows: their reads fall on different banks
 
@@ -64,11 +65,12 @@ struct Found {
     }
 };
 
-__device__ inline Found find_entries(const int32_t* __restrict__ ids, int R, int k, int E)
+// (id: of this lane's slot, -1 past the slots)
+__device__ inline Found find_entries(int id, int R, int k, int E)
 {
     const int lane = threadIdx.x & 63;
     Found f;
-    f.id = lane < R ? ids[lane] : -1;
+    f.id = id;
     const bool live = f.id >= 0 && f.id < E;
     if (!live) f.id = -1 - lane;      // like no other
     int rank = 0;                     // this token's earlier slots of the same expert
@@ -126,13 +128,21 @@ __device__ inline void copy_item(uint8_t* dst, const uint8_t* rows0, const uint8
     }
 }
 
-// This lane's 8 scales of an item (weight row lane & 15).  Always 8 loads, so
-// that the wait counts are exact; past the row the last one again, which meets
-// codes that are zeros.
-__device__ inline void load_scales(float (&s)[GPI], const float* row, int G, int it)
+// The scales of an item's groups into [group][weight row] after its codes: lane
+// l of copy j brings row l & 15 of group 4 j + (l >> 4) (past the row: zeros).
+__device__ inline void copy_scales(uint8_t* dst, const float* rows0, const float* rows8, int G, int it)
 {
+    const int lane = threadIdx.x & 63, r = lane & 15;
 #pragma unroll
-    for (int q = 0; q < GPI; ++q) s[q] = row[min(it * GPI + q, G - 1)];
+    for (int j = 0; j < 2; ++j) {
+        const int g = it * GPI + 4 * j + (lane >> 4);
+        const int64_t far = r < 8 ? 0 : (rows8 - rows0) * 4;
+        // (gate and up rows of one expert: less than 2^31 bytes apart)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(rows0), (short)0,
+                                              (int)((rows8 - rows0) * 4 + 8 * G * 4), 0x00020000),
+            (lds_void*)(dst + PIECE + j * 256), 4, g < G ? (int)far + ((r & 7) * G + g) * 4 : OOB, 0, 0, 0);
+    }
 }
 
 // Workgroup barrier for what was stored to LDS; copies in flight stay in flight.
@@ -154,32 +164,50 @@ __device__ inline void load_chunks(half8 (&v)[NX], const half8* x, int n8, int t
 
 // acc[r] += sum over the item's groups of sa4(q)[r] s_w[q] P, P of activation row 4 (lane >> 4) + r and weight row
 // lane & 15.  `x`: the codes of this lane's activation row lane & 15 at the item's first byte; `left`: bytes of the
-// row from there (reads stop at the row's end: the weights' codes past it are zeros).
+// row from there.
 template <typename Scale>
-__device__ inline void item_products(v4f& acc, const uint8_t* buf, const uint8_t* x, int left, const float (&sw)[GPI],
-                                     Scale sa4)
+__device__ inline void item_products(v4f& acc, const uint8_t* buf, const uint8_t* x, int left, Scale sa4)
 {
     const int lane = threadIdx.x & 63, row = lane & 15, kg = lane >> 4;
+    const float* sw = reinterpret_cast<const float*>(buf + PIECE) + row;
+    const int groups = min(GPI, left / 64);
+    // four groups at a time, their reads together and then their products: one
+    // after the other each group waits for LDS and for the matrix unit (an item
+    // took 0.7 us); all eight unrolled, a launch of a few microseconds fetches
+    // more code than it saves
+#pragma unroll 1
+    for (int q0 = 0; q0 < groups; q0 += 4) {
+        v4i w[4], a[4], P[4];
 #pragma unroll
-    for (int q = 0; q < GPI; ++q) {
-        if (64 * q >= left) break;
-        const v4i w = *reinterpret_cast<const v4i*>(buf + row * ITEM + ((4 * q + kg) ^ row) * 16);
-        const v4i a = *reinterpret_cast<const v4i*>(x + 64 * q + 16 * kg);
-        v4i P = __builtin_amdgcn_mfma_i32_16x16x64_i8(widen_lo(a), widen_lo(w), v4i{}, 0, 0, 0);
-        P = __builtin_amdgcn_mfma_i32_16x16x64_i8(widen_hi(a), widen_hi(w), P, 0, 0, 0);
-        const v4f s = sa4(q);
+        for (int i = 0; i < 4; ++i) {
+            const int q = min(q0 + i, groups - 1);
+            w[i] = *reinterpret_cast<const v4i*>(buf + row * ITEM + ((4 * q + kg) ^ row) * 16);
+            a[i] = *reinterpret_cast<const v4i*>(x + 64 * q + 16 * kg);
+        }
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[r] = fmaf(s[r] * sw[q], (float)P[r], acc[r]);
+        for (int i = 0; i < 4; ++i)
+            P[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(widen_lo(a[i]), widen_lo(w[i]), v4i{}, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            P[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(widen_hi(a[i]), widen_hi(w[i]), P[i], 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (q0 + i >= groups) break;
+            const v4f s = sa4(q0 + i);
+            const float sn = sw[16 * (q0 + i)];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[r] = fmaf(s[r] * sn, (float)P[i][r], acc[r]);
+        }
     }
 }
 
-// This item's copies and scales have landed: all but the operations of the
-// next item, where one is in flight (8 copies and GPI scales).
-__device__ inline void wait_copies(bool next)
+// This item's copies have landed: all but the 10 of the item after it (8 of
+// codes, 2 of scales).  Items past the last are fetched too, as zeros from no
+// address, so that this count always holds.
+__device__ inline void wait_copies()
 {
     asm volatile("" ::: "memory");
-    if (next) __builtin_amdgcn_s_waitcnt(((8 + GPI) & 15) | (((8 + GPI) >> 4) << 14) | 0xF70);
-    else __builtin_amdgcn_s_waitcnt(0xF70);
+    __builtin_amdgcn_s_waitcnt(0xF70 | 10);
     asm volatile("" ::: "memory");
 }
 
@@ -201,22 +229,25 @@ __host__ __device__ inline int up_lds(const TokenArgs& a)
 template <int NX>
 __global__ __launch_bounds__(UP_WAVES * 64) void token_up_kernel(TokenArgs a, _Float16* __restrict__ h)
 {
-    // (buffers of their own: the compiler then keeps the stores of the codes
-    // apart from the copies in flight)
-    __shared__ __attribute__((aligned(1024))) uint8_t bufs[UP_WAVES * BUFS * PIECE];
+    // (objects of their own: the compiler then tells the copies in flight from
+    // the other buffer's reads and the stores of the codes)
+    __shared__ __attribute__((aligned(1024))) uint8_t buf0[UP_WAVES * BUF];
+    __shared__ __attribute__((aligned(1024))) uint8_t buf1[UP_WAVES * BUF];
     extern __shared__ __attribute__((aligned(16))) uint8_t xq[];
     __shared__ Entries t;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int M = (int)a.p.M, k = a.p.k, H = a.p.H, I = a.p.I, G = a.G, R = M * k;
-    uint8_t* buf = bufs + wave * BUFS * PIECE;
     const int stride = H / 2 + PAD;
     float* xs = reinterpret_cast<float*>(xq + M * stride);
 
     const int n8 = M * (H / 8);
+    // (the ids first: what is asked for before them is waited for with them)
+    int id = a.p.ids[min(lane, R - 1)];
     half8 v[NX];
     load_chunks(v, static_cast<const half8*>(a.p.x), n8, UP_WAVES * 64);
-    const Found f = find_entries(a.p.ids, R, k, a.p.E);
+    id = lane < R ? id : -1;
+    const Found f = find_entries(id, R, k, a.p.E);
     const int blocks = I / 8, block = blockIdx.x * UP_WAVES + wave, y = block / blocks;
     if (blockIdx.x * UP_WAVES >= f.n * blocks) return;
     const bool live = y < f.n;
@@ -225,15 +256,14 @@ __global__ __launch_bounds__(UP_WAVES * 64) void token_up_kernel(TokenArgs a, _F
     const uint8_t* gate = a.p.qw_gu + ((int64_t)e * 2 * I + n0) * rowbytes;
     const uint8_t* up = gate + (int64_t)I * rowbytes;
     const int wr = lane & 15;
-    const float* srow = a.p.s_gu + ((int64_t)e * 2 * I + n0 + (wr < 8 ? wr : I + wr - 8)) * G;
-    float sw[BUFS][GPI];
-    auto fetch = [&](int b, int it) {
-        copy_item(buf + b * PIECE, gate, up, rowbytes, it);
-        load_scales(sw[b], srow, G, it);
+    const float* sgate = a.p.s_gu + ((int64_t)e * 2 * I + n0) * G;
+    auto fetch = [&](uint8_t* buf, int it) {
+        copy_item(buf + wave * BUF, gate, up, rowbytes, it);
+        copy_scales(buf + wave * BUF, sgate, sgate + (int64_t)I * G, G, it);
     };
-#pragma unroll
-    for (int b = 0; b < BUFS; ++b)
-        if (b < items) fetch(b, b);
+    // (a wave without an entry: rows of expert 0)
+    fetch(buf0, 0);
+    fetch(buf1, 1);
 
     // the codes of x beside them
 #pragma unroll
@@ -257,15 +287,16 @@ __global__ __launch_bounds__(UP_WAVES * 64) void token_up_kernel(TokenArgs a, _F
 #pragma unroll
         for (int b = 0; b < BUFS; ++b) {
             const int it = i0 + b;
-            if (it >= items) break;
-            wait_copies(it + 1 < items);
-            item_products(acc, buf + b * PIECE, xrow + it * ITEM, rowbytes - it * ITEM, sw[b], [&](int q) {
-                return *reinterpret_cast<const v4f*>(xs + (it * GPI + q) * 16 + 4 * (lane >> 4));
-            });
+            wait_copies();
+            if (it < items)
+                item_products(acc, (b ? buf1 : buf0) + wave * BUF, xrow + it * ITEM, rowbytes - it * ITEM, [&](int q) {
+                    return *reinterpret_cast<const v4f*>(xs + (it * GPI + q) * 16 + 4 * (lane >> 4));
+                });
             asm volatile("" ::: "memory");
-            if (it + BUFS < items) fetch(b, it + BUFS);
+            fetch(b ? buf1 : buf0, it + BUFS);
         }
     }
+    __builtin_amdgcn_s_waitcnt(0xF70);   // no copy outlives the wave
     if (!live) return;
     // lane 16 (m >> 2) + n, register m & 3: activation row m and weight row n (gate rows 0..7, up rows 8..15)
 #pragma unroll
@@ -288,33 +319,49 @@ __host__ __device__ inline int down_lds(const TokenArgs& a)
 template <int NX>
 __global__ __launch_bounds__(DOWN_WAVES * 64) void token_down_kernel(TokenArgs a, const _Float16* __restrict__ h)
 {
-    __shared__ __attribute__((aligned(1024))) uint8_t bufs[DOWN_WAVES * BUFS * PIECE];
+    __shared__ __attribute__((aligned(1024))) uint8_t buf0[DOWN_WAVES * BUF];
+    __shared__ __attribute__((aligned(1024))) uint8_t buf1[DOWN_WAVES * BUF];
     extern __shared__ __attribute__((aligned(16))) uint8_t hq[];
     __shared__ Entries t;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int M = (int)a.p.M, k = a.p.k, H = a.p.H, I = a.p.I, G = a.G, R = M * k, M4 = a.M4;
-    uint8_t* buf = bufs + wave * BUFS * PIECE;
     const int stride = I / 2 + PAD;
     float* tab = reinterpret_cast<float*>(hq + R * stride);
 
     const int n8 = R * (I / 8);
+    int id = a.p.ids[min(lane, R - 1)];
     half8 v[NX];
     load_chunks(v, reinterpret_cast<const half8*>(h), n8, DOWN_WAVES * 64);
-    const Found f = find_entries(a.p.ids, R, k, a.p.E);
+    float gate[NX];
+#pragma unroll
+    for (int j = 0; j < NX; ++j) gate[j] = a.p.gates[min(tid + j * DOWN_WAVES * 64, n8 - 1) / (I / 8)];
+    id = lane < R ? id : -1;
+    const Found f = find_entries(id, R, k, a.p.E);
     const int n0 = blockIdx.x * 16, rowbytes = I / 2, per = (rowbytes + ITEM - 1) / ITEM, items = f.n * per;
     const int wr = lane & 15;
-    float sw[BUFS][GPI];
-    auto fetch = [&](int b, int item) {
-        const int en = item / per, it = item - en * per;
+    auto fetch = [&](uint8_t* buf, int item) {
+        int en = item / per, it = item - en * per;
+        if (item >= items) {
+            en = 0;
+            it = per;                            // past the rows: zeros
+        }
         const int64_t first = (int64_t)f.expert(en) * H + n0;
         const uint8_t* w = a.p.qw_down + first * rowbytes;
-        copy_item(buf + b * PIECE, w, w + 8 * (int64_t)rowbytes, rowbytes, it);
-        load_scales(sw[b], a.p.s_down + (first + wr) * G, G, it);
+        const float* sd = a.p.s_down + first * G;
+        copy_item(buf + wave * BUF, w, w + 8 * (int64_t)rowbytes, rowbytes, it);
+        copy_scales(buf + wave * BUF, sd, sd + 8 * G, G, it);
     };
-#pragma unroll
-    for (int b = 0; b < BUFS; ++b)
-        if (wave + b * DOWN_WAVES < items) fetch(b, wave + b * DOWN_WAVES);
+    if (f.n == 0) {                              // nothing live: zeros
+        for (int i = tid; i < M * 16; i += DOWN_WAVES * 64) {
+            const int64_t o = (int64_t)(i >> 4) * H + n0 + (i & 15);
+            static_cast<_Float16*>(a.p.y16)[o] = (_Float16)0.0f;
+            if (a.p.y32) a.p.y32[o] = 0.0f;
+        }
+        return;
+    }
+    fetch(buf0, wave);
+    fetch(buf1, wave + DOWN_WAVES);
 
     if (wave == 0) write_entries(t, f, k);
     for (int i = tid; i < R * G * M4; i += DOWN_WAVES * 64) tab[i] = 0.0f;
@@ -330,7 +377,7 @@ __global__ __launch_bounds__(DOWN_WAVES * 64) void token_down_kernel(TokenArgs a
         const float amax = qrule::group_max<16>(qrule::absmax8(v[j]));
         const float scale = amax / 7.0f;
         *reinterpret_cast<uint32_t*>(hq + s * stride + 4 * c) = qrule::quantize8(v[j], scale, amax != 0.0f);
-        if ((c & 15) == 0) tab[(en * G + (c >> 4)) * M4 + s / k] = amax != 0.0f ? scale * a.p.gates[s] : 0.0f;
+        if ((c & 15) == 0) tab[(en * G + (c >> 4)) * M4 + s / k] = amax != 0.0f ? scale * gate[j] : 0.0f;
     }
     lds_barrier();
 
@@ -339,25 +386,26 @@ __global__ __launch_bounds__(DOWN_WAVES * 64) void token_down_kernel(TokenArgs a
 #pragma unroll
         for (int b = 0; b < BUFS; ++b) {
             const int item = i0 + b * DOWN_WAVES;
-            if (item >= items) break;
-            wait_copies(item + DOWN_WAVES < items);
-            const int en = item / per, it = item - en * per;
-            const int s = wr < TOKENS ? t.slot[en][wr] : -1;
-            item_products(acc, buf + b * PIECE, hq + (s < 0 ? 0 : s) * stride + it * ITEM, rowbytes - it * ITEM, sw[b],
-                          [&](int q) {
-                              v4f v = {};
-                              if (4 * (lane >> 4) < M4)
-                                  v = *reinterpret_cast<const v4f*>(tab + (en * G + it * GPI + q) * M4 +
-                                                                    4 * (lane >> 4));
-                              return v;
-                          });
+            wait_copies();
+            if (item < items) {
+                const int en = item / per, it = item - en * per;
+                const int s = t.slot[en][wr];
+                item_products(acc, (b ? buf1 : buf0) + wave * BUF, hq + (s < 0 ? 0 : s) * stride + it * ITEM,
+                              rowbytes - it * ITEM, [&](int q) {
+                                  v4f v = {};
+                                  if (4 * (lane >> 4) < M4)
+                                      v = *reinterpret_cast<const v4f*>(tab + (en * G + it * GPI + q) * M4 +
+                                                                        4 * (lane >> 4));
+                                  return v;
+                              });
+            }
             asm volatile("" ::: "memory");
-            const int next = item + BUFS * DOWN_WAVES;
-            if (next < items) fetch(b, next);
+            fetch(b ? buf1 : buf0, item + BUFS * DOWN_WAVES);
         }
     }
+    __builtin_amdgcn_s_waitcnt(0xF70);           // no copy outlives its buffer
     __syncthreads();
-    float* red = reinterpret_cast<float*>(bufs);  // the buffers are done with
+    float* red = reinterpret_cast<float*>(buf0);  // the buffers are done with
     *reinterpret_cast<v4f*>(red + (wave * 64 + lane) * 4) = acc;
     __syncthreads();
     if (tid < 16 * TOKENS) {
@@ -391,7 +439,7 @@ bool experts_token_supports(const ExpertsProblem& p)
     if (p.M > TOKENS || p.M * p.k > SLOTS || p.H > 16384 || p.I > 16384) return false;
     // what a workgroup quantizes, and its LDS beside buffers and entries: two workgroups of the first launch on a CU, one of the second
     if (p.M * p.H > 32768 || p.M * p.k * p.I > 32768) return false;
-    return up_lds(token_args(p, p.H)) <= 14 * 1024 && down_lds(token_args(p, p.I)) <= 30 * 1024;
+    return up_lds(token_args(p, p.H)) <= 10 * 1024 && down_lds(token_args(p, p.I)) <= 22 * 1024;
 }
 
 template <int NX_UP, int NX_DOWN>
