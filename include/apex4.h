@@ -441,8 +441,11 @@ apex4_status apex4_pack_weight_e4m3(const void* w, int32_t w_type, int64_t N, in
  *   0 <= M, N <= 2^26 (either 0: no-op), 0 < K < 2^23, K % 128 == 0, M * K and N * K < 2^34.
  *
  * apex4_linear_e4m3: apex4_quantize_e4m3(x) into the workspace, then
- * apex4_gemm_e4m3, with the bits of those two calls; y has the type of x.
- *   workspace: at least apex4_linear_e4m3_workspace_size() bytes, 256-byte aligned.
+ * apex4_gemm_e4m3, with the bits of those two calls; y has the type of x.  Up
+ * to 16 rows with M * K <= 16384 and N * K <= 2^25 are one launch that
+ * quantizes the rows itself and needs no workspace.
+ *   workspace: at least apex4_linear_e4m3_workspace_size() bytes (NULL allowed
+ *   when that is 0), 256-byte aligned.
  */
 size_t apex4_gemm_e4m3_workspace_size(int64_t M, int64_t N, int64_t K);
 apex4_status apex4_gemm_e4m3(const void* qa8, const float* s_a, const void* qw8, const float* s_w, int64_t M,

@@ -87,12 +87,18 @@ def test_e4m3_refusals(L):
         assert gemm(**bad) == ALIGN, bad
     assert gemm(M=0, qa=None) == OK and gemm(N=0, qw=None) == OK
 
-    def linear(x=A, t=1, qw=A, sw=B, M=8, N=40, K=256, y=C, y32=None, ws=0x100000, n=None):
+    def linear(x=A, t=1, qw=A, sw=B, M=80, N=40, K=256, y=C, y32=None, ws=0x100000, n=None):
         n = L.apex4_linear_e4m3_workspace_size(M, N, K) if n is None else n
         return L.apex4_linear_e4m3(x, t, qw, sw, M, N, K, y, y32, ws, n, None)
 
-    need = L.apex4_linear_e4m3_workspace_size(8, 40, 256)
-    assert need >= 8 * 256 + 8 * 2 * 4
+    need = L.apex4_linear_e4m3_workspace_size(80, 40, 256)
+    assert need >= 80 * 256 + 80 * 2 * 4
+    # the smallest calls are one launch without a workspace
+    assert L.apex4_linear_e4m3_workspace_size(1, 4096, 4096) == 0
+    assert L.apex4_linear_e4m3_workspace_size(16, 40, 1024) == 0
+    assert L.apex4_linear_e4m3_workspace_size(17, 40, 256) > 0
+    assert L.apex4_linear_e4m3_workspace_size(16, 40, 1152) > 0
+    assert linear(M=8, ws=None, x=None) == INVALID
     assert linear(n=need - 1) == WORKSPACE and linear(ws=None) == WORKSPACE
     for bad in (dict(M=-1), dict(K=130), dict(x=None), dict(qw=None), dict(sw=None), dict(y=None)):
         assert linear(**bad) == INVALID, bad

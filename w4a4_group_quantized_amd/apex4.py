@@ -576,10 +576,11 @@ def linear_e4m3(x, qw8, sw, *, want_y32: bool = False, y=None, y32=None, workspa
         y = torch.empty((M, N), dtype=x.dtype, device=dev)
     if want_y32 and y32 is None:
         y32 = torch.empty((M, N), dtype=torch.float32, device=dev)
-    if workspace is None:
-        workspace = torch.empty(linear_e4m3_workspace_size(M, N, K), dtype=torch.uint8, device=dev)
+    need = linear_e4m3_workspace_size(M, N, K)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     _call("apex4_linear_e4m3", dev, x.data_ptr(), code, qw8.data_ptr(), sw.data_ptr(), M, N, K, y.data_ptr(),
-          _ptr(y32), workspace.data_ptr(), workspace.numel())
+          _ptr(y32), _ptr(workspace), 0 if workspace is None else workspace.numel())
     return (y, y32) if want_y32 else y
 
 

@@ -193,6 +193,7 @@ apex4_status apex4_gemm_e4m3(const void* qa8, const float* s_a, const void* qw8,
 size_t apex4_linear_e4m3_workspace_size(int64_t M, int64_t N, int64_t K)
 {
     if (!e4m3_sizes(M, N, K) || M == 0 || N == 0) return 0;
+    if (apex4::e4m3_rows_quantizes(e4m3_problem(M, N, K))) return 0;
     return align256((size_t)M * K) + align256((size_t)M * (K / 128) * 4) + apex4_gemm_e4m3_workspace_size(M, N, K);
 }
 
@@ -210,19 +211,20 @@ apex4_status apex4_linear_e4m3(const void* x, int32_t x_type, const void* qw8, c
         !aligned(workspace, 256))
         return APEX4_ERR_ALIGNMENT;
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    const size_t qa_bytes = align256((size_t)M * K), sa_bytes = align256((size_t)M * (K / 128) * 4);
-    float* sa = reinterpret_cast<float*>(ws + qa_bytes);
-    const hipError_t e = apex4::launch_quantize_e4m3(x, x_type == APEX4_BF16, M, K, ws, sa, st);
-    if (e != hipSuccess) return APEX4_ERR_HIP;
     apex4::E4m3Problem p = e4m3_problem(M, N, K);
-    p.qa = ws;
-    p.sa = sa;
     p.qw = static_cast<const uint8_t*>(qw8);
     p.sw = s_w;
     p.bf16 = x_type == APEX4_BF16;
     p.y = y;
     p.y32 = y_f32;
+    if (apex4::e4m3_rows_quantizes(p)) return to_status(apex4::launch_e4m3_rows(p, x, st));
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const size_t qa_bytes = align256((size_t)M * K), sa_bytes = align256((size_t)M * (K / 128) * 4);
+    float* sa = reinterpret_cast<float*>(ws + qa_bytes);
+    const hipError_t e = apex4::launch_quantize_e4m3(x, p.bf16, M, K, ws, sa, st);
+    if (e != hipSuccess) return APEX4_ERR_HIP;
+    p.qa = ws;
+    p.sa = sa;
     p.ws = ws + qa_bytes + sa_bytes;
     return to_status(apex4::launch_gemm_e4m3(p, st));
 }

@@ -164,6 +164,9 @@ struct E4m3Problem {
 };
 size_t e4m3_workspace_bytes(const E4m3Problem& p);
 hipError_t launch_gemm_e4m3(const E4m3Problem& p, hipStream_t stream);
+// the smallest calls, which quantize the rows x (of y's type) themselves
+bool e4m3_rows_quantizes(const E4m3Problem& p);
+hipError_t launch_e4m3_rows(const E4m3Problem& p, const void* x, hipStream_t stream);
 hipError_t launch_quantize_e4m3(const void* x, bool bf16, int64_t rows, int64_t K, void* q8, float* s,
                                 hipStream_t stream);
 hipError_t launch_pack_e4m3(const void* w, bool bf16, int64_t N, int64_t K, void* q8, float* s, hipStream_t stream);
