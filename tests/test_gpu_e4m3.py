@@ -94,7 +94,8 @@ def check_gemm(dev, M, N, K, seed, dtype):
 # a block of 128; one block of K, and numbers of blocks that fill no item
 SHAPES = [(1, 1, 128), (4, 33, 4096), (5, 200, 4096), (16, 40, 1024), (1, 48, 16384), (1, 128, 128), (2, 17, 256), (3, 130, 640), (16, 96, 512), (17, 257, 384), (33, 64, 1152),
           (64, 384, 1024), (65, 129, 896), (128, 128, 128), (130, 300, 768), (257, 520, 640), (300, 1000, 256),
-          (513, 136, 1408)]
+          (513, 136, 1408),
+          (9, 9000, 4224), (16, 70000, 640), (24, 8300, 5248), (3, 300, 114816)]
 
 
 @pytest.mark.parametrize("M,N,K", SHAPES)

@@ -12,7 +12,7 @@ typedef float v16f __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void;
 
-constexpr int KB = 128;          // K values (bytes of a row) per stage: one block
+constexpr int KB = 128;          // K values (bytes of a row) of a block
 
 struct TileArgs {
     E4m3Problem p;
@@ -63,13 +63,19 @@ __device__ inline void tile_coords(const TileArgs& a, int tile, int& by, int& bx
 
 // WN x WM waves, each NT tiles of 16 weight rows by MT tiles of 16 activation
 // rows; WPS: waves per SIMD that registers and LDS leave room for.
-template <bool BF16, int WN, int WM, int NT, int MT, int WPS>
+// KST: blocks of K per stage.
+template <bool BF16, int WN, int WM, int NT, int MT, int WPS, int KST>
 __global__ __launch_bounds__(WN* WM * 64, WPS) void e4m3_tile_kernel(TileArgs a)
 {
     constexpr int BN = WN * NT * 16, BM = WM * MT * 16, WAVES = WN * WM;
-    constexpr int LOADS = (BN + BM) / 8 / WAVES;     // 1 KB copies per wave and stage
-    static_assert(BN % (WAVES * 8) == 0 && BM % (WAVES * 8) == 0, "a copy step is of w or of x");
-    constexpr int STAGE = (BN + BM) * KB;
+    constexpr int RB = KST * KB;                     // bytes of a row per stage
+    constexpr int LPR = RB / 16, RPC = 64 / LPR;     // lanes per row, rows per 1 KB copy
+    constexpr int STEP = WAVES * RPC;                // rows that the waves' copies bring at a time
+    constexpr int LOADS = (BN + BM) / STEP;          // 1 KB copies per wave and stage
+    static_assert(BN % STEP == 0 && BM % STEP == 0, "a copy step is of w or of x");
+    constexpr int STAGE = (BN + BM) * RB;
+    // (objects of their own: the compiler then tells the copies in flight from
+    // the reads of the other buffers)
     __shared__ __attribute__((aligned(1024))) uint8_t buf0[STAGE];
     __shared__ __attribute__((aligned(1024))) uint8_t buf1[STAGE];
     const int tid = threadIdx.x, lane = tid & 63;
@@ -93,49 +99,57 @@ __global__ __launch_bounds__(WN* WM * 64, WPS) void e4m3_tile_kernel(TileArgs a)
     tile_coords(a, lin, by, bx);
     const int m0 = by * BM, n0 = bx * BN;
     const int K = p.K, G = K / KB;
-    const int s0 = split ? kpart * G / a.parts : 0;
-    const int stages = split ? (kpart + 1) * G / a.parts - s0 : G;
+    const int all = (G + KST - 1) / KST;             // stages of all of K
+    const int s0 = split ? kpart * all / a.parts : 0;
+    const int stages = split ? (kpart + 1) * all / a.parts - s0 : all;
     const int rows_m = min(BM, p.M - m0), rows_n = min(BN, p.N - n0);
     const __amdgpu_buffer_rsrc_t rSA = buffer_of(p.sa + (int64_t)m0 * G, (uint32_t)rows_m * G * 4);
     const int nblk = n0 / 128, nblks = (rows_n + 127) / 128;
     const __amdgpu_buffer_rsrc_t rSW = buffer_of(p.sw + (int64_t)nblk * G, (uint32_t)nblks * G * 4);
 
-    // Copy j of this wave brings rows 8 (j WAVES + wave) .. + 7 of the stage's
-    // BN rows of w and BM rows of x, 128 bytes each; lane l fetches chunk
-    // (l & 7) ^ (row & 7) of row l >> 3, so that the fragment reads of 8 rows
-    // at one column touch every bank once.  A descriptor per copy, so
-    // that one lane offset serves all of them and rows past the end read zeros.
+    // Copy j of this wave brings rows RPC (j WAVES + wave) .. of the stage's BN
+    // rows of w and BM rows of x; lane l fetches chunk (l % LPR) ^ (row & KEY) of
+    // row l / LPR, so that the fragment reads of 16 rows at one column touch every
+    // bank once.  A descriptor per copy, so that one lane offset serves all of
+    // them and rows past the end read zeros.
     const uint8_t* src[LOADS];
     uint32_t bytes[LOADS];
 #pragma unroll
     for (int j = 0; j < LOADS; ++j) {
-        const int r = j * WAVES * 8;
+        const int r = j * STEP;
         const bool w = r < BN;
         const int first = w ? r : r - BN;
         const int left = max(0, (w ? rows_n : rows_m) - first);
         src[j] = w ? p.qw + (int64_t)(n0 + first) * K : p.qa + (int64_t)(m0 + first) * K;
-        bytes[j] = __builtin_amdgcn_readfirstlane((uint32_t)min(left, WAVES * 8) * K);
+        bytes[j] = __builtin_amdgcn_readfirstlane((uint32_t)min(left, STEP) * K);
     }
-    const int voff = (8 * wave + (lane >> 3)) * K + ((lane & 7) ^ (lane >> 3)) * 16;
+    constexpr int KEY = LPR < 16 ? LPR - 1 : 15;      // bits of the row that place its chunks
+    const int lrow = RPC * wave + lane / LPR, lchunk = (lane % LPR) ^ (lrow & KEY);
     auto copy = [&](uint8_t* dst, int t, int j0, int j1) {
 #pragma unroll
-        for (int j = j0; j < j1; ++j)
-            copy_1k(src[j], bytes[j], dst + (j * WAVES + wave) * 1024, voff, (s0 + t) * KB);
+        for (int j = j0; j < j1; ++j) {
+            // (steps of fewer than 16 rows: the row's upper bit comes from the step)
+            const int chunk = lchunk ^ (j * STEP & KEY);
+            // (more blocks a stage than K has left: those stay out)
+            const bool out = KST > 1 && (s0 + t) * KST + chunk / 8 >= G;
+            copy_1k(src[j], bytes[j], dst + (j * WAVES + wave) * 1024, out ? (int)0x80000000 : lrow * K + chunk * 16,
+                    (s0 + t) * RB);
+        }
     };
 
-    // scales of four stages at a time: one register set, reloaded as soon as
-    // the last of the four stages has taken its values
+    // scales of four blocks at a time: one register set, reloaded as soon as
+    // the last of the four has given its values
     uint32_t saoff[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) saoff[i] = (uint32_t)(wm * MT * 16 + i * 16 + (lane & 15)) * G * 4;
     const uint32_t swoff = (uint32_t)(wn * NT * 16 / 128) * G * 4;
     v4f sa[MT], sw;
-    auto load_scales = [&](int t) {
+    auto load_scales = [&](int block) {
 #pragma unroll
         for (int i = 0; i < MT; ++i)
             sa[i] = __builtin_bit_cast(
-                v4f, __builtin_amdgcn_raw_buffer_load_b128(rSA, (int)saoff[i] + (s0 + t) * 4, 0, 0));
-        sw = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rSW, (int)swoff + (s0 + t) * 4, 0, 0));
+                v4f, __builtin_amdgcn_raw_buffer_load_b128(rSA, (int)saoff[i] + (s0 * KST + block) * 4, 0, 0));
+        sw = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rSW, (int)swoff + (s0 * KST + block) * 4, 0, 0));
     };
 
     // Fragment offsets: row lane & 15, chunks (lane >> 4) + 4 j (any split of
@@ -144,11 +158,13 @@ __global__ __launch_bounds__(WN* WM * 64, WPS) void e4m3_tile_kernel(TileArgs a)
     // the others: with neighbouring chunks in neighbouring lane groups their
     // 16 rows lie in 16 different places of the 256 bytes (chunks 2 (lane >>
     // 4) + j took two cycles).
-    const int row = lane & 15, key = row & 7;
-    int foff[2];
+    const int row = lane & 15, key = row & KEY;
+    int foff[KST][2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) foff[j] = row * KB + (((lane >> 4) + 4 * j) ^ key) * 16;
-    const int wbase = wn * NT * 16 * KB, xbase = (BN + wm * MT * 16) * KB;
+    for (int q = 0; q < KST; ++q)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) foff[q][j] = row * RB + ((8 * q + (lane >> 4) + 4 * j) ^ key) * 16;
+    const int wbase = wn * NT * 16 * RB, xbase = (BN + wm * MT * 16) * RB;
 
     v4f acc[MT][NT];
 #pragma unroll
@@ -156,23 +172,21 @@ __global__ __launch_bounds__(WN* WM * 64, WPS) void e4m3_tile_kernel(TileArgs a)
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j] = v4f{};
 
-    auto frag = [&](const uint8_t* b) {
-        const v4i lo = *reinterpret_cast<const v4i*>(b + foff[0]);
-        const v4i hi = *reinterpret_cast<const v4i*>(b + foff[1]);
+    auto frag = [&](const uint8_t* b, int q) {
+        const v4i lo = *reinterpret_cast<const v4i*>(b + foff[q][0]);
+        const v4i hi = *reinterpret_cast<const v4i*>(b + foff[q][1]);
         return v8i{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
     };
-    auto compute = [&](const uint8_t* b, const float (&S)[MT], uint8_t* next, int t_next) {
+    auto compute = [&](const uint8_t* b, int q, const float (&S)[MT], auto&& issue) {
         v8i x[MT], w[2];
         v4f P[2][MT];
 #pragma unroll
-        for (int i = 0; i < MT; ++i) x[i] = frag(b + xbase + i * 16 * KB);
-        w[0] = frag(b + wbase);
+        for (int i = 0; i < MT; ++i) x[i] = frag(b + xbase + i * 16 * RB, q);
+        w[0] = frag(b + wbase, q);
 #pragma unroll
         for (int j = 0; j <= NT; ++j) {
-            // the next stage's copies, two beside each of the first w tiles
-            // (past the last stage: stage 0 again, into a buffer that is not read)
-            if (2 * j < LOADS) copy(next, t_next, 2 * j, min(2 * j + 2, LOADS));
-            if (j + 1 < NT) w[(j + 1) & 1] = frag(b + wbase + (j + 1) * 16 * KB);
+            issue(j);
+            if (j + 1 < NT) w[(j + 1) & 1] = frag(b + wbase + (j + 1) * 16 * RB, q);
             // the products of w tile j beside the fold of tile j - 1, kept in
             // this order: left alone, the compiler folds each product at once
             // and waits for the matrix unit
@@ -198,11 +212,25 @@ __global__ __launch_bounds__(WN* WM * 64, WPS) void e4m3_tile_kernel(TileArgs a)
             const int t = t0 + h;
             if (t >= stages) break;
             stage_barrier();
-            float S[MT];
+            // the next stage's copies, two beside each of the first w tiles,
+            // the rest at once (past the last stage: a stage again, into a
+            // buffer that is not read)
+            auto issue = [&](int j) {
+                if (2 * j < LOADS)
+                    copy(h & 1 ? buf0 : buf1, t + 1 < stages ? t + 1 : 0, 2 * j,
+                         j == NT ? LOADS : min(2 * j + 2, LOADS));
+            };
 #pragma unroll
-            for (int i = 0; i < MT; ++i) S[i] = sa[i][h] * sw[h];
-            if (h == 3) load_scales(t + 1);
-            compute(h & 1 ? buf1 : buf0, S, h & 1 ? buf0 : buf1, t + 1 < stages ? t + 1 : 0);
+            for (int q = 0; q < KST; ++q) {
+                const int o = (KST * h + q) & 3;
+                float S[MT];
+#pragma unroll
+                for (int i = 0; i < MT; ++i) S[i] = sa[i][o] * sw[o];
+                if (o == 3) load_scales(t * KST + q + 1);
+                if (KST > 1 && (s0 + t) * KST + q >= G) continue;
+                if (q == 0) compute(h & 1 ? buf1 : buf0, q, S, issue);
+                else compute(h & 1 ? buf1 : buf0, q, S, [](int) {});
+            }
         }
     }
 
@@ -249,10 +277,10 @@ __global__ __launch_bounds__(WN* WM * 64, WPS) void e4m3_tile_kernel(TileArgs a)
     }
     uint16_t* y = static_cast<uint16_t*>(p.y);
     if (p.N % 8 == 0 && (reinterpret_cast<uintptr_t>(y) & 15) == 0) {
+        constexpr int OL = ROW / 16;                  // lanes per row
 #pragma unroll 4
-        for (int q = 0; q < MT * 16 * ROW / 1024; ++q) {
-            constexpr int LPR = ROW / 16;             // lanes per row
-            const int lm = 64 / LPR * q + lane / LPR, c = 2 * (lane % LPR);
+        for (int q = lane; q < MT * 16 * OL; q += 64) {
+            const int lm = q / OL, c = 2 * (q % OL);
             const uint2 u = *reinterpret_cast<const uint2*>(out + lm * ROW + (c ^ (lm & PM)) * 8);
             const uint2 v = *reinterpret_cast<const uint2*>(out + lm * ROW + ((c + 1) ^ (lm & PM)) * 8);
             const int m = r0 + lm, n = c0 + 4 * c;
@@ -302,22 +330,25 @@ __global__ __launch_bounds__(256) void e4m3_reduce_kernel(TileArgs a)
 
 // The tile shapes, and how a call is cut: the shape and the number of K parts
 // of the last tiles with the least modelled time.  The model's numbers are
-// measured on 256 compute units: a stage (128 of K) of a CU that holds all the
+// measured on 256 compute units: a block (128 of K) of a CU that holds all the
 // workgroups it can, and of one that holds a single one, which waits for its
-// copies; 5.9 TB/s for the operands, 12 TB/s for weights read again by another
+// copies; 5.5 TB/s for the operands, 12 TB/s for weights read again by another
 // row of tiles; the shorter of the two times hides to two thirds under the
 // longer; 4 TB/s for writing the partial sums and reading them again, and 1 us
-// for that launch.  E.g. 64 x 28672 x 8192: 128 x 64 tiles (weight rows x rows)
-// in two parts 46 us, in one 53, 256 x 256 163; 16 x 28672 x 8192: 128 x 32 in
-// two parts 39, 128 x 64 in one 49; 4096 x 8192 x 8192: 256 x 256 260, 128 x 128
-// 321, 128 x 64 419.
+// for that launch.  For few rows what counts is how much of a weight row one
+// copy covers: 16 x 28672 x 8192 (235 MB, weights from HBM) takes 57 us with
+// 128 bytes of 128 rows a stage, 47 with 256 bytes of 64 and 43 (5.5 TB/s)
+// with 512 bytes of 64; beyond 32 rows the codes of x take their part of the
+// copies, and 128 bytes of 128 weight rows are as good (64 x 28672 x 8192: 62
+// us both).  Many rows: 4096 x 8192 x 8192 260 us in tiles of 256 x 256, 321 in
+// 128 x 128, 419 in 128 x 64.
 struct Shape {
     int bn, bm, per_cu;          // weight rows, activation rows, workgroups that fit a CU
-    double loaded_us, alone_us;  // one stage
+    double loaded_us, alone_us;  // one block of K
 };
-constexpr int SHAPES = 4;
+constexpr int SHAPES = 5;
 constexpr Shape kShapes[SHAPES] = {
-    {256, 256, 1, 2.0, 1.6}, {128, 128, 2, 1.25, 0.78}, {128, 64, 3, 1.09, 0.6}, {128, 32, 4, 1.1, 0.5}};
+    {256, 256, 1, 2.0, 1.6}, {128, 128, 2, 1.25, 0.78}, {128, 64, 3, 1.09, 0.6}, {64, 32, 3, 0.6, 0.45}, {64, 16, 2, 0.4, 0.32}};
 
 struct Cut {
     int shape, tail, parts;
@@ -346,7 +377,7 @@ Cut choose(const E4m3Problem& p, int cus)
             }
             double us = (double)(tiles / slots) * G * s.loaded_us + last * ((G + parts - 1) / parts);
             const double w = (double)p.N * p.K, rows = (p.M + s.bm - 1) / s.bm;
-            const double read = (w + (double)p.M * p.K + 2.0 * p.M * p.N) / 5.9e6 + (rows - 1) * w / 12e6;
+            const double read = (w + (double)p.M * p.K + 2.0 * p.M * p.N) / 5.5e6 + (rows - 1) * w / 12e6;
             us = us > read ? us + 0.35 * read : read + 0.35 * us;
             const int64_t mem = parts > 1 ? tail * parts * s.bm * s.bn * 4 : 0;
             if (mem) us += 1.0 + (double)mem / 4e6;
@@ -359,14 +390,14 @@ Cut choose(const E4m3Problem& p, int cus)
     return best;
 }
 
-template <bool BF16, int WN, int WM, int NT, int MT, int WPS>
+template <bool BF16, int WN, int WM, int NT, int MT, int WPS, int KST = 1>
 hipError_t launch_shape(TileArgs a, hipStream_t stream)
 {
     constexpr int BN = WN * NT * 16, BM = WM * MT * 16;
     a.tiles_m = (a.p.M + BM - 1) / BM;
     a.tiles_n = (a.p.N + BN - 1) / BN;
     const int64_t grid = (int64_t)a.tiles_m * a.tiles_n + (int64_t)a.tail * (a.parts - 1);
-    e4m3_tile_kernel<BF16, WN, WM, NT, MT, WPS><<<(unsigned)grid, WN * WM * 64, 0, stream>>>(a);
+    e4m3_tile_kernel<BF16, WN, WM, NT, MT, WPS, KST><<<(unsigned)grid, WN * WM * 64, 0, stream>>>(a);
     if (a.tail) {
         const int64_t n = (int64_t)a.tail * (BM * BN / 4);
         e4m3_reduce_kernel<BF16, BN, BM><<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(a);
@@ -380,7 +411,8 @@ hipError_t launch_cut(const TileArgs& a, int shape, hipStream_t stream)
     if (shape == 0) return launch_shape<BF16, 2, 4, 8, 4, 2>(a, stream);
     if (shape == 1) return launch_shape<BF16, 2, 2, 4, 4, 2>(a, stream);
     if (shape == 2) return launch_shape<BF16, 4, 1, 2, 4, 3>(a, stream);
-    return launch_shape<BF16, 4, 1, 2, 2, 4>(a, stream);
+    if (shape == 3) return launch_shape<BF16, 4, 1, 1, 2, 3, 2>(a, stream);
+    return launch_shape<BF16, 4, 1, 1, 1, 2, 4>(a, stream);
 }
 
 }  // namespace
