@@ -8,6 +8,7 @@
 // are quantized per token, and the products run per expert over its rows.
 #include "experts.h"
 #include "internal.h"
+#include "quant_rule.h"
 
 namespace apex4 {
 namespace {
@@ -58,12 +59,26 @@ Parts parts_of(void* ws, int64_t M, int32_t k, int32_t E, int32_t H, int32_t I)
 // them again to place its own; the ids stay in L2.  Each wave takes a
 // contiguous run of slots, so that only the waves' counts cross the barrier.
 constexpr int PLAN_WAVES = 16;
+// The workgroups past the experts quantize x meanwhile (the rule of
+// apex4_quantize_act, a chunk of 8 values a thread).
 __global__ __launch_bounds__(64 * PLAN_WAVES) void plan_kernel(const int32_t* __restrict__ ids, int32_t R, int32_t E,
                                                                int32_t* __restrict__ offsets,
                                                                int32_t* __restrict__ order,
-                                                               int32_t* __restrict__ place)
+                                                               int32_t* __restrict__ place,
+                                                               const qrule::half8* __restrict__ x, int64_t n8,
+                                                               uint32_t* __restrict__ xq, float* __restrict__ xs)
 {
     __shared__ int below[PLAN_WAVES], equal[PLAN_WAVES];
+    if (blockIdx.x >= E) {
+        const int64_t t = (int64_t)(blockIdx.x - E) * (64 * PLAN_WAVES) + threadIdx.x;
+        if (t >= n8) return;      // (whole groups of 16 lanes)
+        const qrule::half8 v = x[t];
+        const float amax = qrule::group_max<16>(qrule::absmax8(v));
+        const float scale = amax / 7.0f;
+        xq[t] = qrule::quantize8(v, scale, amax != 0.0f);
+        if ((t & 15) == 0) xs[t / 16] = amax != 0.0f ? scale : 0.0f;
+        return;
+    }
     const int e = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int per = ((R + PLAN_WAVES - 1) / PLAN_WAVES + 63) / 64 * 64;
     const int64_t first = (int64_t)wave * per;
@@ -120,24 +135,36 @@ __global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ 
     const int per = H / 4;
     const int64_t m = t / per;
     const int c = (int)(t - m * per) * 4;
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int j = 0; j < k; ++j) {
-        const int r = place[m * k + j];
-        if (r < 0) continue;
-        const float g = gates[m * k + j];
-        const float4 v = *reinterpret_cast<const float4*>(d + (int64_t)r * H + c);
-        s[0] = fmaf(g, v.x, s[0]);
-        s[1] = fmaf(g, v.y, s[1]);
-        s[2] = fmaf(g, v.z, s[2]);
-        s[3] = fmaf(g, v.w, s[3]);
+    typedef float v4f __attribute__((ext_vector_type(4)));
+    v4f s = {};
+    // eight slots' rows at a time, so that their reads are under way together
+    for (int j0 = 0; j0 < k; j0 += 8) {
+        int r[8];
+        float g[8];
+        v4f v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            r[j] = j0 + j < k ? place[m * k + j0 + j] : -1;
+            g[j] = r[j] >= 0 ? gates[m * k + j0 + j] : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            v[j] = r[j] >= 0 ? *reinterpret_cast<const v4f*>(d + (int64_t)r[j] * H + c) : v4f{};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[i] = fmaf(g[j], v[j][i], s[i]);
     }
+    typedef _Float16 half4 __attribute__((ext_vector_type(4)));
+    half4 o;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float v = s[i];
         asm volatile("" : "+v"(v));   // y16 is the fp16 rounding of y32
-        y16[m * H + c + i] = (_Float16)v;
+        o[i] = (_Float16)v;
         if (y32) y32[m * H + c + i] = v;
     }
+    *reinterpret_cast<half4*>(y16 + m * H + c) = o;
 }
 
 }  // namespace
@@ -152,9 +179,11 @@ hipError_t launch_experts(const ExpertsProblem& p, hipStream_t stream)
     const Parts w = parts_of(p.ws, p.M, p.k, p.E, p.H, p.I);
     const int32_t R = (int32_t)(p.M * p.k);
     if (experts_token_supports(p)) return launch_experts_token(p, w.h, stream);
-    plan_kernel<<<p.E, 64 * PLAN_WAVES, 0, stream>>>(p.ids, R, p.E, w.offsets, w.order, w.place);
-    hipError_t e = launch_quantize(p.x, p.M, p.H, 128, w.xq, w.xs, stream);
-    if (e != hipSuccess) return e;
+    const int64_t n8 = p.M * (p.H / 8);
+    const unsigned chunks = (unsigned)((n8 + 64 * PLAN_WAVES - 1) / (64 * PLAN_WAVES));
+    plan_kernel<<<p.E + chunks, 64 * PLAN_WAVES, 0, stream>>>(p.ids, R, p.E, w.offsets, w.order, w.place,
+                                                              static_cast<const qrule::half8*>(p.x), n8,
+                                                              reinterpret_cast<uint32_t*>(w.xq), w.xs);
     ExpertsProduct a{};
     a.offsets = w.offsets;
     a.order = w.order;
@@ -169,7 +198,7 @@ hipError_t launch_experts(const ExpertsProblem& p, hipStream_t stream)
     a.h = w.h;
     a.rows = p.M;
     launch_experts_tiled(a, true, R, stream);
-    e = launch_quantize(w.h, R, p.I, 128, w.hq, w.hs, stream);
+    const hipError_t e = launch_quantize(w.h, R, p.I, 128, w.hq, w.hs, stream);
     if (e != hipSuccess) return e;
     a.qx = w.hq;
     a.sx = w.hs;

@@ -1,8 +1,8 @@
 // The experts' W4A4 products (apex4_experts_w4a4) in LDS tiles on gfx950.
 //
 // A workgroup computes BN weight rows of one expert by BM of its rows.  The
-// packed nibbles go straight from memory to LDS (stages of 128 bytes a row:
-// two groups of 128 codes), two stage buffers, the copies of the next stage
+// packed nibbles go straight from memory to LDS (stages of SB bytes a row, SB /
+// 64 groups of 128 codes), two stage buffers, the copies of the next stage
 // issued beside the first products of this one; the scales of the stage's
 // groups come in by 4-byte copies, turned so that group and row index the
 // buffer.  A wave reads 16 bytes a lane of 16 rows, widens the nibbles to the
@@ -26,7 +26,6 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void;
 
-constexpr int SB = 128;              // bytes of a row per stage: 256 codes, two groups
 constexpr int OOB = (int)0x80000000; // past every buffer: reads zeros
 
 __device__ inline __amdgpu_buffer_rsrc_t buffer_of(const void* p, uint32_t bytes)
@@ -101,18 +100,24 @@ __device__ inline bool find_tile(const int32_t* __restrict__ offsets, int E, int
 }
 
 // UP: gate and up rows in alternating tiles of 16, h out; else d out.
-// WN x WM waves, each NT tiles of 16 weight rows by MT tiles of 16 rows.
-template <bool UP, int WN, int WM, int NT, int MT, int WPS>
+// WN x WM waves, each NT tiles of 16 weight rows by MT tiles of 16 rows; SB:
+// bytes of a row per stage.
+template <bool UP, int WN, int WM, int NT, int MT, int WPS, int SB>
 __global__ __launch_bounds__(WN* WM * 64, WPS) void experts_tile_kernel(ExpertsProduct a)
 {
     constexpr int BN = WN * NT * 16, BM = WM * MT * 16, WAVES = WN * WM;
-    constexpr int WCOPIES = BN / 8 / WAVES;                    // per wave and stage
-    constexpr int XCOPIES = (BM / 8 + WAVES - 1) / WAVES;
+    constexpr int GS = SB / 64;                                // groups per stage
+    constexpr int LPR = SB / 16, RPC = 64 / LPR;               // lanes per row, rows per 1 KB copy
+    constexpr int KEY = LPR - 1;                               // bits of the row that place its chunks
+    constexpr int WCOPIES = BN / RPC / WAVES;                  // per wave and stage
+    constexpr int XCOPIES = (BM / RPC + WAVES - 1) / WAVES;
     constexpr int WS = BN / 64, XS = (BM + 63) / 64;           // scale copies per group
-    constexpr int SCOPIES = (2 * (WS + XS) + WAVES - 1) / WAVES;
+    constexpr int SCOPIES = (GS * (WS + XS) + WAVES - 1) / WAVES;
     constexpr int DATA = (BN + BM) * SB;
-    constexpr int STAGE = DATA + 2 * 256 * (WS + XS);
-    static_assert(BN % (8 * WAVES) == 0 && BN % 64 == 0, "copies of the weights divide among the waves");
+    constexpr int STAGE = DATA + GS * 256 * (WS + XS);
+    static_assert(LPR <= 16 && RPC * WAVES % 16 == 0 && BN % (RPC * WAVES) == 0 && BN % 64 == 0 && BM % RPC == 0,
+                  "copies of the weights divide among the waves");
+    static_assert(!UP || NT % 2 == 0, "a wave holds gate and up");
     __shared__ __attribute__((aligned(1024))) uint8_t buf0[STAGE];
     __shared__ __attribute__((aligned(1024))) uint8_t buf1[STAGE];
     const int tid = threadIdx.x, lane = tid & 63;
@@ -130,7 +135,7 @@ __global__ __launch_bounds__(WN* WM * 64, WPS) void experts_tile_kernel(ExpertsP
     count = __builtin_amdgcn_readfirstlane(count);
     const int m0 = __builtin_amdgcn_readfirstlane(mt) * BM, n0 = __builtin_amdgcn_readfirstlane(nt) * BN;
     const int rowbytes = a.K / 2, G = a.K / 128, half = a.N / 2;
-    const int stages = (G + 1) / 2;
+    const int stages = (G + GS - 1) / GS;
     const uint8_t* qw = a.qw + (int64_t)e * a.N * rowbytes;
     const float* sw = a.sw + (int64_t)e * a.N * G;
     // weight row of row r of the tile (a.N and more: none)
@@ -148,30 +153,38 @@ __global__ __launch_bounds__(WN* WM * 64, WPS) void experts_tile_kernel(ExpertsP
     const uint8_t* qx = a.qx + base * rowbytes;
     const float* sx = a.sx + base * G;
 
-    // --- the copies of this wave: 8 rows of 128 bytes each, lane l chunk
-    // (l & 7) ^ (row & 7) of row l >> 3 (the fragment reads then touch every
-    // bank once); a last stage of one group leaves its upper half unset ---
-    const int chunk = (lane & 7) ^ (lane >> 3);
-    const int wvoff = (lane >> 3) * rowbytes + chunk * 16;
+    // --- the copies of this wave: RPC rows of SB bytes each, lane l chunk
+    // (l % LPR) ^ row of row l / LPR (the fragment reads then touch every bank
+    // once); groups that K does not have stay out ---
+    const int lrow = RPC * wave + lane / LPR;
+    const int chunk = (lane % LPR) ^ (lrow & KEY);
+    const int wvoff = (lane / LPR) * rowbytes + chunk * 16;
     const uint8_t* wsrc[WCOPIES];
     uint32_t wbytes[WCOPIES];
 #pragma unroll
     for (int j = 0; j < WCOPIES; ++j) {
-        const int row = weight_row(8 * (j * WAVES + wave));
+        const int row = weight_row(RPC * (j * WAVES + wave));
         wsrc[j] = qw + (int64_t)row * rowbytes;
-        wbytes[j] = __builtin_amdgcn_readfirstlane(row < a.N ? 8 * rowbytes : 0);
+        wbytes[j] = __builtin_amdgcn_readfirstlane(row < a.N ? RPC * rowbytes : 0);
     }
+    auto copy_w = [&](uint8_t* dst, int t) {
+        const bool out = t * GS + chunk / 4 >= G;
+#pragma unroll
+        for (int j = 0; j < WCOPIES; ++j)
+            copy16(wsrc[j], wbytes[j], dst + (j * WAVES + wave) * 1024, out ? OOB : wvoff, t * SB);
+    };
+    copy_w(buf0, 0);      // (before the rows are looked up: their way is longer)
     int xvoff[XCOPIES];
 #pragma unroll
     for (int j = 0; j < XCOPIES; ++j) {
-        const int r = act_row(8 * (j * WAVES + wave) + (lane >> 3));
+        const int r = act_row(RPC * (j * WAVES + wave) + lane / LPR);
         xvoff[j] = r < 0 ? OOB : r * rowbytes + chunk * 16;
     }
-    // scale copies: copy s = 2 (WS + XS) rows of 64 values: group s & 1
+    // scale copies: of 64 rows and one group each; copy c is of group c % GS
     int svoff[SCOPIES];
 #pragma unroll
     for (int j = 0; j < SCOPIES; ++j) {
-        const int s = (j * WAVES + wave) >> 1;
+        const int s = (j * WAVES + wave) / GS;
         int r;
         if (s < WS) {
             r = weight_row(64 * s + lane);
@@ -182,29 +195,25 @@ __global__ __launch_bounds__(WN* WM * 64, WPS) void experts_tile_kernel(ExpertsP
         svoff[j] = r < 0 ? OOB : r * G * 4;
     }
     const uint32_t xbytes = (uint32_t)(base_rows * rowbytes), sxbytes = (uint32_t)(base_rows * G * 4);
-    auto copy = [&](uint8_t* dst, int t) {
-        const bool one = 2 * t + 1 >= G;                       // the stage's second group does not exist
-        const bool skip = one && chunk >= 4;
-#pragma unroll
-        for (int j = 0; j < WCOPIES; ++j)
-            copy16(wsrc[j], wbytes[j], dst + (j * WAVES + wave) * 1024, skip ? OOB : wvoff, t * SB);
+    auto copy_x = [&](uint8_t* dst, int t) {
+        const bool out = t * GS + chunk / 4 >= G;
 #pragma unroll
         for (int j = 0; j < XCOPIES; ++j)
-            if (j * WAVES + wave < BM / 8)
-                copy16(qx, xbytes, dst + BN * SB + (j * WAVES + wave) * 1024, skip ? OOB : xvoff[j], t * SB);
+            if (j * WAVES + wave < BM / RPC)
+                copy16(qx, xbytes, dst + BN * SB + (j * WAVES + wave) * 1024, out ? OOB : xvoff[j], t * SB);
 #pragma unroll
         for (int j = 0; j < SCOPIES; ++j) {
-            const int c = j * WAVES + wave, s = c >> 1, g = c & 1;
+            const int c = j * WAVES + wave, s = c / GS, g = c % GS;
             if (s < WS + XS)
                 copy4(s < WS ? sw : sx, s < WS ? (uint32_t)a.N * G * 4 : sxbytes,
-                      dst + DATA + (g * (WS + XS) + s) * 256, one && g ? OOB : svoff[j], (2 * t + g) * 4);
+                      dst + DATA + (g * (WS + XS) + s) * 256, t * GS + g >= G ? OOB : svoff[j], (t * GS + g) * 4);
         }
     };
 
-    const int row = lane & 15, kg = lane >> 4, key = row & 7;
-    int foff[2];
+    const int row = lane & 15, kg = lane >> 4, key = row & KEY;
+    int foff[GS];
 #pragma unroll
-    for (int g = 0; g < 2; ++g) foff[g] = row * SB + ((4 * g + kg) ^ key) * 16;
+    for (int g = 0; g < GS; ++g) foff[g] = row * SB + ((4 * g + kg) ^ key) * 16;
 
     v4f acc[MT][NT];
 #pragma unroll
@@ -212,11 +221,12 @@ __global__ __launch_bounds__(WN* WM * 64, WPS) void experts_tile_kernel(ExpertsP
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j] = v4f{};
 
-    auto compute = [&](const uint8_t* b, auto&& issue) {
+    auto compute = [&](const uint8_t* b, int t, auto&& issue) {
         const uint8_t* wb = b + wn * NT * 16 * SB;
         const uint8_t* xb = b + (BN + wm * MT * 16) * SB;
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
+        for (int g = 0; g < GS; ++g) {
+            if (g > 0 && t * GS + g >= G) break;
             const float* scales = reinterpret_cast<const float*>(b + DATA + g * (WS + XS) * 256);
             const float* sws = scales + wn * NT * 16 + 4 * kg;
             const float* sas = scales + 64 * WS + wm * MT * 16 + row;
@@ -259,14 +269,18 @@ __global__ __launch_bounds__(WN* WM * 64, WPS) void experts_tile_kernel(ExpertsP
         }
     };
 
-    copy(buf0, 0);
+    copy_x(buf0, 0);
     for (int t0 = 0; t0 < stages; t0 += 2) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int t = t0 + h;
             if (t >= stages) break;
             stage_barrier();
-            compute(h ? buf1 : buf0, [&]() { copy(h ? buf0 : buf1, t + 1 < stages ? t + 1 : 0); });
+            // (past the last stage: the first again, into a buffer that is not read)
+            compute(h ? buf1 : buf0, t, [&]() {
+                copy_w(h ? buf0 : buf1, t + 1 < stages ? t + 1 : 0);
+                copy_x(h ? buf0 : buf1, t + 1 < stages ? t + 1 : 0);
+            });
         }
     }
     stage_barrier();      // the copies in flight land before the workgroup ends
@@ -300,15 +314,15 @@ __global__ __launch_bounds__(WN* WM * 64, WPS) void experts_tile_kernel(ExpertsP
     }
 }
 
-template <int WN, int WM, int NT, int MT, int WPS>
+template <int WN, int WM, int NT, int MT, int WPS, int SB>
 void launch_shape(const ExpertsProduct& a, bool up, int64_t R, hipStream_t stream)
 {
     constexpr int BN = WN * NT * 16, BM = WM * MT * 16;
     // at most this many row tiles: a partial one per expert with rows
     const int64_t tiles_m = R / BM + (R < a.E ? R : a.E);
     const unsigned grid = (unsigned)(tiles_m * ((a.N + BN - 1) / BN));
-    if (up) experts_tile_kernel<true, WN, WM, NT, MT, WPS><<<grid, WN * WM * 64, 0, stream>>>(a);
-    else experts_tile_kernel<false, WN, WM, NT, MT, WPS><<<grid, WN * WM * 64, 0, stream>>>(a);
+    if (up) experts_tile_kernel<true, WN, WM, NT, MT, WPS, SB><<<grid, WN * WM * 64, 0, stream>>>(a);
+    else experts_tile_kernel<false, WN, WM, NT, MT, WPS, SB><<<grid, WN * WM * 64, 0, stream>>>(a);
 }
 
 }  // namespace
@@ -321,10 +335,10 @@ void launch_experts_tiled(const ExpertsProduct& a, bool up, int64_t R, hipStream
 #else
     const int shape = mean <= 12 ? 3 : 2;
 #endif
-    if (shape == 0) launch_shape<2, 4, 8, 4, 2>(a, up, R, stream);
-    else if (shape == 1) launch_shape<2, 2, 4, 4, 2>(a, up, R, stream);
-    else if (shape == 2) launch_shape<4, 1, 2, 4, 3>(a, up, R, stream);
-    else launch_shape<4, 1, 2, 2, 3>(a, up, R, stream);
+    if (shape == 2) launch_shape<4, 1, 2, 4, 3, 128>(a, up, R, stream);
+    else if (shape == 3) launch_shape<4, 1, 2, 2, 3, 128>(a, up, R, stream);
+    else if (shape == 4) launch_shape<4, 1, 2, 1, 2, 256>(a, up, R, stream);
+    else launch_shape<4, 1, 2, 2, 2, 256>(a, up, R, stream);
 }
 
 }  // namespace apex4
