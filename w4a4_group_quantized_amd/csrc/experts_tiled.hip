@@ -12,10 +12,15 @@
 // activation row and four consecutive weight rows; the products of tile j are
 // issued beside the rescale of tile j - 1.
 //
-// What bounds it: for long runs of rows the vector ALU, which converts,
-// multiplies the scales and adds (3 instructions an output and group, 48
-// clocks of a 16x16 tile against 32 of its matrix instructions); for few rows
-// the stream of the weights.
+// What bounds it: for long runs of rows the vector ALU (99% busy at 512 rows an
+// expert, 4096 x 2816: 650 us, 1160 TOPS): it widens both operands, converts,
+// multiplies the scales and adds, 27 instructions a 16x16 tile and group, 108
+// clocks against 32 of its matrix instructions.  (The micro-scaling
+// instruction, with the weights split into two 2-bit E2M1 operands and the
+// activations as E2M3, returns the same sums in fp32 for 27% fewer vector
+// instructions, but its 96-byte groups cost more in copies and LDS than that:
+// 725 us.)  For few rows it is the stream of the weights (355 MB in 80 us, 4.4
+// TB/s, at 2.5 rows an expert).
 #include "experts.h"
 #include "internal.h"
 
@@ -26,6 +31,10 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void lds_void;
 
+constexpr int SB = 128;              // bytes of a row per stage (256 took as long at 2.5 rows an expert, with less room)
+constexpr int GS = SB / 64;          // groups per stage
+constexpr int LPR = SB / 16, RPC = 64 / LPR;   // lanes per row, rows per 1 KB copy
+constexpr int KEY = LPR - 1;         // bits of the row that place its chunks
 constexpr int OOB = (int)0x80000000; // past every buffer: reads zeros
 
 __device__ inline __amdgpu_buffer_rsrc_t buffer_of(const void* p, uint32_t bytes)
@@ -100,23 +109,18 @@ __device__ inline bool find_tile(const int32_t* __restrict__ offsets, int E, int
 }
 
 // UP: gate and up rows in alternating tiles of 16, h out; else d out.
-// WN x WM waves, each NT tiles of 16 weight rows by MT tiles of 16 rows; SB:
-// bytes of a row per stage.
-template <bool UP, int WN, int WM, int NT, int MT, int WPS, int SB>
+// WN x WM waves, each NT tiles of 16 weight rows by MT tiles of 16 rows.
+template <bool UP, int WN, int WM, int NT, int MT, int WPS>
 __global__ __launch_bounds__(WN* WM * 64, WPS) void experts_tile_kernel(ExpertsProduct a)
 {
     constexpr int BN = WN * NT * 16, BM = WM * MT * 16, WAVES = WN * WM;
-    constexpr int GS = SB / 64;                                // groups per stage
-    constexpr int LPR = SB / 16, RPC = 64 / LPR;               // lanes per row, rows per 1 KB copy
-    constexpr int KEY = LPR - 1;                               // bits of the row that place its chunks
     constexpr int WCOPIES = BN / RPC / WAVES;                  // per wave and stage
     constexpr int XCOPIES = (BM / RPC + WAVES - 1) / WAVES;
     constexpr int WS = BN / 64, XS = (BM + 63) / 64;           // scale copies per group
     constexpr int SCOPIES = (GS * (WS + XS) + WAVES - 1) / WAVES;
     constexpr int DATA = (BN + BM) * SB;
     constexpr int STAGE = DATA + GS * 256 * (WS + XS);
-    static_assert(LPR <= 16 && RPC * WAVES % 16 == 0 && BN % (RPC * WAVES) == 0 && BN % 64 == 0 && BM % RPC == 0,
-                  "copies of the weights divide among the waves");
+    static_assert(BN % (RPC * WAVES) == 0 && BN % 64 == 0, "copies of the weights divide among the waves");
     static_assert(!UP || NT % 2 == 0, "a wave holds gate and up");
     __shared__ __attribute__((aligned(1024))) uint8_t buf0[STAGE];
     __shared__ __attribute__((aligned(1024))) uint8_t buf1[STAGE];
@@ -314,31 +318,31 @@ __global__ __launch_bounds__(WN* WM * 64, WPS) void experts_tile_kernel(ExpertsP
     }
 }
 
-template <int WN, int WM, int NT, int MT, int WPS, int SB>
+// Tiles of 128 weight rows by BM = 16 MT activation rows, 4 waves.
+template <int MT>
 void launch_shape(const ExpertsProduct& a, bool up, int64_t R, hipStream_t stream)
 {
-    constexpr int BN = WN * NT * 16, BM = WM * MT * 16;
+    constexpr int BN = 128, BM = 16 * MT;
     // at most this many row tiles: a partial one per expert with rows
     const int64_t tiles_m = R / BM + (R < a.E ? R : a.E);
     const unsigned grid = (unsigned)(tiles_m * ((a.N + BN - 1) / BN));
-    if (up) experts_tile_kernel<true, WN, WM, NT, MT, WPS, SB><<<grid, WN * WM * 64, 0, stream>>>(a);
-    else experts_tile_kernel<false, WN, WM, NT, MT, WPS, SB><<<grid, WN * WM * 64, 0, stream>>>(a);
+    if (up) experts_tile_kernel<true, 4, 1, 2, MT, 3><<<grid, 256, 0, stream>>>(a);
+    else experts_tile_kernel<false, 4, 1, 2, MT, 3><<<grid, 256, 0, stream>>>(a);
 }
 
 }  // namespace
 
+// Three workgroups a CU in both shapes.  64 rows from a mean of 12 rows an
+// expert on (hidden 4096, 1408 between): with 64 experts, 16 rows each 106 us
+// for gate and up against 116 of 32-row tiles, 512 rows each 650 against 790;
+// 2.5 rows each 94 against 80.  Tiles of 128 x 128 and 256 x 256 were slower at
+// every size (512 rows: 660 and 800), with fewer waves a SIMD to fill the
+// vector ALU.
 void launch_experts_tiled(const ExpertsProduct& a, bool up, int64_t R, hipStream_t stream)
 {
     const int64_t mean = R / (R < a.E ? R : a.E);
-#ifdef EXPERTS_SHAPE
-    const int shape = EXPERTS_SHAPE;
-#else
-    const int shape = mean <= 12 ? 3 : 2;
-#endif
-    if (shape == 2) launch_shape<4, 1, 2, 4, 3, 128>(a, up, R, stream);
-    else if (shape == 3) launch_shape<4, 1, 2, 2, 3, 128>(a, up, R, stream);
-    else if (shape == 4) launch_shape<4, 1, 2, 1, 2, 256>(a, up, R, stream);
-    else launch_shape<4, 1, 2, 2, 2, 256>(a, up, R, stream);
+    if (mean > 12) launch_shape<4>(a, up, R, stream);
+    else launch_shape<2>(a, up, R, stream);
 }
 
 }  // namespace apex4
