@@ -348,9 +348,9 @@ apex4_status apex4_select_granularity(int64_t M, int64_t N, int64_t K, double mi
  * are live; without a bias the sum of the two best scores, or the best
  * logit), and only the experts of the topk_group best groups can be chosen.
  * The k experts with the largest keys are chosen, in descending order; equal
- * keys, and equal groups, go to the lowest index.  An expert whose logit or
- * key is -inf or NaN is masked: it takes no part in the softmax and is not
- * chosen.  A place without a live expert left gets id -1 and gate 0 (a row of
+ * keys, and equal groups, go to the lowest index.  An expert whose logit is
+ * -inf or NaN takes no part in the softmax; one whose logit or key is -inf or
+ * NaN is masked: it is not chosen.  A place without a live expert left gets id -1 and gate 0 (a row of
  * padding with all logits -inf routes nowhere; apex4_experts_w4a4 does no
  * work for such places).  A logit of +inf counts as the largest fp32 number.
  *     gates[m,j] = scale * p[m, ids[m,j]], divided by the sum of the chosen
@@ -360,7 +360,7 @@ apex4_status apex4_select_granularity(int64_t M, int64_t N, int64_t K, double mi
  * bits.
  *   logits [M, E] of logits_type (APEX4_F32, APEX4_F16 or APEX4_BF16),
  *   bias [E] fp32 or NULL; ids [M, k] int32, gates [M, k] fp32 (outputs).
- *   0 <= M <= 2^26 (0: no-op), 1 <= E <= 1024, 1 <= k <= 64; n_group >= 1 divides E,
+ *   0 <= M <= 2^25 (0: no-op), 1 <= E <= 1024, 1 <= k <= 64; n_group >= 1 divides E,
  *   n_group <= 64, 1 <= topk_group <= n_group, k <= topk_group * E / n_group,
  *   group_top 1 or 2; score APEX4_SCORE_SOFTMAX or APEX4_SCORE_SIGMOID; scale
  *   finite.  Pointers aligned to their elements.  Asynchronous on `stream`.
@@ -376,11 +376,13 @@ apex4_status apex4_route(const void* logits, int32_t logits_type, int64_t M, int
  *         [g; u] = W4A4(x[m], gate_up[e])             (I gate rows, then I up rows)
  *         h      = fp16(silu(g) * u), kept within +-65504, silu(g) = g / (1 + exp(-g))
  *         d      = W4A4(h, down[e])
- *     y[m] = sum over j of gates[m,j] * d             (fp32, j ascending; then fp16)
+ *     y[m] = sum over j of gates[m,j] * d             (fp32; then fp16)
  * g, u and d are fp32 sums and are not rounded.  A slot with another id (-1
  * of apex4_route, an expert that lives elsewhere) costs no product and adds
  * nothing, whatever its gate; a token without a slot gets zeros.  A token may
- * name an expert more than once.
+ * name an expert more than once.  A token's result depends on its own slots
+ * only: infinities or NaN in other tokens, or in the scales of experts that it
+ * does not name, leave it as it is.
  *   x_f16 [M, H] fp16, 16-byte aligned;  ids [M, k] int32, gates [M, k] fp32.
  *   qw_gate_up [E, 2I, H/2] and s_gate_up [E, 2I, H/128], qw_down [E, H, I/2]
  *   and s_down [E, H, I/128]: apex4_pack_weight outputs with group 128 (of the
@@ -395,8 +397,8 @@ apex4_status apex4_route(const void* logits, int32_t logits_type, int64_t M, int
  *   M >= 0 (0: no-op), 1 <= k <= 64, 1 <= E <= 1024, H and I positive
  *   multiples of 128, M * k < 2^31, M * k * I < 2^34,
  *   2 * I * H < 2^32, (M + k) * H < 2^32.
- * The results do not depend on timing: no atomics, every sum in a fixed
- * order.  Asynchronous on `stream`; every check runs on the host before
+ * The results do not depend on timing: no atomics, every sum in an order that
+ * the sizes and the ids fix.  Asynchronous on `stream`; every check runs on the host before
  * anything is launched.
  */
 size_t apex4_experts_workspace_size(int64_t M, int32_t k, int64_t E, int64_t H, int64_t I, int32_t group);
@@ -410,9 +412,11 @@ apex4_status apex4_experts_w4a4(const void* x_f16, const int32_t* ids, const flo
  * row and 128 columns of the activations, one per 128 x 128 of the weights.
  *     s = max|v| / 448 over the block (fp32, correctly rounded)
  *     q = e4m3(clamp(v / s, -448, 448)), round to nearest even of the
- *         correctly rounded fp32 quotient;  s == 0 gives q = 0
+ *         correctly rounded fp32 quotient;  s == 0 gives q = 0;  max passes
+ *         over NaN, and a NaN's code is NaN, as is an infinity's (its s is
+ *         infinite), so that both make the products they take part in NaN
  *     y[m,n] = sum_j s_a[m,j] * s_w[n/128, j] * sum_{k in block j} qa[m,k] * qw[n,k]
- * with an fp32 sum over the blocks, in no fixed order of the additions.  The
+ * with an fp32 sum over the blocks, in an order that the sizes fix.  The
  * sum of a block comes from the FP8 matrix instruction, which adds 8
  * neighbouring products aligned to the largest of them, cut below 2^-13 of
  * it, and those sums in fp32.  These are 8-bit values of their own, unlike the INT4 codes
@@ -438,7 +442,8 @@ apex4_status apex4_pack_weight_e4m3(const void* w, int32_t w_type, int64_t N, in
  *   workspace: at least apex4_gemm_e4m3_workspace_size() bytes (NULL allowed
  *   when that is 0), 16-byte aligned, caller-owned, overwritten; calls that
  *   share one workspace race.
- *   0 <= M, N <= 2^26 (either 0: no-op), 0 < K < 2^23, K % 128 == 0, M * K and N * K < 2^34.
+ *   0 <= M, N <= 2^26 (either 0: no-op), 0 < K < 2^23, K % 128 == 0, M * K and N * K < 2^34,
+ *   M * N < 2^37.
  *
  * apex4_linear_e4m3: apex4_quantize_e4m3(x) into the workspace, then
  * apex4_gemm_e4m3, with the bits of those two calls; y has the type of x.  Up

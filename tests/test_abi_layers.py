@@ -130,3 +130,12 @@ def test_plain_implementations_agree_with_each_other():
     q, s = ref.int4(np.array([[7.0, 0.5, 1.5, -7.0] + [0.0] * 124], dtype=np.float16))
     assert s[0, 0] == 1.0 and q[0, :4].tolist() == [7, 0, 2, -7]
     assert ref.pack(np.array([[1, -1, 7, -8]])).tolist() == [[0xF1, 0x87]]
+
+
+def test_sizes_past_the_launch_limits_are_refused(L):
+    assert route(L, M=(1 << 25) + 1) == INVALID
+    M, N = 1 << 20, 1 << 17
+    assert L.apex4_gemm_e4m3_workspace_size(M, N, 128) == 0
+    assert L.apex4_linear_e4m3_workspace_size(M, N, 128) == 0
+    assert L.apex4_gemm_e4m3(None, None, None, None, M, N, 128, 1, None, None, None, 0, None) == INVALID
+    assert L.apex4_linear_e4m3(None, 1, None, None, M, N, 128, None, None, None, 0, None) == INVALID

@@ -18,6 +18,9 @@ constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 // threads along a dimension (8 elements, or 64 threads a row)
 constexpr uint64_t kMaxElements = uint64_t(1) << 34;
 constexpr int64_t kMaxRows = int64_t(1) << 26;
+constexpr int64_t kMaxTokens = int64_t(1) << 25;   // of apex4_route: 64 threads each, rounded up to four
+// outputs of an 8-bit product: more do not fit the memory, and tiles are counted in 32 bits
+constexpr uint64_t kMaxOutputs = uint64_t(1) << 37;
 
 apex4_status to_status(hipError_t e) { return e == hipSuccess ? APEX4_OK : APEX4_ERR_HIP; }
 
@@ -39,6 +42,7 @@ bool experts_sizes(int64_t M, int32_t k, int64_t E, int64_t H, int64_t I)
 bool e4m3_sizes(int64_t M, int64_t N, int64_t K)
 {
     if (M < 0 || N < 0 || M > kMaxRows || N > kMaxRows || K <= 0 || K % 128 != 0 || K >= (int64_t(1) << 23)) return false;
+    if ((uint64_t)M * N >= kMaxOutputs) return false;
     return (uint64_t)M * K < kMaxElements && (uint64_t)N * K < kMaxElements;
 }
 
@@ -69,7 +73,7 @@ apex4_status apex4_route(const void* logits, int32_t logits_type, int64_t M, int
                          const float* bias, int32_t n_group, int32_t topk_group, int32_t group_top, int32_t k,
                          int32_t renormalize, float scale, int32_t* ids, float* gates, void* stream)
 {
-    if (M < 0 || M > kMaxRows || E < 1 || E > 1024 || k < 1 || k > 64) return APEX4_ERR_INVALID_ARG;
+    if (M < 0 || M > kMaxTokens || E < 1 || E > 1024 || k < 1 || k > 64) return APEX4_ERR_INVALID_ARG;
     if (n_group < 1 || n_group > 64 || E % n_group != 0 || topk_group < 1 || topk_group > n_group)
         return APEX4_ERR_INVALID_ARG;
     if (k > topk_group * (E / n_group) || (group_top != 1 && group_top != 2) || !std::isfinite(scale))

@@ -57,11 +57,16 @@ __device__ inline float absmax(const Eight& e)
 // The codes of 8 values: the correctly rounded fp32 quotient by the scale, kept
 // within the largest E4M3 number (a scale that is a subnormal number may be
 // rounded down so far that the quotient is above it), rounded to nearest even.
+// A NaN, and an infinity by its infinite scale, stays a NaN (the comparison is
+// false for it); in a block of zeros s is 0 and the value itself says which.
 __device__ inline uint2 codes8(const Eight& e, float s)
 {
     float q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = s > 0.0f ? fminf(fmaxf(e.v[i] / s, -448.0f), 448.0f) : 0.0f;
+    for (int i = 0; i < 8; ++i) {
+        const float v = s > 0.0f ? e.v[i] / s : e.v[i] + 0.0f;
+        q[i] = fabsf(v) > 448.0f ? copysignf(448.0f, v) : v;
+    }
     int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
     lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
     int hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);

@@ -18,7 +18,7 @@
 //   - the scores' exp and reciprocal are written out (a sigmoid in 64 bits is
 //     about 26 instructions here, over 60 from the library);
 //   - lane moves are DPP (moves through LDS, 130 a row, were two thirds of the
-//     first kernel's 38 us);
+//     first kernel's 38 us; the row takes 29 now);
 //   - a round of "largest key of the wave" runs on 32 bits: the keys rounded to
 //     fp32, in the order of the numbers.  Rounding keeps the order, so the
 //     largest key is among the lanes that hold the largest rounded one; only
@@ -174,8 +174,8 @@ struct Row {
 // score cancels for large |x|; the sum of a softmax within 1e-6; one rounding
 // by the bias), and `sure` says whether no two keys that decide were nearer to
 // each other than four times that.  If some were, the caller asks again in 64
-// bits: about one row in a few hundred, where all of them in 64 bits took 44 us
-// instead of 22 (16384 rows of 256 experts in 8 groups).
+// bits: about one row in a few hundred, where all of them in 64 bits took 41 us
+// instead of 29 (16384 rows of 256 experts in 8 groups).
 template <int V, bool WIDE, int GROUPS, typename T>
 __device__ inline int choose(const RouteArgs& a, int64_t row, const float (&x)[V], const Row& of, T* values, bool& sure)
 {
