@@ -59,6 +59,7 @@ Parts parts_of(void* ws, int64_t M, int32_t k, int32_t E, int32_t H, int32_t I)
 // them again to place its own; the ids stay in L2.  Each wave takes a
 // contiguous run of slots, so that only the waves' counts cross the barrier.
 constexpr int PLAN_WAVES = 16;
+constexpr int PLAN_READS = 8;   // ids a lane asks for together
 // The workgroups past the experts quantize x meanwhile (the rule of
 // apex4_quantize_act, a chunk of 8 values a thread).
 __global__ __launch_bounds__(64 * PLAN_WAVES) void plan_kernel(const int32_t* __restrict__ ids, int32_t R, int32_t E,
@@ -84,12 +85,19 @@ __global__ __launch_bounds__(64 * PLAN_WAVES) void plan_kernel(const int32_t* __
     const int64_t first = (int64_t)wave * per;
     const int last = (int)min((int64_t)R, first + per);
     int lt = 0, eq = 0;
-    for (int64_t s = first + lane; s < last; s += 64) {
-        const int id = ids[s];
-        lt += id >= 0 && id < e;
-        eq += id == e;
-        // slots without an expert: one workgroup says so
-        if (e == 0 && (id < 0 || id >= E)) place[s] = -1;
+    for (int64_t s0 = first + lane; s0 < last; s0 += 64 * PLAN_READS) {
+        int id[PLAN_READS];
+#pragma unroll
+        for (int i = 0; i < PLAN_READS; ++i) id[i] = ids[min(s0 + 64 * i, (int64_t)R - 1)];
+#pragma unroll
+        for (int i = 0; i < PLAN_READS; ++i) {
+            const int64_t s = s0 + 64 * i;
+            const bool in = s < last;
+            lt += in && id[i] >= 0 && id[i] < e;
+            eq += in && id[i] == e;
+            // slots without an expert: one workgroup says so
+            if (in && e == 0 && (id[i] < 0 || id[i] >= E)) place[s] = -1;
+        }
     }
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) {
@@ -112,16 +120,22 @@ __global__ __launch_bounds__(64 * PLAN_WAVES) void plan_kernel(const int32_t* __
         if (e == E - 1) offsets[E] = row + count;
     }
     if (equal[wave] == 0) return;
-    for (int64_t s0 = first; s0 < last; s0 += 64) {
-        const int64_t s = s0 + lane;
-        const bool mine = s < last && ids[s] == e;
-        const uint64_t who = __ballot(mine);
-        if (mine) {
-            const int r = row + __popcll(who & ((1ull << lane) - 1));
-            order[r] = (int)s;
-            place[s] = r;
+    for (int64_t s0 = first + lane; s0 - lane < last; s0 += 64 * PLAN_READS) {
+        int id[PLAN_READS];
+#pragma unroll
+        for (int i = 0; i < PLAN_READS; ++i) id[i] = ids[min(s0 + 64 * i, (int64_t)R - 1)];
+#pragma unroll
+        for (int i = 0; i < PLAN_READS; ++i) {
+            const int64_t s = s0 + 64 * i;
+            const bool mine = s < last && id[i] == e;
+            const uint64_t who = __ballot(mine);
+            if (mine) {
+                const int r = row + __popcll(who & ((1ull << lane) - 1));
+                order[r] = (int)s;
+                place[s] = r;
+            }
+            row += __popcll(who);
         }
-        row += __popcll(who);
     }
 }
 
