@@ -119,6 +119,20 @@ def test_the_same_expert_several_times(dev, M):
     assert torch.equal(y, y32.half())
 
 
+@pytest.mark.parametrize("M,E,k,H,I", [(40, 2, 1, 128, 2048), (70, 3, 3, 256, 2176), (20, 4, 2, 384, 4096)])
+def test_experts_whose_down_products_run_in_parts(dev, M, E, k, H, I):
+    w, gu, down = experts_on(dev, E, H, I, 6)
+    x = inputs.activations(np.random.default_rng(M), M, H, "outlier", M)
+    rng = np.random.default_rng(9)
+    ids = rng.integers(-1, E + 1, (M, k)).astype(np.int32)
+    gates = rng.uniform(-1.0, 1.0, (M, k)).astype(np.float32)
+    args = [torch.from_numpy(t).to(dev) for t in (x, ids, gates)]
+    y, y32 = apex4.experts(*args, *w, want_y32=True)
+    want, bound = ref.experts(x, ids, gates, gu, down)
+    assert np.all(np.abs(y32.cpu().numpy().astype(np.float64) - want) <= bound)
+    assert torch.equal(y, y32.half()) and torch.equal(apex4.experts(*args, *w), y)
+
+
 @pytest.mark.parametrize("M", [2, 20, 300])
 @pytest.mark.parametrize("N", [64, 129])
 def test_e4m3_outputs_at_any_address(dev, M, N):

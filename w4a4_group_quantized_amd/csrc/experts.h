@@ -19,7 +19,9 @@ struct ExpertsProduct {
     int64_t rows;             // tokens
     int32_t k, E, N, K;
     _Float16* h;              // gate and up: [R, N/2]
-    float* d;                 // down: [R, N]
+    float* d;                 // down: [parts, R, N]
+    int32_t parts;            // K in this many parts (gate and up: 1)
+    int64_t part_stride;      // R N
 };
 
 // silu(g) u, kept within fp16
@@ -32,6 +34,9 @@ __device__ inline _Float16 experts_h(float g, float u)
 // A few tokens (experts_token.hip): the whole network in two launches; h: [R, I].
 bool experts_token_supports(const ExpertsProblem& p);
 hipError_t launch_experts_token(const ExpertsProblem& p, _Float16* h, hipStream_t stream);
+
+// K parts of the down product
+int experts_parts(int64_t R, int32_t E, int32_t H, int32_t I);
 
 void launch_experts_tiled(const ExpertsProduct& a, bool up, int64_t R, hipStream_t stream);
 

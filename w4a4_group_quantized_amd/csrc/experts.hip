@@ -25,7 +25,8 @@ struct Parts {
     _Float16* h;         // [R, I]
     uint8_t* hq;         // [R, I/2]
     float* hs;           // [R, I/128]
-    float* d;            // [R, H]
+    float* d;            // [parts, R, H], the down product's K parts
+    int parts;
     size_t bytes;
 };
 
@@ -48,7 +49,8 @@ Parts parts_of(void* ws, int64_t M, int32_t k, int32_t E, int32_t H, int32_t I)
     w.h = reinterpret_cast<_Float16*>(take((size_t)R * I * 2));
     w.hq = take((size_t)R * (I / 2));
     w.hs = reinterpret_cast<float*>(take((size_t)R * (I / 128) * 4));
-    w.d = reinterpret_cast<float*>(take((size_t)R * H * 4));
+    w.parts = experts_parts(R, E, H, I);
+    w.d = reinterpret_cast<float*>(take((size_t)w.parts * R * H * 4));
     w.bytes = at;
     return w;
 }
@@ -139,9 +141,11 @@ __global__ __launch_bounds__(64 * PLAN_WAVES) void plan_kernel(const int32_t* __
     }
 }
 
-// y = the sum of a token's slots, in slot order, one rounding to fp16 at the end.
+// y = the sum of a token's slots, in slot order, of each slot's K parts, in
+// their order; one rounding to fp16 at the end.
 __global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ d, const int32_t* __restrict__ place,
                                                       const float* __restrict__ gates, int32_t k, int32_t H,
+                                                      int32_t parts, int64_t part_stride,
                                                       int64_t n4, _Float16* __restrict__ y16, float* __restrict__ y32)
 {
     const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -164,6 +168,10 @@ __global__ __launch_bounds__(256) void combine_kernel(const float* __restrict__ 
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             v[j] = r[j] >= 0 ? *reinterpret_cast<const v4f*>(d + (int64_t)r[j] * H + c) : v4f{};
+        for (int p = 1; p < parts; ++p)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (r[j] >= 0) v[j] += *reinterpret_cast<const v4f*>(d + p * part_stride + (int64_t)r[j] * H + c);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -211,6 +219,7 @@ hipError_t launch_experts(const ExpertsProblem& p, hipStream_t stream)
     a.K = p.H;
     a.h = w.h;
     a.rows = p.M;
+    a.parts = 1;
     launch_experts_tiled(a, true, R, stream);
     const hipError_t e = launch_quantize(w.h, R, p.I, 128, w.hq, w.hs, stream);
     if (e != hipSuccess) return e;
@@ -221,9 +230,12 @@ hipError_t launch_experts(const ExpertsProblem& p, hipStream_t stream)
     a.N = p.H;
     a.K = p.I;
     a.d = w.d;
+    a.parts = w.parts;
+    a.part_stride = (int64_t)R * p.H;
     launch_experts_tiled(a, false, R, stream);
     const int64_t n4 = p.M * (p.H / 4);
-    combine_kernel<<<(unsigned)((n4 + 255) / 256), 256, 0, stream>>>(w.d, w.place, p.gates, p.k, p.H, n4,
+    combine_kernel<<<(unsigned)((n4 + 255) / 256), 256, 0, stream>>>(w.d, w.place, p.gates, p.k, p.H, w.parts,
+                                                                     (int64_t)R * p.H, n4,
                                                                      static_cast<_Float16*>(p.y16), p.y32);
     return hipGetLastError();
 }

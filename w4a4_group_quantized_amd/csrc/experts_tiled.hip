@@ -14,8 +14,11 @@
 //
 // What bounds it: for long runs of rows the vector ALU (99% busy at 512 rows an
 // expert, 4096 x 2816: 650 us, 1160 TOPS): it widens both operands, converts,
-// multiplies the scales and adds, 27 instructions a 16x16 tile and group, 108
-// clocks against 32 of its matrix instructions.  (The micro-scaling
+// multiplies the scales and adds, 25 instructions a 16x16 tile and group (12
+// of them the rescale, 9 the widening), 100 clocks against 32 of its matrix
+// instructions.  (Scale products from the fp32 matrix instruction: 758 us, it
+// does not run beside the vector ALU.  Activations stored as bytes, which
+// leaves 6 of the 9 out: 672 and 710 us, twice the bytes to copy.  The micro-scaling
 // instruction, with the weights split into two 2-bit E2M1 operands and the
 // activations as E2M3, returns the same sums in fp32 for 27% fewer vector
 // instructions, but its 96-byte groups cost more in copies and LDS than that:
@@ -132,6 +135,9 @@ __global__ __launch_bounds__(WN* WM * 64, WPS) void experts_tile_kernel(ExpertsP
     int unit = blockIdx.x;
     const int per = (int)gridDim.x >> 3;
     if (unit < per * 8) unit = (unit & 7) * per + (unit >> 3);
+    // (UP: one part)
+    const int units = UP ? (int)gridDim.x : (int)gridDim.x / a.parts, kpart = UP ? 0 : unit / units;
+    if (!UP) unit -= kpart * units;
     int e, first, count, mt, nt;
     if (!find_tile(a.offsets, a.E, (a.N + BN - 1) / BN, BM, unit, e, first, count, mt, nt)) return;
     e = __builtin_amdgcn_readfirstlane(e);
@@ -139,7 +145,8 @@ __global__ __launch_bounds__(WN* WM * 64, WPS) void experts_tile_kernel(ExpertsP
     count = __builtin_amdgcn_readfirstlane(count);
     const int m0 = __builtin_amdgcn_readfirstlane(mt) * BM, n0 = __builtin_amdgcn_readfirstlane(nt) * BN;
     const int rowbytes = a.K / 2, G = a.K / 128, half = a.N / 2;
-    const int stages = (G + GS - 1) / GS;
+    const int all = (G + GS - 1) / GS;
+    const int s0 = UP ? 0 : kpart * all / a.parts, stages = UP ? all : (kpart + 1) * all / a.parts - s0;
     const uint8_t* qw = a.qw + (int64_t)e * a.N * rowbytes;
     const float* sw = a.sw + (int64_t)e * a.N * G;
     // weight row of row r of the tile (a.N and more: none)
@@ -172,6 +179,7 @@ __global__ __launch_bounds__(WN* WM * 64, WPS) void experts_tile_kernel(ExpertsP
         wbytes[j] = __builtin_amdgcn_readfirstlane(row < a.N ? RPC * rowbytes : 0);
     }
     auto copy_w = [&](uint8_t* dst, int t) {
+        t += s0;
         const bool out = t * GS + chunk / 4 >= G;
 #pragma unroll
         for (int j = 0; j < WCOPIES; ++j)
@@ -200,6 +208,7 @@ __global__ __launch_bounds__(WN* WM * 64, WPS) void experts_tile_kernel(ExpertsP
     }
     const uint32_t xbytes = (uint32_t)(base_rows * rowbytes), sxbytes = (uint32_t)(base_rows * G * 4);
     auto copy_x = [&](uint8_t* dst, int t) {
+        t += s0;
         const bool out = t * GS + chunk / 4 >= G;
 #pragma unroll
         for (int j = 0; j < XCOPIES; ++j)
@@ -230,7 +239,7 @@ __global__ __launch_bounds__(WN* WM * 64, WPS) void experts_tile_kernel(ExpertsP
         const uint8_t* xb = b + (BN + wm * MT * 16) * SB;
 #pragma unroll
         for (int g = 0; g < GS; ++g) {
-            if (g > 0 && t * GS + g >= G) break;
+            if (g > 0 && (s0 + t) * GS + g >= G) break;
             const float* scales = reinterpret_cast<const float*>(b + DATA + g * (WS + XS) * 256);
             const float* sws = scales + wn * NT * 16 + 4 * kg;
             const float* sas = scales + 64 * WS + wm * MT * 16 + row;
@@ -312,36 +321,52 @@ __global__ __launch_bounds__(WN* WM * 64, WPS) void experts_tile_kernel(ExpertsP
             for (int j = 0; j < NT; ++j) {
                 const int n = n0 + (wn * NT + j) * 16 + 4 * kg;
                 if (n < a.N)
-                    *reinterpret_cast<v4f*>(a.d + (int64_t)(first + m) * a.N + n) = acc[i][j] * 0.00390625f;
+                    *reinterpret_cast<v4f*>(a.d + kpart * a.part_stride + (int64_t)(first + m) * a.N + n) = acc[i][j] * 0.00390625f;
             }
         }
     }
 }
 
-// Tiles of 128 weight rows by BM = 16 MT activation rows, 4 waves.
+constexpr int BN = 128;      // weight rows of a tile
+
+// at most this many tiles of rows: a partial one per expert with rows
+int64_t row_tiles(int64_t R, int32_t E, int bm) { return R / bm + (R < E ? R : E); }
+
+// Three workgroups a CU in both shapes.  64 rows from a mean of 12 rows an
+// expert on (hidden 4096, 1408 between): with 64 experts, 16 rows each 106 us
+// for gate and up against 116 of 32-row tiles, 512 rows each 650 against 790;
+// 2.5 rows each 94 against 80.  48 rows took as long or longer but for one
+// size (301 tokens, 2 of 8 experts, 4096 x 11008: 317 us a call against 329;
+// 512 rows each 1263 against 1186).  Tiles of 128 x 128 and 256 x 256 were
+// slower at every size (512 rows: 660 and 800), with fewer waves a SIMD to
+// fill the vector ALU.
+bool tall_tiles(int64_t R, int32_t E) { return R / (R < E ? R : E) > 12; }
+
+// Tiles of 128 weight rows by 16 MT activation rows, 4 waves.
 template <int MT>
 void launch_shape(const ExpertsProduct& a, bool up, int64_t R, hipStream_t stream)
 {
-    constexpr int BN = 128, BM = 16 * MT;
-    // at most this many row tiles: a partial one per expert with rows
-    const int64_t tiles_m = R / BM + (R < a.E ? R : a.E);
-    const unsigned grid = (unsigned)(tiles_m * ((a.N + BN - 1) / BN));
+    const unsigned grid = (unsigned)(row_tiles(R, a.E, 16 * MT) * ((a.N + BN - 1) / BN)) * a.parts;
     if (up) experts_tile_kernel<true, 4, 1, 2, MT, 3><<<grid, 256, 0, stream>>>(a);
     else experts_tile_kernel<false, 4, 1, 2, MT, 3><<<grid, 256, 0, stream>>>(a);
 }
 
 }  // namespace
 
-// Three workgroups a CU in both shapes.  64 rows from a mean of 12 rows an
-// expert on (hidden 4096, 1408 between): with 64 experts, 16 rows each 106 us
-// for gate and up against 116 of 32-row tiles, 512 rows each 650 against 790;
-// 2.5 rows each 94 against 80.  Tiles of 128 x 128 and 256 x 256 were slower at
-// every size (512 rows: 660 and 800), with fewer waves a SIMD to fill the
-// vector ALU.
+// Two parts of K where all the tiles of the down product find room at once
+// (three a CU) and K is long: 301 tokens, 2 of 8 experts, 4096 x 11008 338 us
+// a call undivided, 329 in two parts, 325 in three; 200 tokens, 1024 x 4096 55,
+// 47 and 49.  Where they do not, the parts' sums cost more than they fill (600
+// tokens, 4 of 16 experts, 4096 x 1408: 132 and 148).
+int experts_parts(int64_t R, int32_t E, int32_t H, int32_t I)
+{
+    const int64_t units = row_tiles(R, E, tall_tiles(R, E) ? 64 : 32) * ((H + BN - 1) / BN);
+    return units <= 3 * (int64_t)cu_count() && I / 128 >= 16 ? 2 : 1;
+}
+
 void launch_experts_tiled(const ExpertsProduct& a, bool up, int64_t R, hipStream_t stream)
 {
-    const int64_t mean = R / (R < a.E ? R : a.E);
-    if (mean > 12) launch_shape<4>(a, up, R, stream);
+    if (tall_tiles(R, a.E)) launch_shape<4>(a, up, R, stream);
     else launch_shape<2>(a, up, R, stream);
 }
 
