@@ -83,18 +83,21 @@ __global__ __launch_bounds__(WN* WM * 64, WPS) void e4m3_tile_kernel(TileArgs a)
     const int wn = wave % WN, wm = wave / WN;
     const E4m3Problem& p = a.p;
 
-    // full tiles first (XCD b mod 8 walks a contiguous range of them), then
-    // the parts of the others
+    // full tiles first, then the parts of the others, part by part; XCD b mod 8
+    // walks a contiguous range of the tiles in either (with the parts' tiles in
+    // launch order each L2 fetches most of both operands: 515 x 4008 x 11008 49
+    // us instead of 41, 300 x 8192 x 8192 59 instead of 54, 256 x 4096 x 4096
+    // 14.6 and 15.8; a contiguous range of all parts' tiles 40, 54 and 21)
     const int full = a.tiles_n * a.tiles_m - a.tail;
     int lin = blockIdx.x, kpart = 0;
     const bool split = lin >= full;
     if (split) {
         kpart = (lin - full) / a.tail;
-        lin = full + (lin - full) % a.tail;
-    } else {
-        const int per = full >> 3;
-        if (lin < per * 8) lin = (lin & 7) * per + (lin >> 3);
+        lin = (lin - full) % a.tail;
     }
+    const int per = (split ? a.tail : full) >> 3;
+    if (lin < per * 8) lin = (lin & 7) * per + (lin >> 3);
+    if (split) lin += full;
     int by, bx;
     tile_coords(a, lin, by, bx);
     const int m0 = by * BM, n0 = bx * BN;
