@@ -4,10 +4,11 @@
 // rejected call touches neither the device nor the caller's memory.
 #include "apex4.h"
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
-#include "internal.h"
+#include "layers.h"
 
 namespace {
 
@@ -66,6 +67,18 @@ apex4_status check_e4m3_quantize(const void* x, int32_t type, int64_t rows, int6
 }
 
 }  // namespace
+
+int apex4::compute_units()
+{
+    // cached per device (relaxed atomics: any thread may write the same value)
+    static std::atomic<int> cache[64] = {};
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 0;
+    int n = cache[dev].load(std::memory_order_relaxed);
+    if (n == 0 && hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) == hipSuccess)
+        cache[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
 
 extern "C" {
 

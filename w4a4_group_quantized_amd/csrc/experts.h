@@ -4,7 +4,7 @@
 
 #include <cstdint>
 
-#include "internal.h"
+#include "layers.h"
 
 namespace apex4 {
 

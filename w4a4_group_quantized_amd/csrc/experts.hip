@@ -7,7 +7,7 @@
 // row of every slot and the first row of every expert), the activation codes
 // are quantized per token, and the products run per expert over its rows.
 #include "experts.h"
-#include "internal.h"
+#include "layers.h"
 #include "quant_rule.h"
 
 namespace apex4 {

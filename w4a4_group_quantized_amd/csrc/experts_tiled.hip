@@ -25,7 +25,7 @@
 // 725 us.)  For few rows it is the stream of the weights (355 MB in 80 us, 4.4
 // TB/s, at 2.5 rows an expert).
 #include "experts.h"
-#include "internal.h"
+#include "layers.h"
 
 namespace apex4 {
 namespace {
@@ -361,7 +361,7 @@ void launch_shape(const ExpertsProduct& a, bool up, int64_t R, hipStream_t strea
 int experts_parts(int64_t R, int32_t E, int32_t H, int32_t I)
 {
     const int64_t units = row_tiles(R, E, tall_tiles(R, E) ? 64 : 32) * ((H + BN - 1) / BN);
-    return units <= 3 * (int64_t)cu_count() && I / 128 >= 16 ? 2 : 1;
+    return units <= 3 * (int64_t)compute_units() && I / 128 >= 16 ? 2 : 1;
 }
 
 void launch_experts_tiled(const ExpertsProduct& a, bool up, int64_t R, hipStream_t stream)

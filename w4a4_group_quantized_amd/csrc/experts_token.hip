@@ -24,7 +24,7 @@
 // LDS: piece c (16 bytes) of a row sits at c ^ row, so that the 16 rows' reads
 // of one column touch every bank once.
 #include "experts.h"
-#include "internal.h"
+#include "layers.h"
 #include "quant_rule.h"
 
 namespace apex4 {

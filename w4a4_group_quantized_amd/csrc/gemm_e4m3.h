@@ -5,7 +5,7 @@
 
 #include <cstdint>
 
-#include "internal.h"
+#include "layers.h"
 #include "quant_rule.h"
 
 namespace apex4 {

@@ -13,7 +13,7 @@
 // fp16 and less of bf16's; widening the codes for the fp16 instruction would
 // halve the matrix rate.
 #include "gemm_e4m3.h"
-#include "internal.h"
+#include "layers.h"
 
 namespace apex4 {
 namespace {

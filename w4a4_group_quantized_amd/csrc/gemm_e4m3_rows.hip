@@ -17,7 +17,7 @@
 // lane holds one activation row m = lane & 15 and four weight rows: s_a is one
 // value per lane and block.  The four waves' sums meet in LDS, in wave order.
 #include "gemm_e4m3.h"
-#include "internal.h"
+#include "layers.h"
 
 namespace apex4 {
 namespace {

@@ -1,6 +1,6 @@
 // The 8-bit block-scaled product (apex4_gemm_e4m3) in LDS tiles on gfx950.
 #include "gemm_e4m3.h"
-#include "internal.h"
+#include "layers.h"
 
 namespace apex4 {
 namespace {
@@ -420,11 +420,11 @@ hipError_t launch_cut(const TileArgs& a, int shape, hipStream_t stream)
 
 }  // namespace
 
-size_t e4m3_tiled_workspace_bytes(const E4m3Problem& p) { return choose(p, cu_count()).bytes; }
+size_t e4m3_tiled_workspace_bytes(const E4m3Problem& p) { return choose(p, compute_units()).bytes; }
 
 hipError_t launch_e4m3_tiled(const E4m3Problem& p, hipStream_t stream)
 {
-    const Cut cut = choose(p, cu_count());
+    const Cut cut = choose(p, compute_units());
     TileArgs a{};
     a.p = p;
     a.tail = cut.tail;

@@ -969,8 +969,6 @@ void launch_pp_all(const PPArgs& t, const PingpongSplit& sp, hipStream_t stream)
 // cover 4 row blocks x 8 column blocks
 int tile_band_rows(int tiles_m) { return tiles_m < 4 ? tiles_m : 4; }
 
-}  // namespace
-
 int cu_count()
 {
     // compute units of the current device, cached per device (relaxed atomics:
@@ -985,6 +983,8 @@ int cu_count()
     }
     return n;
 }
+
+}  // namespace
 
 PingpongSplit pingpong_split(const GemmProblem& p)
 {

@@ -25,7 +25,7 @@
 //     where those are several do the 64-bit keys and the indices decide;
 //   - up to 4 values a lane are sorted once, and a round looks at each lane's
 //     first only.
-#include "internal.h"
+#include "layers.h"
 
 namespace apex4 {
 namespace {
