@@ -6,7 +6,7 @@
 // small steps around it.  The six launches of the general path (order of the
 // slots, codes of x, product, codes of h, product, sum) took 50 us for one
 // token and 8 of 64 experts (4096 x 1408; 74 MB of weights, 14 us at the rate
-// of a large copy), of which the two products were 36; this way it takes 26.5.
+// of a large copy), of which the two products were 36; this way it takes 27.
 // Here
 //   - no plan: a wave looks at the at most 64 ids itself.  An entry is an
 //     expert with the tokens that name it, one slot a token (a token that names
@@ -166,7 +166,8 @@ __device__ inline void load_chunks(half8 (&v)[NX], const half8* x, int n8, int t
 // acc[r] += sum over the item's groups of sa4(q)[r] s_w[q] P, P of activation row 4 (lane >> 4) + r and weight row
 // lane & 15.  `x`: the codes of this lane's activation row lane & 15 at the item's first byte; `left`: bytes of the
 // row from there.
-template <typename Scale>
+// APART: the item is of an entry that not every token names.
+template <bool APART, typename Scale>
 __device__ inline void item_products(v4f& acc, const uint8_t* buf, const uint8_t* x, int left, Scale sa4)
 {
     const int lane = threadIdx.x & 63, row = lane & 15, kg = lane >> 4;
@@ -196,9 +197,17 @@ __device__ inline void item_products(v4f& acc, const uint8_t* buf, const uint8_t
             if (q0 + i >= groups) break;
             const v4f s = sa4(q0 + i);
             const float sn = sw[16 * (q0 + i)];
+            float f[4];
 #pragma unroll
-            // (a scale of 0 takes nothing, also from an infinite weight scale: a token that does not name the entry)
-            for (int r = 0; r < 4; ++r) acc[r] = fmaf(s[r] != 0.0f ? s[r] * sn : 0.0f, (float)P[i][r], acc[r]);
+            for (int r = 0; r < 4; ++r) f[r] = s[r] * sn;
+            // a token that does not name the entry has the scale 0 here and takes nothing from it, also
+            // where its weight scales are no numbers (one branch a group: a choice a value took 5% of the time)
+            if (APART && __ballot(!(fabsf(sn) < __builtin_inff())) != 0) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) f[r] = s[r] != 0.0f ? f[r] : 0.0f;
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[r] = fmaf(f[r], (float)P[i][r], acc[r]);
         }
     }
 }
@@ -291,7 +300,7 @@ __global__ __launch_bounds__(UP_WAVES * 64) void token_up_kernel(TokenArgs a, _F
             const int it = i0 + b;
             wait_copies();
             if (it < items)
-                item_products(acc, (b ? buf1 : buf0) + wave * BUF, xrow + it * ITEM, rowbytes - it * ITEM, [&](int q) {
+                item_products<false>(acc, (b ? buf1 : buf0) + wave * BUF, xrow + it * ITEM, rowbytes - it * ITEM, [&](int q) {
                     return *reinterpret_cast<const v4f*>(xs + (it * GPI + q) * 16 + 4 * (lane >> 4));
                 });
             asm volatile("" ::: "memory");
@@ -392,7 +401,7 @@ __global__ __launch_bounds__(DOWN_WAVES * 64) void token_down_kernel(TokenArgs a
             if (item < items) {
                 const int en = item / per, it = item - en * per;
                 const int s = t.slot[en][wr];
-                item_products(acc, (b ? buf1 : buf0) + wave * BUF, hq + (s < 0 ? 0 : s) * stride + it * ITEM,
+                item_products<true>(acc, (b ? buf1 : buf0) + wave * BUF, hq + (s < 0 ? 0 : s) * stride + it * ITEM,
                               rowbytes - it * ITEM, [&](int q) {
                                   v4f v = {};
                                   if (4 * (lane >> 4) < M4)
