@@ -173,7 +173,8 @@ struct Row {
 // of its value (exp within |x| 2^-24 relative, a factor that the slope of the
 // score cancels for large |x|; the sum of a softmax within 1e-6; one rounding
 // by the bias), and `sure` says whether no two keys that decide were nearer to
-// each other than four times that.  If some were, the caller asks again in 64
+// each other than four times that, and every kept group is above every dropped
+// one by more than their keys may be off by.  If not, the caller asks again in 64
 // bits: about one row in a few hundred, where all of them in 64 bits took 41 us
 // instead of 29 (16384 rows of 256 experts in 8 groups).
 template <int V, bool WIDE, int GROUPS, typename T>
@@ -235,7 +236,10 @@ __device__ inline int choose(const RouteArgs& a, int64_t row, const float (&x)[V
         if (share >= 2) merge(dpp<SWAP1, 0xF>(none, b1), dpp<SWAP1, 0xF>(none, b2));
         if (share >= 4) merge(dpp<SWAP2, 0xF>(none, b1), dpp<SWAP2, 0xF>(none, b2));
         if (share >= 8) merge(dpp<HALF_MIRROR, 0xF>(none, b1), dpp<HALF_MIRROR, 0xF>(none, b2));
-        const T sum = GROUPS == 2 && b2 != none ? b1 + b2 : b1;
+        T sum = GROUPS == 2 && b2 != none ? b1 + b2 : b1;
+        // (two keys near the ends of fp32 have a sum outside it, which is still above that of a dead group)
+        const T most = (T)3.402823466e38f;
+        if (!EXACT && b1 != none) sum = larger(-most, smaller(most, sum));
         int ahead = 0;        // groups before this one
         for (int j = 0; j < a.n_group; ++j) {
             const T other = read_lane(sum, j * share);
@@ -243,11 +247,19 @@ __device__ inline int choose(const RouteArgs& a, int64_t row, const float (&x)[V
         }
         const uint64_t kept = __ballot(mine < a.n_group && ahead < a.keep);
         if (!EXACT && (WIDE || GROUPS == 2)) {
-            // the worst group kept against the best one dropped (orders as integers: the least by its complement)
-            const bool in = kept >> lane & 1;
-            const uint32_t o = ordered((float)sum);
-            const uint32_t low = ~wave_max(in ? ~o : 0), best = wave_max(!in && mine < a.n_group ? o : 0);
-            if (best && from_ordered(best) != masked && near((T)from_ordered(low), (T)from_ordered(best))) sure = false;
+            // Every kept group has to be above every dropped one by more than
+            // what both may be off by.  That goes with the keys, which may
+            // cancel in the sum: 1e-6 max(1, |key|) each, and the roundings of
+            // the sum and of the two lines below, 2^-24 of it each.  (At the
+            // ends of fp32 the bounds are infinite: not sure.)  The least
+            // bound of the kept ones as integers, by its complement.
+            auto size = [](T key) { return key > 1 ? key : key < -1 ? -key : (T)1; };
+            T off = (T)1.5e-6 * size(b1);
+            if (GROUPS == 2 && b2 != none) off += (T)1.5e-6 * size(b2);
+            const bool in = kept >> lane & 1, dropped = !in && mine < a.n_group && b1 != none;
+            const uint32_t low = ~wave_max(in ? ~ordered((float)(sum - off)) : 0);
+            const uint32_t best = wave_max(dropped ? ordered((float)(sum + off)) : 0);
+            if (low <= best) sure = false;
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
