@@ -382,7 +382,10 @@ apex4_status apex4_route(const void* logits, int32_t logits_type, int64_t M, int
  * nothing, whatever its gate; a token without a slot gets zeros.  A token may
  * name an expert more than once.  A token's result depends on its own slots
  * only: infinities or NaN in other tokens, or in the scales of experts that it
- * does not name, leave it as it is.
+ * does not name, leave it as it is.  Its own stay visible: y is NaN where x or
+ * a scale of gate_up is not finite (the scale of a group of 128 of x or h is not
+ * finite where a value is not, and h is NaN where g or u is not finite), and y
+ * is not finite where a gate or a scale of down is not.
  *   x_f16 [M, H] fp16, 16-byte aligned;  ids [M, k] int32, gates [M, k] fp32.
  *   qw_gate_up [E, 2I, H/2] and s_gate_up [E, 2I, H/128], qw_down [E, H, I/2]
  *   and s_down [E, H, I/128]: apex4_pack_weight outputs with group 128 (of the

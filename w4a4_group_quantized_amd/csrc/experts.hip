@@ -76,10 +76,9 @@ __global__ __launch_bounds__(64 * PLAN_WAVES) void plan_kernel(const int32_t* __
         const int64_t t = (int64_t)(blockIdx.x - E) * (64 * PLAN_WAVES) + threadIdx.x;
         if (t >= n8) return;      // (whole groups of 16 lanes)
         const qrule::half8 v = x[t];
-        const float amax = qrule::group_max<16>(qrule::absmax8(v));
-        const float scale = amax / 7.0f;
-        xq[t] = qrule::quantize8(v, scale, amax != 0.0f);
-        if ((t & 15) == 0) xs[t / 16] = amax != 0.0f ? scale : 0.0f;
+        const float scale = experts_scale(v);
+        xq[t] = qrule::quantize8(v, scale, scale != 0.0f);
+        if ((t & 15) == 0) xs[t / 16] = scale;
         return;
     }
     const int e = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -139,6 +138,18 @@ __global__ __launch_bounds__(64 * PLAN_WAVES) void plan_kernel(const int32_t* __
             row += __popcll(who);
         }
     }
+}
+
+// h to codes and scales, a chunk of 8 values a thread (rows without a slot too: nothing reads them)
+__global__ __launch_bounds__(256) void quantize_h_kernel(const qrule::half8* __restrict__ h, int64_t n8,
+                                                         uint32_t* __restrict__ hq, float* __restrict__ hs)
+{
+    const int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (t >= n8) return;          // (whole groups of 16 lanes)
+    const qrule::half8 v = h[t];
+    const float scale = experts_scale(v);
+    hq[t] = qrule::quantize8(v, scale, scale != 0.0f);
+    if ((t & 15) == 0) hs[t / 16] = scale;
 }
 
 // y = the sum of a token's slots, in slot order, of each slot's K parts, in
@@ -221,8 +232,9 @@ hipError_t launch_experts(const ExpertsProblem& p, hipStream_t stream)
     a.rows = p.M;
     a.parts = 1;
     launch_experts_tiled(a, true, R, stream);
-    const hipError_t e = launch_quantize(w.h, R, p.I, 128, w.hq, w.hs, stream);
-    if (e != hipSuccess) return e;
+    const int64_t h8 = (int64_t)R * (p.I / 8);
+    quantize_h_kernel<<<(unsigned)((h8 + 255) / 256), 256, 0, stream>>>(
+        reinterpret_cast<const qrule::half8*>(w.h), h8, reinterpret_cast<uint32_t*>(w.hq), w.hs);
     a.qx = w.hq;
     a.sx = w.hs;
     a.qw = p.qw_down;

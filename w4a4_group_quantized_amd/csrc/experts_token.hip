@@ -281,11 +281,10 @@ __global__ __launch_bounds__(UP_WAVES * 64) void token_up_kernel(TokenArgs a, _F
     for (int j = 0; j < NX; ++j) {
         const int i = tid + j * UP_WAVES * 64;
         if (i >= n8) break;
-        const float amax = qrule::group_max<16>(qrule::absmax8(v[j]));
-        const float scale = amax / 7.0f;
+        const float scale = experts_scale(v[j]);
         const int m = i / (H / 8), c = i - m * (H / 8);
-        *reinterpret_cast<uint32_t*>(xq + m * stride + 4 * c) = qrule::quantize8(v[j], scale, amax != 0.0f);
-        if ((c & 15) == 0) xs[(c >> 4) * 16 + m] = amax != 0.0f ? scale : 0.0f;
+        *reinterpret_cast<uint32_t*>(xq + m * stride + 4 * c) = qrule::quantize8(v[j], scale, scale != 0.0f);
+        if ((c & 15) == 0) xs[(c >> 4) * 16 + m] = scale;
     }
     for (int i = tid; i < G * 16; i += UP_WAVES * 64)
         if ((i & 15) >= M) xs[i] = 0.0f;
@@ -385,10 +384,9 @@ __global__ __launch_bounds__(DOWN_WAVES * 64) void token_down_kernel(TokenArgs a
         if (i >= n8) break;
         const int s = i / (I / 8), c = i - s * (I / 8), en = t.entry[s];
         if (en < 0) continue;                    // (16 neighbouring lanes share a slot; its h is not set)
-        const float amax = qrule::group_max<16>(qrule::absmax8(v[j]));
-        const float scale = amax / 7.0f;
-        *reinterpret_cast<uint32_t*>(hq + s * stride + 4 * c) = qrule::quantize8(v[j], scale, amax != 0.0f);
-        if ((c & 15) == 0) tab[(en * G + (c >> 4)) * M4 + s / k] = amax != 0.0f ? scale * gate[j] : 0.0f;
+        const float scale = experts_scale(v[j]);
+        *reinterpret_cast<uint32_t*>(hq + s * stride + 4 * c) = qrule::quantize8(v[j], scale, scale != 0.0f);
+        if ((c & 15) == 0) tab[(en * G + (c >> 4)) * M4 + s / k] = scale != 0.0f ? scale * gate[j] : 0.0f;
     }
     lds_barrier();
 
