@@ -105,3 +105,51 @@ def test_products_past_fp16_stay_within_it(dev, M):
     w[3] *= 1e-3
     y, y32 = apex4.experts(x, ids, gates, *w, want_y32=True)
     assert torch.isfinite(y).all() and torch.isfinite(y32).all()
+
+
+@pytest.mark.parametrize("M", TOKENS)
+@pytest.mark.parametrize("value", VALUES)
+def test_zeros_times_what_is_no_number(dev, M, value):
+    """A zero on one side of a product does not hide what is no number on the other."""
+    x, ids, gates, w = problem(dev, M)
+    named = (ids == 1).any(1)
+    zeros = x.clone()
+    zeros[:] = 0
+    off = gates.clone()
+    off[ids == 1] = 0
+    clean, none = apex4.experts(x, ids, off, *w), apex4.experts(zeros, ids, gates, *w)
+    broken = [t.clone() for t in w]
+    broken[3][1] = value
+    for y, other in ((apex4.experts(x, ids, off, *broken), clean), (apex4.experts(zeros, ids, gates, *broken), none)):
+        assert not torch.isfinite(y[named]).any()
+        assert torch.equal(y[~named], other[~named])
+    off[ids == 1] = value
+    y = apex4.experts(zeros, ids, off, *w)
+    assert torch.isnan(y[named]).all() and (y[~named] == 0).all()
+
+
+@pytest.mark.parametrize("M,experts,k,hidden,inter", [(2, 64, 8, 256, 1408), (3, 16, 4, 384, 2176), (4, 12, 5, 256, 1152),
+                                                      (8, 6, 4, 128, 640), (16, 20, 2, 128, 640), (5, 3, 3, 256, 128),
+                                                      (70, 12, 5, 256, 2176)])
+def test_a_tokens_bits_go_by_its_own_slots(dev, M, experts, k, hidden, inter):
+    """What the other tokens name, and what they hold, changes no bit of a token."""
+    rng = np.random.default_rng(M + k)
+    w = []
+    for n, cols in ((2 * inter, hidden), (hidden, inter)):
+        w.append(torch.from_numpy(rng.integers(0, 256, (experts, n, cols // 2), dtype=np.uint8)).to(dev))
+        w.append(torch.from_numpy(rng.uniform(0.001, 0.01, (experts, n, cols // 128)).astype(np.float32)).to(dev))
+    x = torch.from_numpy(rng.standard_normal((M, hidden), dtype=np.float32)).half().to(dev)
+    gates = torch.from_numpy(rng.uniform(-1.0, 1.0, (M, k)).astype(np.float32)).to(dev)
+    ids = rng.integers(-1, experts, (M, k)).astype(np.int32)
+    ids[0] = rng.permutation(experts)[:k]
+    _, first = apex4.experts(x, torch.from_numpy(ids).to(dev), gates, *w, want_y32=True)
+    for m in (0, M // 2, M - 1):
+        for draw in range(6):
+            other = rng.integers(-1, experts, (M, k)).astype(np.int32)
+            if draw == 5:
+                other[:] = -1
+            other[m] = ids[m]
+            z = torch.from_numpy(rng.standard_normal((M, hidden), dtype=np.float32)).half().to(dev)
+            z[m] = x[m]
+            _, y32 = apex4.experts(z, torch.from_numpy(other).to(dev), gates, *w, want_y32=True)
+            assert torch.equal(y32[m], first[m]), (m, draw)

@@ -18,9 +18,11 @@
 //   - weights come by direct-to-LDS copies into a buffer of each wave's own,
 //     16 rows by 512 bytes (1024 codes) at a time, so that no barrier stands
 //     between a wave and its stream;
-//   - the down launch walks all entries for its 16 columns and adds them in
-//     one accumulator, with the gate in the activation's scale; the waves'
-//     sums are added in wave order.
+//   - the down launch walks all entries for its 16 columns.  Which wave takes
+//     an item goes by the entries of all tokens, so each item's sums are stored
+//     by slot, over the codes that the item alone has read, and a token's are
+//     added at the end in the order of its slots: its result does not depend
+//     on what other tokens name.
 // LDS: piece c (16 bytes) of a row sits at c ^ row, so that the 16 rows' reads
 // of one column touch every bank once.
 #include "experts.h"
@@ -47,7 +49,7 @@ constexpr int OOB = (int)0x80000000; // past every buffer: reads zeros
 constexpr int PAD = 16;              // bytes between activation rows: their reads fall on different banks
 
 struct Entries {
-    signed char slot[SLOTS][TOKENS];  // of an entry's token, -1 for none
+    signed char slot[SLOTS][TOKENS];  // of an entry's token; ~(its first slot) for a token that does not name it
     signed char entry[SLOTS];         // of a slot, -1 for none
 };
 
@@ -94,7 +96,8 @@ __device__ inline Found find_entries(int id, int R, int k, int E)
 __device__ inline void write_entries(Entries& t, const Found& f, int k)
 {
     const int lane = threadIdx.x & 63;
-    *reinterpret_cast<int4*>(t.slot[lane]) = make_int4(-1, -1, -1, -1);
+    const int none = (~lane & 255) * 0x01010101;
+    if (f.leads >> lane & 1) *reinterpret_cast<int4*>(t.slot[f.entry]) = make_int4(none, none, none, none);
     t.entry[lane] = (signed char)f.entry;
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -166,8 +169,7 @@ __device__ inline void load_chunks(half8 (&v)[NX], const half8* x, int n8, int t
 // acc[r] += sum over the item's groups of sa4(q)[r] s_w[q] P, P of activation row 4 (lane >> 4) + r and weight row
 // lane & 15.  `x`: the codes of this lane's activation row lane & 15 at the item's first byte; `left`: bytes of the
 // row from there.
-// APART: the item is of an entry that not every token names.
-template <bool APART, typename Scale>
+template <typename Scale>
 __device__ inline void item_products(v4f& acc, const uint8_t* buf, const uint8_t* x, int left, Scale sa4)
 {
     const int lane = threadIdx.x & 63, row = lane & 15, kg = lane >> 4;
@@ -197,17 +199,8 @@ __device__ inline void item_products(v4f& acc, const uint8_t* buf, const uint8_t
             if (q0 + i >= groups) break;
             const v4f s = sa4(q0 + i);
             const float sn = sw[16 * (q0 + i)];
-            float f[4];
 #pragma unroll
-            for (int r = 0; r < 4; ++r) f[r] = s[r] * sn;
-            // a token that does not name the entry has the scale 0 here and takes nothing from it, also
-            // where its weight scales are no numbers (one branch a group: a choice a value took 5% of the time)
-            if (APART && __ballot(!(fabsf(sn) < __builtin_inff())) != 0) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) f[r] = s[r] != 0.0f ? f[r] : 0.0f;
-            }
-#pragma unroll
-            for (int r = 0; r < 4; ++r) acc[r] = fmaf(f[r], (float)P[i][r], acc[r]);
+            for (int r = 0; r < 4; ++r) acc[r] = fmaf(s[r] * sn, (float)P[i][r], acc[r]);
         }
     }
 }
@@ -299,7 +292,7 @@ __global__ __launch_bounds__(UP_WAVES * 64) void token_up_kernel(TokenArgs a, _F
             const int it = i0 + b;
             wait_copies();
             if (it < items)
-                item_products<false>(acc, (b ? buf1 : buf0) + wave * BUF, xrow + it * ITEM, rowbytes - it * ITEM, [&](int q) {
+                item_products(acc, (b ? buf1 : buf0) + wave * BUF, xrow + it * ITEM, rowbytes - it * ITEM, [&](int q) {
                     return *reinterpret_cast<const v4f*>(xs + (it * GPI + q) * 16 + 4 * (lane >> 4));
                 });
             asm volatile("" ::: "memory");
@@ -319,7 +312,7 @@ __global__ __launch_bounds__(UP_WAVES * 64) void token_up_kernel(TokenArgs a, _F
 }
 
 // LDS of the down launch beside the waves' buffers: the codes of h (rows of
-// I/2 + PAD bytes by slot), the scales times the gates as [entry][G][M4].
+// I/2 + PAD bytes by slot), their scales as [entry][G][M4].
 __host__ __device__ inline int down_lds(const TokenArgs& a)
 {
     const int R = (int)a.p.M * a.p.k;
@@ -333,6 +326,7 @@ __global__ __launch_bounds__(DOWN_WAVES * 64) void token_down_kernel(TokenArgs a
     __shared__ __attribute__((aligned(1024))) uint8_t buf1[DOWN_WAVES * BUF];
     extern __shared__ __attribute__((aligned(16))) uint8_t hq[];
     __shared__ Entries t;
+    __shared__ float gates[SLOTS];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int M = (int)a.p.M, k = a.p.k, H = a.p.H, I = a.p.I, G = a.G, R = M * k, M4 = a.M4;
@@ -343,9 +337,7 @@ __global__ __launch_bounds__(DOWN_WAVES * 64) void token_down_kernel(TokenArgs a
     int id = a.p.ids[min(lane, R - 1)];
     half8 v[NX];
     load_chunks(v, reinterpret_cast<const half8*>(h), n8, DOWN_WAVES * 64);
-    float gate[NX];
-#pragma unroll
-    for (int j = 0; j < NX; ++j) gate[j] = a.p.gates[min(tid + j * DOWN_WAVES * 64, n8 - 1) / (I / 8)];
+    const float gate = a.p.gates[min(lane, R - 1)];
     id = lane < R ? id : -1;
     const Found f = find_entries(id, R, k, a.p.E);
     const int n0 = blockIdx.x * 16, rowbytes = I / 2, per = (rowbytes + ITEM - 1) / ITEM, items = f.n * per;
@@ -374,10 +366,10 @@ __global__ __launch_bounds__(DOWN_WAVES * 64) void token_down_kernel(TokenArgs a
     fetch(buf1, wave + DOWN_WAVES);
 
     if (wave == 0) write_entries(t, f, k);
-    for (int i = tid; i < R * G * M4; i += DOWN_WAVES * 64) tab[i] = 0.0f;
     lds_barrier();
 
-    // the codes of h, and its scales with the gates
+    // the codes of h, and its scales (those of tokens that do not name an entry stay unset: what the matrix
+    // instruction makes of their rows is not stored)
 #pragma unroll
     for (int j = 0; j < NX; ++j) {
         const int i = tid + j * DOWN_WAVES * 64;
@@ -386,21 +378,30 @@ __global__ __launch_bounds__(DOWN_WAVES * 64) void token_down_kernel(TokenArgs a
         if (en < 0) continue;                    // (16 neighbouring lanes share a slot; its h is not set)
         const float scale = experts_scale(v[j]);
         *reinterpret_cast<uint32_t*>(hq + s * stride + 4 * c) = qrule::quantize8(v[j], scale, scale != 0.0f);
-        if ((c & 15) == 0) tab[(en * G + (c >> 4)) * M4 + s / k] = scale != 0.0f ? scale * gate[j] : 0.0f;
+        if ((c & 15) == 0) tab[(en * G + (c >> 4)) * M4 + s / k] = scale;
     }
+    if (wave == 0) gates[lane] = gate;
     lds_barrier();
 
-    v4f acc = {};
+    // the sums of item `it` for slot s: 16 floats in place of the codes that they were made of
+    auto sums = [&](int s, int it) { return reinterpret_cast<float*>(hq + s * stride + it * ITEM); };
     for (int i0 = wave; i0 < items; i0 += BUFS * DOWN_WAVES) {
 #pragma unroll
         for (int b = 0; b < BUFS; ++b) {
             const int item = i0 + b * DOWN_WAVES;
+            const bool mine = item < items;
+            const int en = item / per, it = item - en * per;
+            v4f acc = {};
+            int four = -1;
             wait_copies();
-            if (item < items) {
-                const int en = item / per, it = item - en * per;
-                const int s = t.slot[en][wr];
-                item_products<true>(acc, (b ? buf1 : buf0) + wave * BUF, hq + (s < 0 ? 0 : s) * stride + it * ITEM,
-                              rowbytes - it * ITEM, [&](int q) {
+            if (mine) {
+                // the slots of this lane's activation row (one that no token gives takes another's codes) and of
+                // its four rows of sums
+                int s = t.slot[en][wr];
+                s ^= s >> 31;
+                four = *reinterpret_cast<const int*>(&t.slot[en][4 * (lane >> 4)]);
+                item_products(acc, (b ? buf1 : buf0) + wave * BUF, hq + s * stride + it * ITEM, rowbytes - it * ITEM,
+                              [&](int q) {
                                   v4f v = {};
                                   if (4 * (lane >> 4) < M4)
                                       v = *reinterpret_cast<const v4f*>(tab + (en * G + it * GPI + q) * M4 +
@@ -410,20 +411,39 @@ __global__ __launch_bounds__(DOWN_WAVES * 64) void token_down_kernel(TokenArgs a
             }
             asm volatile("" ::: "memory");
             fetch(b ? buf1 : buf0, item + BUFS * DOWN_WAVES);
+            // (after the next copies: the sums are the end of the item's chain)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int to = (signed char)(four >> (8 * r));
+                if (to >= 0) sums(to, it)[wr] = acc[r];
+            }
         }
     }
     __builtin_amdgcn_s_waitcnt(0xF70);           // no copy outlives its buffer
     __syncthreads();
+    // each slot's sum with its gate, 0 for a dead one; then each token's, in the order of its slots
     float* red = reinterpret_cast<float*>(buf0);  // the buffers are done with
-    *reinterpret_cast<v4f*>(red + (wave * 64 + lane) * 4) = acc;
+#pragma unroll 1
+    for (int i = tid; i < R * 16; i += DOWN_WAVES * 64) {
+        const int s = i >> 4;
+        float d = 0.0f;
+#pragma unroll 1
+        for (int it = 0; it < per; ++it) d += sums(s, it)[i & 15];
+        red[i] = t.entry[s] >= 0 ? gates[s] * (d * 0.00390625f) : 0.0f;
+    }
     __syncthreads();
     if (tid < 16 * TOKENS) {
         const int m = tid >> 4, c = tid & 15;
         if (m < M) {
             float v = 0.0f;
+#pragma unroll 1
+            for (int j0 = 0; j0 < k; j0 += 8) {
+                float d[8];
 #pragma unroll
-            for (int w = 0; w < DOWN_WAVES; ++w) v += red[(w * 64 + 16 * (m >> 2) + c) * 4 + (m & 3)];
-            v *= 0.00390625f;
+                for (int j = 0; j < 8; ++j) d[j] = red[(m * k + min(j0 + j, k - 1)) * 16 + c];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v += j0 + j < k ? d[j] : 0.0f;
+            }
             asm volatile("" : "+v"(v));          // y16 is the fp16 rounding of y32
             const int64_t o = (int64_t)m * H + n0 + c;
             static_cast<_Float16*>(a.p.y16)[o] = (_Float16)v;
