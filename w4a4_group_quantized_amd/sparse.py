@@ -123,6 +123,9 @@ class SparseLayerW4A4(torch.nn.Module):
         ids, gates = self.route(rows, None if padding is None else padding.reshape(-1))
         y = self.experts(rows, ids, gates)
         if self.shared is not None:
-            gate, up = self.shared[0](rows).chunk(2, dim=-1)
-            y = y + self.shared[1]((torch.nn.functional.silu(gate) * up).contiguous())
+            # within the type's range, as the routed experts' h: an infinity would cost the token its whole row
+            # (the codes of a block with one are NaN), and silu(-inf) is NaN; a NaN stays
+            most = torch.finfo(rows.dtype).max
+            gate, up = self.shared[0](rows).clamp_(-most, most).chunk(2, dim=-1)
+            y = y + self.shared[1]((torch.nn.functional.silu(gate) * up).clamp_(-most, most))
         return y.reshape(x.shape)
