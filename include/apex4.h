@@ -327,7 +327,8 @@ apex4_status apex4_select_granularity(int64_t M, int64_t N, int64_t K, double mi
 
 /*
  * Sparse expert layers and 8-bit layers: the parts of a W4A4 model that are
- * not one dense W4A4 product.
+ * not one dense W4A4 product.  Their workspace sizes go by the current device's
+ * compute units: ask for them with the device of the call current.
  *
  * Element types of the calls below that take one.
  */

@@ -408,6 +408,16 @@ def _call(fn: str, device, *args) -> None:
         raise Apex4Error(fn, status)
 
 
+def _size(fn: str, device, *args) -> int:
+    """A workspace size for a call on `device`: it goes by the current device's compute units."""
+    import torch
+    f = getattr(lib(), fn)
+    if torch._C._cuda_getDevice() == device.index:
+        return int(f(*args))
+    with torch.cuda.device(device):
+        return int(f(*args))
+
+
 def route(logits, k: int, *, score: str = "softmax", bias=None, n_group: int = 1, topk_group: int = 1,
           group_top: int = 1, renormalize: bool = True, scale: float = 1.0, out=None):
     """apex4_route: logits [M, E] (float32, float16 or bfloat16 GPU tensor) ->
@@ -440,6 +450,7 @@ def route(logits, k: int, *, score: str = "softmax", bias=None, n_group: int = 1
 
 
 def experts_workspace_size(M: int, k: int, E: int, H: int, I: int, group: int = 128) -> int:
+    """Bytes that `experts` takes on the current device."""
     return int(lib().apex4_experts_workspace_size(M, k, E, H, I, group))
 
 
@@ -477,7 +488,8 @@ def experts(x, ids, gates, qw_gate_up, s_gate_up, qw_down, s_down, *, group: int
     if want_y32 and y32 is None:
         y32 = torch.empty((M, H), dtype=torch.float32, device=dev)
     if workspace is None:
-        workspace = torch.empty(experts_workspace_size(M, k, E, H, I, group), dtype=torch.uint8, device=dev)
+        need = _size("apex4_experts_workspace_size", dev, M, k, E, H, I, group)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     _call("apex4_experts_w4a4", dev, x.data_ptr(), ids.data_ptr(), gates.data_ptr(), M, k, E, H, I, group,
           qw_gate_up.data_ptr(), s_gate_up.data_ptr(), qw_down.data_ptr(), s_down.data_ptr(), y16.data_ptr(),
           _ptr(y32), workspace.data_ptr(), workspace.numel())
@@ -543,7 +555,7 @@ def gemm_e4m3(qa8, sa, qw8, sw, dtype=None, *, want_y32: bool = False, y=None, y
     if want_y32 and y32 is None:
         y32 = torch.empty((M, N), dtype=torch.float32, device=dev)
     if workspace is None:
-        need = int(lib().apex4_gemm_e4m3_workspace_size(M, N, K))
+        need = _size("apex4_gemm_e4m3_workspace_size", dev, M, N, K)
         workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     _call("apex4_gemm_e4m3", dev, _ptr(qa8), _ptr(sa), _ptr(qw8), _ptr(sw), M, N, K, code, _ptr(y), _ptr(y32),
           _ptr(workspace), 0 if workspace is None else workspace.numel())
@@ -551,6 +563,7 @@ def gemm_e4m3(qa8, sa, qw8, sw, dtype=None, *, want_y32: bool = False, y=None, y
 
 
 def linear_e4m3_workspace_size(M: int, N: int, K: int) -> int:
+    """Bytes that `linear_e4m3` takes on the current device."""
     return int(lib().apex4_linear_e4m3_workspace_size(M, N, K))
 
 
@@ -576,7 +589,7 @@ def linear_e4m3(x, qw8, sw, *, want_y32: bool = False, y=None, y32=None, workspa
         y = torch.empty((M, N), dtype=x.dtype, device=dev)
     if want_y32 and y32 is None:
         y32 = torch.empty((M, N), dtype=torch.float32, device=dev)
-    need = linear_e4m3_workspace_size(M, N, K)
+    need = _size("apex4_linear_e4m3_workspace_size", dev, M, N, K)
     if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     _call("apex4_linear_e4m3", dev, x.data_ptr(), code, qw8.data_ptr(), sw.data_ptr(), M, N, K, y.data_ptr(),
