@@ -84,3 +84,20 @@ def test_the_calls_ask_that_way(devices, monkeypatch):
     with pytest.raises(Stop):
         apex4.linear_e4m3(Host(3, 256, dtype=f16), Host(256, 256), Host(2, 2, dtype=f32), y=y)
     assert asked == [1, 1, 1]
+
+
+def test_experts_are_packed_on_their_device(devices, monkeypatch):
+    from w4a4_group_quantized_amd.sparse import W4A4Experts
+    packed = []
+
+    def pack(w, group):
+        packed.append(Device.current)
+        return torch.zeros(w.shape[0], 1, dtype=torch.uint8), torch.zeros(w.shape[0], 1)
+
+    class OnDevice1(torch.Tensor):
+        device = property(lambda self: torch.device("cuda", 1))
+
+    monkeypatch.setattr(apex4, "pack_weight", pack)
+    with pytest.raises(ValueError):        # the packed tensors are on the host
+        W4A4Experts.from_weights(torch.zeros(2, 4, 8).as_subclass(OnDevice1), torch.zeros(2, 4, 2).as_subclass(OnDevice1))
+    assert packed == [1, 1] and Device.current == 0

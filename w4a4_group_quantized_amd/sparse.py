@@ -75,7 +75,8 @@ class W4A4Experts(torch.nn.Module):
         """Quantize and pack fp16 [E, 2I, H] and [E, H, I] GPU weights (the offline step)."""
         packed = []
         for w in (gate_up, down):
-            q, s = apex4.pack_weight(w.reshape(-1, w.shape[-1]).contiguous(), 128)
+            with torch.cuda.device(w.device):      # (the library launches to the current device)
+                q, s = apex4.pack_weight(w.reshape(-1, w.shape[-1]).contiguous(), 128)
             packed += [q.view(*w.shape[:2], -1), s.view(*w.shape[:2], -1)]
         return cls(*packed)
 
