@@ -101,3 +101,26 @@ def test_experts_are_packed_on_their_device(devices, monkeypatch):
     with pytest.raises(ValueError):        # the packed tensors are on the host
         W4A4Experts.from_weights(torch.zeros(2, 4, 8).as_subclass(OnDevice1), torch.zeros(2, 4, 2).as_subclass(OnDevice1))
     assert packed == [1, 1] and Device.current == 0
+
+
+@pytest.mark.parametrize("bad", [dict(n_group=2 ** 32 + 8, topk_group=4), dict(n_group=8, topk_group=2 ** 32 + 4),
+                                 dict(group_top=2 ** 32 + 1), dict(group_top=-2 ** 32 + 2), dict(k=2 ** 33 + 6),
+                                 dict(k=-2 ** 32 + 6)])
+def test_route_refuses_numbers_that_do_not_fit_the_library(devices, monkeypatch, bad):
+    """Taken modulo 2^32 each of them is a right argument."""
+    called = []
+
+    class Lib:
+        apex4_route = staticmethod(lambda *args: called.append(args) or 0)
+
+    class Logits(Host):
+        def data_ptr(self):
+            return 0x10000
+
+    monkeypatch.setattr(apex4, "_lib", Lib)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0)
+    args = dict(k=6) | bad
+    out = Logits(4, args["k"], dtype=torch.int32), Logits(4, args["k"], dtype=torch.float32)
+    with pytest.raises(ValueError, match="32 bits"):
+        apex4.route(Logits(4, 64, dtype=torch.float32), out=out, **args)
+    assert not called

@@ -432,6 +432,9 @@ def route(logits, k: int, *, score: str = "softmax", bias=None, n_group: int = 1
         raise ValueError(f"logits must be [M, E], got {tuple(logits.shape)}")
     if score not in _SCORES:
         raise ValueError(f"unknown score {score!r}; one of {tuple(_SCORES)}")
+    # (0 or, with a negative one, which the library refuses, -1)
+    if (k | n_group | topk_group | group_top) >> 31 not in (0, -1):
+        raise ValueError(f"k, n_group, topk_group and group_top must fit 32 bits, got {k, n_group, topk_group, group_top}")
     code = _type_code(logits, "logits")
     (M, E), dev = logits.shape, logits.device
     if bias is not None:
