@@ -1,7 +1,8 @@
 // C ABI of the sparse-layer and 8-bit calls (include/apex4.h: apex4_route,
 // apex4_experts_w4a4 and the e4m3 calls): host-side argument checks, then the
-// launch on the caller's stream.  Every check runs before any HIP call, so a
-// rejected call touches neither the device nor the caller's memory.
+// launch on the caller's stream.  Every check runs before anything is launched,
+// so a rejected call touches neither the device's work nor the caller's memory
+// (a workspace size asks the runtime which device is current).
 #include "apex4.h"
 
 #include <atomic>

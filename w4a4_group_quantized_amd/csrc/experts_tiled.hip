@@ -22,8 +22,10 @@
 // instruction, with the weights split into two 2-bit E2M1 operands and the
 // activations as E2M3, returns the same sums in fp32 for 27% fewer vector
 // instructions, but its 96-byte groups cost more in copies and LDS than that:
-// 725 us.)  For few rows it is the stream of the weights (355 MB in 80 us, 4.4
-// TB/s, at 2.5 rows an expert).
+// 725 us.)  The dense kernel of this rule has fewer: it widens once a workgroup,
+// on the way into LDS, and takes the scale products from one bf16 matrix
+// instruction on exact splits; neither is built here.  For few rows it is the
+// stream of the weights (355 MB in 80 us, 4.4 TB/s, at 2.5 rows an expert).
 #include "experts.h"
 #include "layers.h"
 

@@ -168,7 +168,10 @@ hipError_t launch(const RowsArgs& a, hipStream_t stream)
 }  // namespace
 
 // One launch without partial sums against tiles with a reduction: 16 x 4096 x
-// 4096 11.6 us a call and 14.3, 16 x 28672 x 8192 64 us and 39.
+// 4096 11.6 us a call and 14.3, 16 x 28672 x 8192 64 us and 39.  Just past the
+// end, 45 MB, weights from memory: 16 x 4096 x 11008 23.2 us and 20.6, 16 x
+// 11008 x 4096 19.7 and 18.8; one row 21.1 and 19.6, and 14.5 and 17.4, so that
+// one row could go further where K is short (1 x 14336 x 8192 24.5 and 30.1).
 bool e4m3_rows_supports(const E4m3Problem& p) { return p.M <= ROWS && (int64_t)p.N * p.K <= (1 << 25); }
 
 // Every workgroup makes the codes of all rows: up to 64 values a thread.

@@ -98,6 +98,8 @@ class SparseLayerW4A4(torch.nn.Module):
     to be computed in; experts: W4A4Experts; shared: (gate_up, down) as
     E4M3Linear, applied to every token; routing: keyword arguments of
     apex4.route (score, bias, n_group, topk_group, group_top, renormalize, scale).
+    A token whose logits are all NaN (a NaN in x) is routed nowhere, like padding:
+    only the shared expert shows it.
     """
 
     def __init__(self, router: torch.Tensor, experts: W4A4Experts, k: int, shared=None, **routing):
