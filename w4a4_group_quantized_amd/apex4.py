@@ -395,11 +395,12 @@ def _need(t, name: str, dtype, shape, device) -> None:
 def _call(fn: str, device, *args) -> None:
     """One library call with `device` current (a launch goes to the current
     device, the tensors' may be another one), on torch's current stream there
-    (read as the bare handle: a torch Stream object costs 2 us)."""
+    (both read bare: a torch Stream object costs 2 us).  GPU tensors are at
+    hand, so torch has been set up for the device."""
     import torch
     f = getattr(lib(), fn)
     index = device.index
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         status = f(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):

@@ -25,8 +25,8 @@
 //     where those are several do the 64-bit keys and the indices decide;
 //   - up to 4 values a lane are sorted once, and a round looks at each lane's
 //     first only.
-// What is left is paid once a row for the whole wave: of 1070 instructions a
-// row the groups' step takes 360, and the rounds most of the rest (one 32-bit
+// What is left is paid once a row for the whole wave: of 1080 instructions a
+// row the groups' step takes 370, and the rounds most of the rest (one 32-bit
 // score a value, 64 bits for the gates only).  Rows that shared a wave would
 // share them; that is not built.
 #include "layers.h"
