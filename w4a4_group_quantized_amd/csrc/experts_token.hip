@@ -3,8 +3,8 @@
 // a column block with the weighted sum over the experts.
 //
 // Such a call is the stream of the chosen experts' weights and the chain of
-// small steps around it.  The six launches of the general path (order of the
-// slots, codes of x, product, codes of h, product, sum) took 50 us for one
+// small steps around it.  Launches of their own for the order of the slots, the
+// codes of x, a product, the codes of h, a product and the sum took 50 us for one
 // token and 8 of 64 experts (4096 x 1408; 74 MB of weights, 14 us at the rate
 // of a large copy), of which the two products were 36; this way it takes 27.
 // Here
