@@ -467,6 +467,117 @@ apex4_status apex4_linear_e4m3(const void* x, int32_t x_type, const void* qw8, c
                                int64_t N, int64_t K, void* y, float* y_f32, void* workspace,
                                size_t workspace_bytes, void* stream);
 
+/*
+ * Attention: rotary positions, a paged key/value cache held in 4 bits, and
+ * attention over it.  Rows of queries, keys and values are [T, heads, D] with
+ * the heads of a token contiguous and ld elements between tokens (the parts of
+ * one fused projection's output can be used where they are).
+ *
+ * Rotary positions: of every head the first R numbers form R / 2 pairs (a, b),
+ *     (a, b) -> s * (a cos(theta) - b sin(theta), b cos(theta) + a sin(theta)),
+ *     theta = positions[t] * freqs[i],   i = 0 .. R/2 - 1
+ * pair i being the numbers i and R/2 + i, or 2i and 2i + 1 (interleaved nonzero).
+ * Angles, sines and the turned pairs are computed in 64 bits and rounded to
+ * fp32, then to the output's type; numbers R .. D-1 are copied.
+ *   x [T, H, D] of type (APEX4_F32, APEX4_F16 or APEX4_BF16), ldx >= H * D;
+ *   y the same with ldy (y == x with ldy == ldx turns in place; other overlaps
+ *   are not allowed).  x and y 16-byte aligned, ldx and ldy multiples of 8.
+ *   positions [T] int64 (beyond +-(2^31 - 1): taken as that), freqs [R/2] fp64,
+ *   8-byte aligned.  Scaled frequencies (longer contexts) are the caller's.
+ *   0 <= T <= 2^24 (0: no-op), 1 <= H <= 1024, D and R multiples of 16,
+ *   16 <= R <= D <= 1024; scale finite.  Asynchronous on `stream`.
+ */
+apex4_status apex4_rope(const void* x, int32_t type, int64_t T, int32_t H, int32_t D, int64_t ldx,
+                        const int64_t* positions, const double* freqs, int32_t R, int32_t interleaved, double scale,
+                        void* y, int64_t ldy, void* stream);
+
+/*
+ * The cache: `pages` pages of `page` tokens (16, 32, 64, ... 1024) each, for Hkv
+ * heads of D numbers (64, 128 or 256).  A key or a value, one head of one token,
+ * is a group of the quantization rule of apex4_quantize_act: s = max|x| / 7,
+ * c = clamp(round_half_even(x / s), -8, 7), kept as the nibble c + 8 and one fp32
+ * scale.  A head that holds a number that is not finite gets a NaN scale, so
+ * that whatever sees the token is NaN.  Token `off` of page p, head h:
+ *   k_codes  [pages, Hkv, page, D/2] bytes: nibble of number d in byte d / 2, even
+ *            d in the low half.
+ *   v_codes  [pages, Hkv, page/16, 8 D] bytes, 16 tokens a row: with off % 16 =
+ *            4 g + i, byte (16 g + r) D/8 + 4 v + i (r < 16, v < D/32) holds the
+ *            numbers r + 32 v (low half) and r + 32 v + 16 (high half): the order
+ *            in which the matrix instructions take 16 tokens, 4 to a lane.
+ *   k_scales, v_scales [pages, Hkv, page] fp32.
+ * All four 16-byte aligned, caller-owned.  A token's place is its slot, p * page
+ * + off.
+ *
+ * apex4_kv4_append: stores T tokens' keys and values, the keys turned by their
+ * positions on the way (quantized from fp32, not from a rounded key), and turns
+ * the same tokens' queries.
+ *   k, v [T, Hkv, D] of type (APEX4_F16 or APEX4_BF16), ldk, ldv >= Hkv * D;
+ *   slots [T] int64: a token whose slot is negative or behind the last page is
+ *   not stored (its queries are turned); the slots of one call must differ.
+ *   positions, freqs, R, interleaved, scale: as in apex4_rope; positions NULL
+ *   (then R 0 and no queries): keys are stored as they are.
+ *   q [T, Hq, D] with ldq, q_out [T, Hq, D] contiguous; or both NULL and Hq 0.
+ *   q_out == q with ldq == Hq * D turns in place.
+ *   Pointers of rows 16-byte aligned, strides multiples of 8; 0 <= T <= 2^24 (0:
+ *   no-op), Hq, Hkv <= 1024, pages < 2^31.
+ * What is not stored keeps its bytes.  Asynchronous on `stream`.
+ */
+apex4_status apex4_kv4_append(const void* q, const void* k, const void* v, int32_t type, int64_t T, int32_t Hq,
+                              int32_t Hkv, int32_t D, int64_t ldq, int64_t ldk, int64_t ldv,
+                              const int64_t* positions, const double* freqs, int32_t R, int32_t interleaved,
+                              double scale, const int64_t* slots, int64_t pages, int32_t page, void* k_codes,
+                              float* k_scales, void* v_codes, float* v_scales, void* q_out, void* stream);
+
+/*
+ * apex4_kv4_read: the values c * s (rounded to `type`: APEX4_F32, APEX4_F16 or
+ * APEX4_BF16) of T cached tokens, k and v [T, Hkv, D], 16-byte aligned.  slots
+ * [T] int64, in any order, repeated or not; a slot that is negative or behind
+ * the last page gives zeros.  Limits as above, T * Hkv * D < 2^38.
+ */
+apex4_status apex4_kv4_read(const void* k_codes, const float* k_scales, const void* v_codes, const float* v_scales,
+                            int64_t pages, int32_t page, int32_t Hkv, int32_t D, const int64_t* slots, int64_t T,
+                            int32_t type, void* k, void* v, void* stream);
+
+/*
+ * Attention of B sequences' newest tokens over the cache:
+ *     o[t, h] = sum_j p_j v_j,  p = softmax over the seen tokens j of
+ *               scale * q[t, h] . k_j,   key head h / (Hq / Hkv)
+ * Sequence b owns the queries cu_q[b] .. cu_q[b+1] - 1 (cu_q NULL: query b, T ==
+ * B) and kv_lens[b] cached tokens, the newest of which are those queries' own:
+ * query i of n stands at position kv_lens[b] - n + i.  causal nonzero: a query
+ * sees the tokens up to its own position; window > 0 (causal only): the last
+ * `window` of those.  Otherwise it sees all kv_lens[b].  Token j lies in page
+ * table[b, j / page]; a page number outside [0, pages) holds nothing, its tokens
+ * are not seen.  A query that sees nothing gives zeros (lse -infinity).
+ *   q [T, Hq, D] of type (APEX4_F16 or APEX4_BF16), ldq; o [T, Hq, D] contiguous, of
+ *   the same type; lse [T, Hq] fp32 or NULL: log of the sum of exp(scale q . k).
+ *   q and o 16-byte aligned, ldq a multiple of 8.
+ *   cu_q [B+1] (ascending; entries are kept within [0, T]), kv_lens [B] (kept
+ *   within [0, cols * page]), table [B, cols]: int32 in device memory.  Rows of q
+ *   that no sequence owns are not read, their o and lse not written.
+ *   max_q, max_kv: what the work is split for, the most queries and cached tokens
+ *   that a sequence is expected to have.  Sequences that have more come out right,
+ *   only slower.
+ *   Products of codes and queries, and of weights and codes, run on the fp16
+ *   matrix units and sum in fp32; a weight p_j
+ *   times the scale of v_j is rounded to fp16, relative to the largest so far.
+ *   Queries and scales that are not finite show in the rows that see them only.
+ *   workspace: at least apex4_kv4_attention_workspace_size() bytes (NULL allowed
+ *   when that is 0; 0 for invalid or empty sizes), 16-byte aligned, caller-owned,
+ *   overwritten; calls that share one race.
+ *   0 <= B <= 65536, 0 <= T <= 2^24 (either 0: no-op), T * Hq < 2^31, Hkv divides Hq, Hq <=
+ *   1024, D 64, 128 or 256, cols * page <= 2^30, max_q and max_kv >= 1, scale finite.
+ * No atomics: the results do not depend on timing.  Asynchronous on `stream`.
+ */
+size_t apex4_kv4_attention_workspace_size(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_q,
+                                          int32_t max_kv);
+apex4_status apex4_kv4_attention(const void* q, int32_t type, int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D,
+                                 int64_t ldq, const int32_t* cu_q, const int32_t* kv_lens, const int32_t* table,
+                                 int64_t cols, const void* k_codes, const float* k_scales, const void* v_codes,
+                                 const float* v_scales, int64_t pages, int32_t page, float scale, int32_t causal,
+                                 int32_t window, int32_t max_q, int32_t max_kv, void* o, float* lse, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

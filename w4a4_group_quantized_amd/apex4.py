@@ -54,6 +54,14 @@ SIGNATURES = {
     "apex4_gemm_e4m3": (_I32, [_P, _P, _P, _P, _I64, _I64, _I64, _I32, _P, _P, _P, ctypes.c_size_t, _P]),
     "apex4_linear_e4m3_workspace_size": (ctypes.c_size_t, [_I64, _I64, _I64]),
     "apex4_linear_e4m3": (_I32, [_P, _I32, _P, _P, _I64, _I64, _I64, _P, _P, _P, ctypes.c_size_t, _P]),
+    "apex4_rope": (_I32, [_P, _I32, _I64, _I32, _I32, _I64, _P, _P, _I32, _I32, ctypes.c_double, _P, _I64, _P]),
+    "apex4_kv4_append": (_I32, [_P, _P, _P, _I32, _I64, _I32, _I32, _I32, _I64, _I64, _I64, _P, _P, _I32, _I32,
+                                ctypes.c_double, _P, _I64, _I32, _P, _P, _P, _P, _P, _P]),
+    "apex4_kv4_read": (_I32, [_P, _P, _P, _P, _I64, _I32, _I32, _I32, _P, _I64, _I32, _P, _P, _P]),
+    "apex4_kv4_attention_workspace_size": (ctypes.c_size_t, [_I64, _I32, _I32, _I32, _I32, _I32, _I32]),
+    "apex4_kv4_attention": (_I32, [_P, _I32, _I64, _I32, _I32, _I32, _I32, _I64, _P, _P, _P, _I64, _P, _P, _P, _P,
+                                   _I64, _I32, ctypes.c_float, _I32, _I32, _I32, _I32, _P, _P, _P,
+                                   ctypes.c_size_t, _P]),
     "apex4_probe_mfma_i8": (_I32, [_I64, _P, ctypes.POINTER(ctypes.c_double), _P]),
     "apex4_probe_mfma_f6": (_I32, [_I64, _P, ctypes.POINTER(ctypes.c_double), _P]),
     "apex4_probe_hbm_read": (_I32, [_P, _I64, _P, ctypes.POINTER(ctypes.c_double), _P]),
@@ -599,6 +607,200 @@ def linear_e4m3(x, qw8, sw, *, want_y32: bool = False, y=None, y32=None, workspa
     _call("apex4_linear_e4m3", dev, x.data_ptr(), code, qw8.data_ptr(), sw.data_ptr(), M, N, K, y.data_ptr(),
           _ptr(y32), _ptr(workspace), 0 if workspace is None else workspace.numel())
     return (y, y32) if want_y32 else y
+
+
+def _rows3(t, name: str, dtype=None, shape=None, device=None) -> int:
+    """Checks rows [T, heads, D] whose heads are contiguous; returns the elements between two of
+    them (parts of a fused projection's output pass as they are)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor (this library has no CPU path)")
+    if t.dim() != 3 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} must have shape {'[T, heads, D]' if shape is None else tuple(shape)}, "
+                         f"got {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
+    (T, H, D), (row, head, one) = t.shape, t.stride()
+    if (one != 1 and D > 1) or (head != D and H > 1) or (row < H * D and T > 1):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return row if T > 1 else H * D
+
+
+def _rotation(positions, inv_freq, T: int, device):
+    """(positions, frequencies, rotated numbers) as the library takes them."""
+    import torch
+    if positions is None or inv_freq is None:
+        raise ValueError("positions and inv_freq belong together")
+    _need(positions, "positions", torch.int64, (T,), device)
+    _need_gpu(inv_freq, "inv_freq", torch.float64, None, device)
+    if inv_freq.dim() != 1:
+        raise ValueError(f"inv_freq must be [R/2], got {tuple(inv_freq.shape)}")
+    return positions.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.shape[0]
+
+
+def rope(x, positions, inv_freq, *, interleaved: bool = False, scale: float = 1.0, out=None):
+    """apex4_rope: rotary positions.  x: float32, float16 or bfloat16 [T, H, D] (a token's heads
+    contiguous), positions int64 [T], inv_freq float64 [R/2]: the first R numbers of every head
+    are turned by positions * inv_freq, as pairs (i, R/2 + i) or, interleaved, (2i, 2i + 1), and
+    multiplied by `scale`.  `out`: where to write, x itself to turn in place (a new contiguous
+    tensor when None)."""
+    import torch
+    ldx = _rows3(x, "x")
+    code = _type_code(x, "x")
+    (T, H, D), dev = x.shape, x.device
+    pos, freq, R = _rotation(positions, inv_freq, T, dev)
+    if out is None:
+        out = torch.empty((T, H, D), dtype=x.dtype, device=dev)
+        ldy = H * D
+    else:
+        ldy = _rows3(out, "out", x.dtype, (T, H, D), dev)
+    _call("apex4_rope", dev, x.data_ptr(), code, T, H, D, ldx, pos, freq, R, int(bool(interleaved)), scale,
+          out.data_ptr(), ldy)
+    return out
+
+
+def kv4_cache(pages: int, kv_heads: int, head_dim: int, page: int = 64, device="cuda"):
+    """An empty 4-bit cache of `pages` pages of `page` tokens: (k_codes, k_scales, v_codes,
+    v_scales), the tensors that kv4_append, kv4_read and kv4_attention take as `cache`."""
+    import torch
+    if head_dim % 32 or page % 16:
+        raise ValueError(f"head_dim must be 64, 128 or 256 and page a power of two from 16, got {head_dim, page}")
+    codes = {"dtype": torch.uint8, "device": device}
+    return (torch.zeros((pages, kv_heads, page, head_dim // 2), **codes),
+            torch.zeros((pages, kv_heads, page), device=device),
+            torch.zeros((pages, kv_heads, page // 16, 8 * head_dim), **codes),
+            torch.zeros((pages, kv_heads, page), device=device))
+
+
+def _kv4(cache):
+    """((k_codes, k_scales, v_codes, v_scales) pointers, pages, page, heads, head dim, device)"""
+    import torch
+    k, ks, v, vs = cache
+    if k.dim() != 4:
+        raise ValueError(f"k_codes must be [pages, heads, page, D/2], got {tuple(k.shape)}")
+    (pages, heads, page, half), dev = k.shape, k.device
+    _need(k, "k_codes", torch.uint8, (pages, heads, page, half), dev)
+    _need(ks, "k_scales", torch.float32, (pages, heads, page), dev)
+    _need(v, "v_codes", torch.uint8, (pages, heads, page // 16, 16 * half), dev)
+    _need(vs, "v_scales", torch.float32, (pages, heads, page), dev)
+    return (k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr()), pages, page, heads, 2 * half, dev
+
+
+def kv4_append(cache, k, v, slots, *, positions=None, inv_freq=None, interleaved: bool = False,
+               rope_scale: float = 1.0, q=None, q_out=None):
+    """apex4_kv4_append: stores keys and values (float16 or bfloat16 [T, Hkv, D]) at slots int64
+    [T] (page * page size + place; negative ones are not stored, the others must differ) of a
+    4-bit cache.  With positions and inv_freq (as in `rope`) the keys are turned on the way, and
+    so are the queries q [T, Hq, D], which are returned (in q_out where it is given; None
+    without q)."""
+    import torch
+    ptrs, pages, page, heads, D, dev = _kv4(cache)
+    ldk = _rows3(k, "k", None, None, dev)
+    T, dtype = k.shape[0], k.dtype
+    if tuple(k.shape[1:]) != (heads, D):
+        raise ValueError(f"k must be [T, {heads}, {D}], got {tuple(k.shape)}")
+    code = _type_code(k, "k", _HALVES)
+    ldv = _rows3(v, "v", dtype, (T, heads, D), dev)
+    _need(slots, "slots", torch.int64, (T,), dev)
+    pos = freq = q_ptr = out_ptr = None
+    R = Hq = ldq = 0
+    if positions is not None or inv_freq is not None:
+        pos, freq, R = _rotation(positions, inv_freq, T, dev)
+    if q is not None:
+        if q.dim() != 3 or pos is None:
+            raise ValueError("q must be [T, Hq, D], and is turned: it needs positions and inv_freq")
+        Hq = q.shape[1]
+        ldq = _rows3(q, "q", dtype, (T, Hq, D), dev)
+        if q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=dtype, device=dev)
+        else:
+            _need(q_out, "q_out", dtype, (T, Hq, D), dev)
+        q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _call("apex4_kv4_append", dev, q_ptr, k.data_ptr(), v.data_ptr(), code, T, Hq, heads, D, ldq, ldk, ldv, pos, freq,
+          R, int(bool(interleaved)), rope_scale, slots.data_ptr(), pages, page, *ptrs, out_ptr)
+    return q_out
+
+
+def kv4_read(cache, slots, dtype=None, out=None):
+    """apex4_kv4_read: the cached tokens at slots int64 [T] as (k, v) [T, Hkv, D] of `dtype`
+    (float32, float16, the default, or bfloat16); negative slots give zeros.  `out`: (k, v) to
+    write."""
+    import torch
+    dtype = torch.float16 if dtype is None else dtype
+    ptrs, pages, page, heads, D, dev = _kv4(cache)
+    _need_gpu(slots, "slots", torch.int64, None, dev)
+    if slots.dim() != 1:
+        raise ValueError(f"slots must be [T], got {tuple(slots.shape)}")
+    T = slots.shape[0]
+    if out is None:
+        k = torch.empty((T, heads, D), dtype=dtype, device=dev)
+        v = torch.empty((T, heads, D), dtype=dtype, device=dev)
+    else:
+        k, v = out
+        _need(k, "k", dtype, (T, heads, D), dev)
+        _need(v, "v", dtype, (T, heads, D), dev)
+    _call("apex4_kv4_read", dev, *ptrs, pages, page, heads, D, slots.data_ptr(), T, _type_code(k, "k"), k.data_ptr(),
+          v.data_ptr())
+    return k, v
+
+
+def kv4_attention_workspace_size(T: int, B: int, Hq: int, Hkv: int, D: int, max_q: int, max_kv: int) -> int:
+    """Bytes that `kv4_attention` takes on the current device."""
+    return int(lib().apex4_kv4_attention_workspace_size(T, B, Hq, Hkv, D, max_q, max_kv))
+
+
+def kv4_attention(q, cache, table, kv_lens, cu_q=None, *, scale: float | None = None, causal: bool = True,
+                  window: int = 0, max_q: int | None = None, max_kv: int | None = None, want_lse: bool = False,
+                  out=None, lse=None, workspace=None):
+    """apex4_kv4_attention: attention of the newest tokens of B sequences over a 4-bit cache.
+    q: float16 or bfloat16 [T, Hq, D]; table: int32 [B, cols] page numbers; kv_lens: int32 [B],
+    cached tokens with the queries' own; cu_q: int32 [B + 1], where each sequence's queries
+    begin (None: one query a sequence).  scale: 1 / sqrt(D) when None; window: of the last
+    `window` tokens only (0: all).  max_q, max_kv: the most queries and tokens that a sequence
+    is expected to have, for the split of the work only (by default ceil(T / B), and what the
+    table can hold).  Returns o [T, Hq, D] (rows that no sequence owns are not written), or
+    (o, lse [T, Hq] float32) with want_lse."""
+    import torch
+    ptrs, pages, page, heads, D, dev = _kv4(cache)
+    ldq = _rows3(q, "q", None, None, dev)
+    T, Hq = q.shape[:2]
+    if q.shape[2] != D:
+        raise ValueError(f"q must be [T, Hq, {D}], got {tuple(q.shape)}")
+    code = _type_code(q, "q", _HALVES)
+    if table.dim() != 2:
+        raise ValueError(f"table must be [B, cols], got {tuple(table.shape)}")
+    B, cols = table.shape
+    _need(table, "table", torch.int32, (B, cols), dev)
+    _need(kv_lens, "kv_lens", torch.int32, (B,), dev)
+    if cu_q is not None:
+        _need(cu_q, "cu_q", torch.int32, (B + 1,), dev)
+    # caller buffers are checked before anything is allocated
+    if out is not None:
+        _need(out, "out", q.dtype, (T, Hq, D), dev)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (T, Hq), dev)
+    if workspace is not None:
+        _need_gpu(workspace, "workspace", torch.uint8, None, dev)
+    if max_q is None:
+        max_q = 1 if cu_q is None else max(1, -(-T // max(B, 1)))
+    if max_kv is None:
+        max_kv = max(1, cols * page)
+    if max(max_q, max_kv, window) >> 31 or min(max_q, max_kv, window) < 0:
+        raise ValueError(f"max_q, max_kv and window must fit 31 bits, got {max_q, max_kv, window}")
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
+    if want_lse and lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    if workspace is None:
+        need = _size("apex4_kv4_attention_workspace_size", dev, T, B, Hq, heads, D, max_q, max_kv)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    _call("apex4_kv4_attention", dev, q.data_ptr(), code, T, B, Hq, heads, D, ldq, _ptr(cu_q), kv_lens.data_ptr(),
+          table.data_ptr(), cols, *ptrs, pages, page, D ** -0.5 if scale is None else scale, int(bool(causal)), window,
+          max_q, max_kv, out.data_ptr(), _ptr(lse), _ptr(workspace), 0 if workspace is None else workspace.numel())
+    return (out, lse) if want_lse else out
 
 
 def _probe(name: str, *args):
