@@ -484,7 +484,7 @@ apex4_status apex4_linear_e4m3(const void* x, int32_t x_type, const void* qw8, c
  *   are not allowed).  x and y 16-byte aligned, ldx and ldy multiples of 8.
  *   positions [T] int64 (beyond +-(2^31 - 1): taken as that), freqs [R/2] fp64,
  *   8-byte aligned.  Scaled frequencies (longer contexts) are the caller's.
- *   0 <= T <= 2^24 (0: no-op), 1 <= H <= 1024, D and R multiples of 16,
+ *   0 <= T < 2^24 (0: no-op), 1 <= H <= 1024, D and R multiples of 16,
  *   16 <= R <= D <= 1024; scale finite.  Asynchronous on `stream`.
  */
 apex4_status apex4_rope(const void* x, int32_t type, int64_t T, int32_t H, int32_t D, int64_t ldx,
@@ -518,7 +518,7 @@ apex4_status apex4_rope(const void* x, int32_t type, int64_t T, int32_t H, int32
  *   (then R 0 and no queries): keys are stored as they are.
  *   q [T, Hq, D] with ldq, q_out [T, Hq, D] contiguous; or both NULL and Hq 0.
  *   q_out == q with ldq == Hq * D turns in place.
- *   Pointers of rows 16-byte aligned, strides multiples of 8; 0 <= T <= 2^24 (0:
+ *   Pointers of rows 16-byte aligned, strides multiples of 8; 0 <= T < 2^24 (0:
  *   no-op), Hq, Hkv <= 1024, pages < 2^31.
  * What is not stored keeps its bytes.  Asynchronous on `stream`.
  */
@@ -532,7 +532,7 @@ apex4_status apex4_kv4_append(const void* q, const void* k, const void* v, int32
  * apex4_kv4_read: the values c * s (rounded to `type`: APEX4_F32, APEX4_F16 or
  * APEX4_BF16) of T cached tokens, k and v [T, Hkv, D], 16-byte aligned.  slots
  * [T] int64, in any order, repeated or not; a slot that is negative or behind
- * the last page gives zeros.  Limits as above, T * Hkv * D < 2^38.
+ * the last page gives zeros.  Limits as above, T * Hkv * D < 2^36.
  */
 apex4_status apex4_kv4_read(const void* k_codes, const float* k_scales, const void* v_codes, const float* v_scales,
                             int64_t pages, int32_t page, int32_t Hkv, int32_t D, const int64_t* slots, int64_t T,
@@ -559,14 +559,15 @@ apex4_status apex4_kv4_read(const void* k_codes, const float* k_scales, const vo
  *   that a sequence is expected to have.  Sequences that have more come out right,
  *   only slower.
  *   Products of codes and queries, and of weights and codes, run on the fp16
- *   matrix units and sum in fp32; a weight p_j
- *   times the scale of v_j is rounded to fp16, relative to the largest so far.
+ *   matrix units and sum in fp32; a weight p_j times the scale of v_j is rounded to
+ *   fp16, relative to the largest so far.  A value's scale below 2^-80 counts as
+ *   2^-80; |scale| times a key's scale has to stay below 2^100.
  *   Queries and scales that are not finite show in the rows that see them only.
  *   workspace: at least apex4_kv4_attention_workspace_size() bytes (NULL allowed
  *   when that is 0; 0 for invalid or empty sizes), 16-byte aligned, caller-owned,
  *   overwritten; calls that share one race.
- *   0 <= B <= 65536, 0 <= T <= 2^24 (either 0: no-op), T * Hq < 2^31, Hkv divides Hq, Hq <=
- *   1024, D 64, 128 or 256, cols * page <= 2^30, max_q and max_kv >= 1, scale finite.
+ *   0 <= B <= 65536, 0 <= T < 2^24 (either 0: no-op), T * Hq < 2^31, B * Hkv < 2^23, Hkv
+ *   divides Hq, Hq <= 1024, D 64, 128 or 256, cols * page <= 2^30, max_q and max_kv >= 1, scale finite.
  * No atomics: the results do not depend on timing.  Asynchronous on `stream`.
  */
 size_t apex4_kv4_attention_workspace_size(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_q,

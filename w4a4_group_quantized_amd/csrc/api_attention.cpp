@@ -13,7 +13,7 @@ namespace {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-constexpr int64_t kMaxTokens = int64_t(1) << 24;     // a launch has fewer than 2^32 threads
+constexpr int64_t kMaxTokens = (int64_t(1) << 24) - 1;      // a launch has fewer than 2^32 threads
 constexpr int64_t kMaxStride = int64_t(1) << 32;
 constexpr int32_t kMaxHeads = 1024;
 
@@ -70,7 +70,8 @@ bool cache_aligned(const apex4::Kv4Cache& c)
 apex4_status attention_sizes(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_q, int32_t max_kv)
 {
     if (!heads_ok(T, Hq) || B < 0 || B > 65536 || Hkv < 1 || Hq % Hkv != 0 || D < 1) return APEX4_ERR_INVALID_ARG;
-    if (T * Hq >= (int64_t(1) << 31) || max_q < 1 || max_kv < 1) return APEX4_ERR_INVALID_ARG;
+    if (T * Hq >= (int64_t(1) << 31) || (int64_t)B * Hkv >= (int64_t(1) << 23) || max_q < 1 || max_kv < 1)
+        return APEX4_ERR_INVALID_ARG;
     return head_dim_ok(D) ? APEX4_OK : APEX4_ERR_UNSUPPORTED;
 }
 
@@ -83,7 +84,9 @@ apex4::Kv4AttentionProblem attention_problem(int64_t T, int32_t B, int32_t Hq, i
     p.Hq = Hq;
     p.cache.Hkv = Hkv;
     p.cache.D = D;
-    p.max_q = static_cast<int32_t>(std::min<int64_t>(max_q, std::max<int64_t>(T, 1)));
+    // (no fewer than the mean, no more than there are)
+    const int64_t mean = B > 0 ? (T + B - 1) / B : 1;
+    p.max_q = static_cast<int32_t>(std::max<int64_t>(1, std::min<int64_t>(std::max<int64_t>(max_q, mean), T)));
     p.max_kv = std::min(max_kv, 1 << 30);
     return p;
 }
@@ -161,7 +164,7 @@ apex4_status apex4_kv4_read(const void* k_codes, const float* k_scales, const vo
 {
     const apex4_status sizes = cache_sizes(pages, page, Hkv, D);
     if (sizes != APEX4_OK) return sizes;
-    if (T < 0 || T > kMaxTokens || T * Hkv * D >= (int64_t(1) << 38)) return APEX4_ERR_INVALID_ARG;
+    if (T < 0 || T > kMaxTokens || T * Hkv * D >= (int64_t(1) << 36)) return APEX4_ERR_INVALID_ARG;
     if (type != APEX4_F32 && !half_type(type)) return APEX4_ERR_UNSUPPORTED;
     if (T == 0) return APEX4_OK;
     apex4::Kv4ReadProblem p{};

@@ -1,107 +1,615 @@
 // Attention over the 4-bit key/value cache (include/apex4.h:
-// apex4_kv4_attention), one wave a query head.
-#include <climits>
+// apex4_kv4_attention).
+//
+// A wave takes 16 RT rows (a row is one query head of one token; the heads that
+// share a key head are rows beside each other) and 64 cached tokens at a time:
+//
+//     S = K Q^T   tokens x rows    v_mfma_f32_16x16x32_f16
+//     t = S s_k scale log2(e) + log2(s_v),  w = 2^(t - M)
+//     O += V^T w  numbers x rows   the same instruction, w rounded to fp16
+//     l += w / s_v
+//
+// M is the row's running maximum of t, so the weights that the matrix unit sees
+// carry the values' scales and the largest of them is near 1 whatever those are;
+// M moves only when a tile exceeds it by 2^8 (fp16 holds that), which keeps the
+// rescaling of O out of most tiles.  l and M are fp32.
+//
+// Codes go to the matrix unit as they lie: the nibble u = c + 8 in the lowest
+// bits of an fp16 is the subnormal number u 2^-24, in bits 4..7 u 2^-20 (the
+// instruction takes subnormal operands exactly), so eight codes cost five
+// instructions.  Where u is a key's, the query's number beside it holds the other
+// 2^-4 and the accumulators start at -8 sum(q); where it is a value's, the factor
+// goes into the end, and 8 sum(w) comes from one more matrix instruction whose
+// first operand is 8 everywhere.
+//
+// Operands come straight from memory in the order that the instruction wants:
+// a lane's 32 numbers of a key are D/8 neighbouring bytes, and the values' layout
+// puts a lane's 4 tokens of all its numbers side by side.  S leaves the matrix
+// unit with 4 tokens of one row in a lane, which is how the second product wants
+// w: nothing goes through LDS but a token's three factors.
+#include <algorithm>
 
 #include "attention.h"
+#include "layers.h"
 #include "rotary.h"
 
 namespace apex4 {
 namespace {
 
-template <bool BF16, int D>
-__global__ __launch_bounds__(64) void row_kernel(Kv4AttentionProblem p, int rows)
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+typedef float float2v __attribute__((ext_vector_type(2)));
+typedef float float4v __attribute__((ext_vector_type(4)));
+
+constexpr int kWaves = 4;
+constexpr int64_t kMaxBlocks = (1 << 24) - 1;
+constexpr float kTiny = 0x1p-80f;      // the least scale of values: 2^8 / kTiny, 2^30 times, stays finite
+constexpr float kLazy = 8.0f;
+
+struct Plan {
+    int tiles;          // row tiles of a sequence and key head that the grid holds (kernels stride over more)
+    int nsplit;         // shares of the cached tokens
+    int chunk;          // tokens of a share but the last
+    float* part_o;      // [nsplit, T * Hq, D], shares' sums relative to their M
+    float2* part_ml;    // [nsplit, T * Hq] of (M, l)
+};
+
+__device__ inline half8 mfma_operand(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
-    __shared__ float qs[D];
-    __shared__ float ps[64];
-    const int lane = threadIdx.x;
-    const int row0 = blockIdx.x % rows, h = blockIdx.x / rows % p.Hq, b = blockIdx.x / rows / p.Hq;
-    const Kv4Cache& c = p.cache;
-    int64_t q0 = b, q1 = b + 1;
+    return __builtin_bit_cast(half8, make_uint4(a, b, c, d));
+}
+
+__device__ inline float4v mfma(half8 a, half8 b, float4v c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+
+// over the four lanes that hold a row
+__device__ inline float row_max(float x)
+{
+    x = fmaxf(x, __shfl_xor(x, 16));
+    return fmaxf(x, __shfl_xor(x, 32));
+}
+__device__ inline float row_sum(float x)
+{
+    x += __shfl_xor(x, 16);
+    return x + __shfl_xor(x, 32);
+}
+
+// The numbers of one row and its place in the batch.
+struct Sequence {
+    int b;
+    int64_t q0;         // its first query
+    int n, kv;          // queries, cached tokens
+};
+
+__device__ inline Sequence sequence(const Kv4AttentionProblem& p, int b)
+{
+    Sequence s{b, b, 1, 0};
     if (p.cu_q) {
-        q0 = max(0, p.cu_q[b]);
-        q1 = min(p.T, (int64_t)p.cu_q[b + 1]);
+        const int64_t from = max(0, p.cu_q[b]), to = min(p.T, (int64_t)p.cu_q[b + 1]);
+        s.q0 = from;
+        s.n = (int)max((int64_t)0, to - from);
     }
-    const int64_t len = q1 - q0;
-    const int64_t kv = min((int64_t)max(0, p.kv_lens[b]), p.cols << c.shift);
-    const int g = h / (p.Hq / c.Hkv);
-    for (int64_t i = row0; i < len; i += rows) {
-        const int64_t at = ((q0 + i) * p.Hq + h) * D;
-        const uint16_t* q = static_cast<const uint16_t*>(p.q) + (q0 + i) * p.ldq + (int64_t)h * D;
-        __syncthreads();
-        for (int d = lane; d < D; d += 64) qs[d] = e4m3::from16<BF16>(q[d]) * p.scale;
-        __syncthreads();
-        const int64_t pos = kv - len + i;
-        const int64_t hi = p.causal ? min(kv, pos + 1) : kv;
-        const int64_t lo = p.window ? max((int64_t)0, pos - p.window + 1) : 0;
-        float m = -INFINITY, l = 0.0f, acc[D / 64] = {};
-        for (int64_t t0 = lo & ~63ll; t0 < hi; t0 += 64) {
-            const int64_t t = t0 + lane;
-            const int64_t pg = t < kv ? p.table[b * p.cols + (t >> c.shift)] : -1;
-            const bool seen = t >= lo && t < hi && pg >= 0 && pg < c.pages;
-            float s = -INFINITY, vs = 0.0f;
-            if (seen) {
-                const int64_t r = ((pg * c.Hkv + g) << c.shift) + (t & (c.page - 1));
-                const uint8_t* k = c.k_codes + r * (D / 2);
-                float dot = 0.0f;
-                for (int d = 0; d < D / 2; ++d) {
-                    dot = fmaf(qs[2 * d], (float)((int)(k[d] & 15) - 8), dot);
-                    dot = fmaf(qs[2 * d + 1], (float)((int)(k[d] >> 4) - 8), dot);
-                }
-                s = dot * c.k_scales[r];
-                vs = c.v_scales[r];
+    s.kv = (int)min((int64_t)max(0, p.kv_lens[b]), p.cols << p.cache.shift);
+    return s;
+}
+
+// the tokens [lo, hi) that query i sees
+__device__ inline int seen_hi(const Kv4AttentionProblem& p, const Sequence& s, int i)
+{
+    return p.causal ? max(0, s.kv - s.n + i + 1) : s.kv;
+}
+__device__ inline int seen_lo(const Kv4AttentionProblem& p, const Sequence& s, int i)
+{
+    return p.window ? max(0, s.kv - s.n + i + 1 - p.window) : 0;
+}
+
+// What a wave holds of its rows.
+template <int D, int RT>
+struct Rows {
+    half8 q[RT][D / 32];
+    float4v bias[RT];       // -8 sum(q) 2^-24
+    float unit[RT];         // the power of two that was taken out of the query
+    int lo[RT], hi[RT];
+    float4v o[RT][D / 16];  // sums of w u, 2^-24 (even tiles of 16 numbers) and 2^-20
+    float4v w[RT];          // 8 sum(w) 2^-24
+    float m[RT], l[RT];
+};
+
+// numbers of a key that lane quad `quad` holds in matrix instruction f
+template <int D>
+__device__ inline int key_number(int quad, int f)
+{
+    if (D == 64) return 16 * quad + 8 * f;
+    return 128 * (f / 4) + 32 * quad + 8 * (f % 4);
+}
+
+template <bool BF16, int D, int RT>
+__device__ inline void load_rows(const Kv4AttentionProblem& p, const Sequence& s, int g, int row0, Rows<D, RT>& r)
+{
+    const int lane = threadIdx.x & 63, quad = lane >> 4;
+    const int share = p.Hq / p.cache.Hkv;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const int row = row0 + 16 * rt + (lane & 15);
+        const bool live = row < s.n * share;
+        const int i = live ? row / share : 0, h = live ? row - i * share : 0;
+        const uint16_t* q = static_cast<const uint16_t*>(p.q) + (s.q0 + i) * p.ldq + (int64_t)(g * share + h) * D;
+        float x[D / 4], most = 0.0f;
+#pragma unroll
+        for (int f = 0; f < D / 32; ++f) {
+            if (live) {
+                rotary::load8<BF16 ? 2 : 1>(q, key_number<D>(quad, f), x + 8 * f);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[8 * f + k] = 0.0f;
             }
-            float top = s;
-            for (int o = 32; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
-            const float next = fmaxf(m, top);
-            const float from = next == -INFINITY ? 0.0f : next, old = expf(m - from);
-            const float w = seen ? expf(s - from) : 0.0f;
-            float sum = w;
-            for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
-            l = l * old + sum;
-            m = next;
-            __syncthreads();
-            ps[lane] = seen ? w * vs : 0.0f;
-            __syncthreads();
-            for (int e = 0; e < D / 64; ++e) acc[e] *= old;
-            for (int k = 0; k < 64; ++k) {
-                const int64_t tk = t0 + k;
-                if (tk < lo || tk >= hi) continue;
-                const int64_t pk = p.table[b * p.cols + (tk >> c.shift)];
-                if (pk < 0 || pk >= c.pages) continue;
-                const int off = (int)(tk & (c.page - 1));
-                const uint8_t* v = c.v_codes + (pk * c.Hkv + g) * c.page * (D / 2) + (off >> 4) * 8 * D;
-                for (int e = 0; e < D / 64; ++e) {
-                    const int d = lane + 64 * e;
-                    const int by = v[(((off >> 2) & 3) * 16 + d % 16) * (D / 8) + d / 32 * 4 + (off & 3)];
-                    acc[e] = fmaf(ps[k], (float)(((d & 16 ? by >> 4 : by) & 15) - 8), acc[e]);
-                }
-            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) most = fmaxf(most, fabsf(x[8 * f + k]));
         }
-        for (int e = 0; e < D / 64; ++e)
-            static_cast<uint16_t*>(p.out)[at + lane + 64 * e] = e4m3::to16<BF16>(l == 0.0f ? 0.0f : acc[e] / l);
-        if (p.lse && lane == 0) p.lse[(q0 + i) * p.Hq + h] = l == 0.0f ? -INFINITY : m + logf(l);
+        most = row_max(most);
+        // rows outside fp16's comfortable range are brought to 16..32 by a power of two
+        int e = 0;
+        if (!(most >= 0x1p-6f && most < 0x1p14f) && most > 0.0f && most < INFINITY) e = 5 - __builtin_amdgcn_frexp_expf(most);
+        r.unit[rt] = __builtin_amdgcn_ldexpf(1.0f, -e);
+        r.bias[rt] = float4v{};
+#pragma unroll
+        for (int f = 0; f < D / 32; ++f) {
+            half8 v;
+            constexpr int order[8] = {0, 4, 1, 5, 2, 6, 3, 7};
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[k] = (_Float16)__builtin_amdgcn_ldexpf(x[8 * f + order[k]], k & 2 ? e - 4 : e);
+            r.q[rt][f] = v;
+            r.bias[rt] = mfma(mfma_operand(0x80088008, 0x80808080, 0x80088008, 0x80808080), v, r.bias[rt]);
+        }
+        r.lo[rt] = live ? seen_lo(p, s, i) : 0;
+        r.hi[rt] = live ? seen_hi(p, s, i) : 0;
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t) r.o[rt][t] = float4v{};
+        r.w[rt] = float4v{};
+        r.m[rt] = -INFINITY;
+        r.l[rt] = 0.0f;
     }
 }
 
-template <bool BF16>
-hipError_t rows(const Kv4AttentionProblem& p, hipStream_t stream)
+// Codes of 64 tokens as they come from memory, 16 tokens a row of the array.
+template <int D>
+struct Codes {
+    uint32_t w[4][D / 32];
+};
+
+template <int D>
+__device__ inline void load_codes(Codes<D>& c, int s, const uint8_t* p)
 {
-    const unsigned blocks = (unsigned)((int64_t)p.B * p.Hq * p.max_q);
-    switch (p.cache.D) {
-    case 64: row_kernel<BF16, 64><<<blocks, 64, 0, stream>>>(p, p.max_q); break;
-    case 128: row_kernel<BF16, 128><<<blocks, 64, 0, stream>>>(p, p.max_q); break;
-    default: row_kernel<BF16, 256><<<blocks, 64, 0, stream>>>(p, p.max_q); break;
+    if (D == 64) {
+        const uint2 a = *reinterpret_cast<const uint2*>(p);
+        c.w[s][0] = a.x, c.w[s][1] = a.y;
+    } else {
+#pragma unroll
+        for (int k = 0; k < D / 128; ++k) {
+            const uint4 a = *reinterpret_cast<const uint4*>(p + (D / 128 == 2 ? 64 * k : 0));
+            c.w[s][4 * k] = a.x, c.w[s][4 * k + 1] = a.y, c.w[s][4 * k + 2] = a.z, c.w[s][4 * k + 3] = a.w;
+        }
+    }
+}
+
+// (a lane's values are D/8 neighbouring bytes)
+template <int D>
+__device__ inline void load_values(Codes<D>& c, int s, const uint8_t* p)
+{
+    if (D == 256) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint4 a = *reinterpret_cast<const uint4*>(p + 16 * k);
+            c.w[s][4 * k] = a.x, c.w[s][4 * k + 1] = a.y, c.w[s][4 * k + 2] = a.z, c.w[s][4 * k + 3] = a.w;
+        }
+    } else {
+        load_codes<D>(c, s, p);
+    }
+}
+
+constexpr uint32_t kLow = 0x000F000F, kHigh = 0x00F000F0;
+
+// The tokens [from, to) in tiles of 64, `step` apart; `lds`: 192 floats of the wave.
+template <int D, int RT>
+__device__ inline void attend(const Kv4AttentionProblem& p, const Sequence& s, int g, int from, int to, int step,
+                              int lo_max, int hi_min, Rows<D, RT>& r, float* lds)
+{
+    const Kv4Cache& c = p.cache;
+    const int lane = threadIdx.x & 63, quad = lane >> 4;
+    const int32_t* table = p.table + s.b * p.cols;
+    const int last = (int)p.cols - 1;
+    const float factor = p.scale * 1.44269504f * 0x1p24f;
+    const int key_at = (lane & 15) * (D / 2) + quad * (D == 64 ? 8 : 16), value_at = lane * (D / 8);
+    bool scaled = false;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) scaled |= r.unit[rt] != 1.0f;
+    scaled = __any(scaled);
+    if (from >= to) return;
+
+    // lane's token of the tile at t: its row in the cache (row 0 where there is none)
+    int page = 0;
+    int64_t row = 0;
+    bool valid = false;
+    Codes<D> k, v;
+    float ks = 0.0f, vs = 0.0f;
+    const auto look = [&](int t) { page = table[min((t + lane) >> c.shift, last)]; };
+    const auto locate = [&](int t) {
+        valid = t + lane < to && page >= 0 && page < c.pages;
+        row = valid ? (((int64_t)page * c.Hkv + g) << c.shift) + ((t + lane) & (c.page - 1)) : 0;
+    };
+    const auto base = [&](int sub) {
+        const uint32_t a = __builtin_amdgcn_readlane((uint32_t)row, 16 * sub);
+        const uint32_t b = __builtin_amdgcn_readlane((uint32_t)(row >> 32), 16 * sub);
+        return (int64_t)((uint64_t)b << 32 | a) * (D / 2);
+    };
+    const auto load_k = [&]() {
+        ks = c.k_scales[row];
+#pragma unroll
+        for (int sub = 0; sub < 4; ++sub) load_codes<D>(k, sub, c.k_codes + base(sub) + key_at);
+    };
+    const auto load_v = [&]() {
+        vs = c.v_scales[row];
+#pragma unroll
+        for (int sub = 0; sub < 4; ++sub) load_values<D>(v, sub, c.v_codes + base(sub) + value_at);
+    };
+    look(from);
+    locate(from);
+    load_k();
+    load_v();
+    look(from + step);
+
+    for (int t0 = from; t0 < to; t0 += step) {
+        // the tile's factors of the tokens, one token a lane, to all lanes
+        const float vsc = vs < kTiny ? kTiny : vs;
+        lds[lane] = valid ? ks * factor : 0.0f;
+        lds[64 + lane] = valid ? __builtin_amdgcn_logf(vsc) : -INFINITY;
+        lds[128 + lane] = valid ? __builtin_amdgcn_rcpf(vsc) : 0.0f;
+        const bool edge = t0 + 64 > hi_min || t0 < lo_max || !__all(valid);
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+
+        float4v x[RT][4];
+#pragma unroll
+        for (int sub = 0; sub < 4; ++sub) {
+#pragma unroll
+            for (int f = 0; f < D / 32; ++f) {
+                const uint32_t u = k.w[sub][f], u8 = u >> 8;
+                const half8 a = mfma_operand(u & kLow, u & kHigh, u8 & kLow, u8 & kHigh);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) x[rt][sub] = mfma(a, r.q[rt][f], f == 0 ? r.bias[rt] : x[rt][sub]);
+            }
+        }
+        locate(t0 + step);
+        load_k();
+
+        half8 w[RT][2];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            if (scaled) {
+#pragma unroll
+                for (int sub = 0; sub < 4; ++sub) x[rt][sub] *= r.unit[rt];
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int sub = 0; sub < 4; ++sub) {
+                const float4v kf = *reinterpret_cast<const float4v*>(lds + 16 * sub + 4 * quad);
+                const float4v ls = *reinterpret_cast<const float4v*>(lds + 64 + 16 * sub + 4 * quad);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[rt][sub][i] = fmaf(x[rt][sub][i], kf[i], ls[i]);
+                if (edge) {
+                    const int t = t0 + 16 * sub + 4 * quad;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (t + i >= r.hi[rt] || t + i < r.lo[rt] || ls[i] == -INFINITY) x[rt][sub][i] = -INFINITY;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = fmaxf(top, x[rt][sub][i]);
+            }
+            top = row_max(top);
+            if (__any(top > r.m[rt] + kLazy)) {
+                const float m = top > r.m[rt] + kLazy ? top : r.m[rt];
+                const float old = m == r.m[rt] ? 1.0f : __builtin_amdgcn_exp2f(r.m[rt] - m);
+                r.m[rt] = m;
+                r.l[rt] *= old;
+                r.w[rt] *= old;
+#pragma unroll
+                for (int t = 0; t < D / 16; ++t) r.o[rt][t] *= old;
+            }
+            const float m = r.m[rt] == -INFINITY ? 0.0f : r.m[rt];
+            uint32_t packed[8];
+#pragma unroll
+            for (int sub = 0; sub < 4; ++sub) {
+                const float4v iv = *reinterpret_cast<const float4v*>(lds + 128 + 16 * sub + 4 * quad);
+                float e[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    e[i] = __builtin_amdgcn_exp2f(x[rt][sub][i] - m);
+                    // (what a row does not see may have a NaN for its scale)
+                    const float back = edge && x[rt][sub][i] == -INFINITY ? 0.0f : iv[i];
+                    r.l[rt] = fmaf(e[i], back, r.l[rt]);
+                }
+                // (codes of tokens 0 and 2, and 1 and 3, share a register)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    packed[2 * sub + i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((float2v{e[i], e[i + 2]}), half2v));
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                w[rt][i] = mfma_operand(packed[4 * i], packed[4 * i + 1], packed[4 * i + 2], packed[4 * i + 3]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+                r.w[rt] = mfma(mfma_operand(0x00080008, 0x00080008, 0x00080008, 0x00080008), w[rt][i], r.w[rt]);
+#pragma unroll
+            for (int n = 0; n < D / 32; ++n) {
+                const uint32_t a = v.w[2 * i][n], a8 = a >> 8, b = v.w[2 * i + 1][n], b8 = b >> 8;
+                const half8 even = mfma_operand(a & kLow, a8 & kLow, b & kLow, b8 & kLow);
+                const half8 odd = mfma_operand(a & kHigh, a8 & kHigh, b & kHigh, b8 & kHigh);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    r.o[rt][2 * n] = mfma(even, w[rt][i], r.o[rt][2 * n]);
+                    r.o[rt][2 * n + 1] = mfma(odd, w[rt][i], r.o[rt][2 * n + 1]);
+                }
+            }
+        }
+        load_v();
+        look(t0 + 2 * step);
+    }
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) r.l[rt] = row_sum(r.l[rt]);
+}
+
+// numbers 16 t + 4 quad .. + 3 of a lane's row, times `by`
+template <int D, int RT>
+__device__ inline float4v row_values(const Rows<D, RT>& r, int rt, int t, float by)
+{
+    const float back = (t & 1 ? 16.0f : 1.0f) * r.w[rt][0], unit = by * (t & 1 ? 0x1p20f : 0x1p24f);
+    return (r.o[rt][t] - back) * unit;
+}
+
+template <bool BF16>
+__device__ inline void store4(void* out, int64_t at, float4v v)
+{
+    uint2 w;
+    w.x = e4m3::to16<BF16>(v[0]) | (uint32_t)e4m3::to16<BF16>(v[1]) << 16;
+    w.y = e4m3::to16<BF16>(v[2]) | (uint32_t)e4m3::to16<BF16>(v[3]) << 16;
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = w;
+}
+
+__device__ inline float log_sum(float m, float l) { return l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.693147181f; }
+
+// Many rows: every wave has rows of its own and walks all the tokens they see.
+template <bool BF16, int D, int RT>
+__global__ __launch_bounds__(256, 2) void rows_kernel(Kv4AttentionProblem p, Plan plan)
+{
+    __shared__ __attribute__((aligned(16))) float lds[kWaves][192];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    int x = blockIdx.x;
+    const int g = x % p.cache.Hkv;
+    x /= p.cache.Hkv;
+    const int first = x % plan.tiles;
+    const Sequence s = sequence(p, x / plan.tiles);
+    const int share = p.Hq / p.cache.Hkv, all = s.n * share, tiles = (all + 16 * RT * kWaves - 1) / (16 * RT * kWaves);
+    for (int k = first; k < tiles; k += plan.tiles) {
+        // (the last rows see the most tokens: first)
+        const int row0 = ((tiles - 1 - k) * kWaves + wave) * 16 * RT;
+        if (row0 >= all) continue;
+        Rows<D, RT> r;
+        load_rows<BF16, D, RT>(p, s, g, row0, r);
+        const int i0 = row0 / share, i1 = min(row0 + 16 * RT - 1, all - 1) / share;
+        attend<D, RT>(p, s, g, seen_lo(p, s, i0) & ~63, seen_hi(p, s, i1), 64, seen_lo(p, s, i1), seen_hi(p, s, i0), r,
+                      lds[wave]);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            const int row = row0 + 16 * rt + (lane & 15);
+            if (row >= all) continue;
+            const int i = row / share;
+            const int64_t at = (s.q0 + i) * p.Hq + g * share + (row - i * share);
+            const float by = r.l[rt] == 0.0f ? 0.0f : 1.0f / r.l[rt];
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t)
+                store4<BF16>(p.out, at * D + 16 * t + 4 * (lane >> 4), row_values(r, rt, t, by));
+            if (p.lse && lane < 16) p.lse[at] = log_sum(r.m[rt], r.l[rt]);
+        }
+    }
+}
+
+// Few rows: the waves of a workgroup have the same rows and every fourth tile
+// of its share of the tokens; their sums meet in LDS.  With one share the rows
+// are written, with more the sums go to the workspace.
+template <bool BF16, int D, int RT>
+__global__ __launch_bounds__(256, 2) void split_kernel(Kv4AttentionProblem p, Plan plan)
+{
+    constexpr int R = 16 * RT, PITCH = D + 4;
+    __shared__ __attribute__((aligned(16))) float lds[kWaves][192];
+    __shared__ __attribute__((aligned(16))) float sums[kWaves][R][PITCH];
+    __shared__ float2 tops[kWaves][R];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    int x = blockIdx.x;
+    const int g = x % p.cache.Hkv;
+    x /= p.cache.Hkv;
+    const int first = x % plan.tiles;
+    x /= plan.tiles;
+    const int part = x % plan.nsplit;
+    const Sequence s = sequence(p, x / plan.nsplit);
+    const int share = p.Hq / p.cache.Hkv, all = s.n * share, tiles = (all + R - 1) / R;
+    for (int k = first; k < tiles; k += plan.tiles) {
+        const int row0 = k * R;
+        const int i0 = row0 / share, i1 = min(row0 + R - 1, all - 1) / share;
+        const int begin = (seen_lo(p, s, i0) & ~63) + part * plan.chunk, end = seen_hi(p, s, i1);
+        const int to = part == plan.nsplit - 1 ? end : min(end, begin + plan.chunk);
+        Rows<D, RT> r;
+        load_rows<BF16, D, RT>(p, s, g, row0, r);
+        attend<D, RT>(p, s, g, begin + 64 * wave, to, 64 * kWaves, seen_lo(p, s, i1), seen_hi(p, s, i0), r, lds[wave]);
+        __syncthreads();                                   // (the rows before are out of LDS)
+        if (lane < 16) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) tops[wave][16 * rt + lane] = make_float2(r.m[rt], r.l[rt]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            const int row = 16 * rt + (lane & 15);
+            float m = tops[0][row].x;
+#pragma unroll
+            for (int v = 1; v < kWaves; ++v) m = fmaxf(m, tops[v][row].x);
+            const float by = r.m[rt] == m ? 1.0f : __builtin_amdgcn_exp2f(r.m[rt] - m);
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t)
+                *reinterpret_cast<float4v*>(&sums[wave][row][16 * t + 4 * (lane >> 4)]) = row_values(r, rt, t, by);
+        }
+        __syncthreads();
+        for (int e = threadIdx.x; e < R * (D / 4); e += 256) {
+            const int row = e / (D / 4), d = e % (D / 4) * 4;
+            if (row0 + row >= all) continue;
+            float m = tops[0][row].x, l = 0.0f;
+#pragma unroll
+            for (int v = 1; v < kWaves; ++v) m = fmaxf(m, tops[v][row].x);
+            float4v o = {};
+#pragma unroll
+            for (int v = 0; v < kWaves; ++v) {
+                const float2 ml = tops[v][row];
+                l += ml.y * (ml.x == m ? 1.0f : __builtin_amdgcn_exp2f(ml.x - m));
+                o += *reinterpret_cast<const float4v*>(&sums[v][row][d]);
+            }
+            const int i = (row0 + row) / share;
+            const int64_t at = (s.q0 + i) * p.Hq + g * share + (row0 + row - i * share);
+            if (plan.nsplit == 1) {
+                store4<BF16>(p.out, at * D + d, o * (l == 0.0f ? 0.0f : 1.0f / l));
+                if (p.lse && d == 0) p.lse[at] = log_sum(m, l);
+            } else {
+                const int64_t slot = (int64_t)part * (p.T * p.Hq) + at;
+                *reinterpret_cast<float4v*>(plan.part_o + slot * D + d) = o;
+                if (d == 0) plan.part_ml[slot] = make_float2(m, l);
+            }
+        }
+    }
+}
+
+// The shares of one row added in their order, WAVES waves a row.
+template <bool BF16, int D, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void join_kernel(Kv4AttentionProblem p, Plan plan)
+{
+    constexpr int EACH = D / 64;
+    __shared__ float sums[WAVES][D];
+    __shared__ float ls[WAVES];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t rows = p.T * p.Hq;
+    for (int64_t at = blockIdx.x; at < rows; at += gridDim.x) {
+        const int64_t t = at / p.Hq;
+        if (p.cu_q && (t < p.cu_q[0] || t >= p.cu_q[p.B])) continue;    // no sequence's
+        float m = -INFINITY;
+        for (int i = lane; i < plan.nsplit; i += 64) m = fmaxf(m, plan.part_ml[i * rows + at].x);
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
+        float o[EACH] = {}, l = 0.0f;
+#pragma unroll 4
+        for (int i = wave; i < plan.nsplit; i += WAVES) {
+            const float2 ml = plan.part_ml[i * rows + at];
+            const float by = ml.x == m ? 1.0f : __builtin_amdgcn_exp2f(ml.x - m);
+            const float* from = plan.part_o + (i * rows + at) * D + lane * EACH;
+            l = fmaf(ml.y, by, l);
+#pragma unroll
+            for (int e = 0; e < EACH; ++e) o[e] = fmaf(from[e], by, o[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) sums[wave][lane * EACH + e] = o[e];
+        if (lane == 0) ls[wave] = l;
+        __syncthreads();
+        l = 0.0f;
+#pragma unroll
+        for (int v = 0; v < WAVES; ++v) l += ls[v];
+        const float by = l == 0.0f ? 0.0f : 1.0f / l;
+        for (int d = threadIdx.x; d < D; d += 64 * WAVES) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int v = 0; v < WAVES; ++v) sum += sums[v][d];
+            static_cast<uint16_t*>(p.out)[at * D + d] = e4m3::to16<BF16>(sum * by);
+        }
+        if (p.lse && threadIdx.x == 0) p.lse[at] = log_sum(m, l);
+        __syncthreads();                                   // (the next row's sums)
+    }
+}
+
+// How a call of these sizes is cut: waves with rows of their own where their
+// workgroups fill the chip, else shares of the tokens.
+struct Cut {
+    bool rows;
+    int rt, tiles, nsplit, chunk;
+};
+
+Cut cut(const Kv4AttentionProblem& p, int64_t span)
+{
+    const int64_t share = p.Hq / p.cache.Hkv, all = (int64_t)p.max_q * share, pairs = (int64_t)p.B * p.cache.Hkv;
+    const int cus = compute_units() > 0 ? compute_units() : 256;
+    Cut c{};
+    c.rt = p.cache.D == 256 || all <= 16 ? 1 : 2;
+    c.nsplit = 1;
+    const int64_t wide = (all + 16 * c.rt * kWaves - 1) / (16 * c.rt * kWaves);
+    c.rows = all > 16 * c.rt && pairs * wide >= cus;
+    const int64_t narrow = (all + 16 * c.rt - 1) / (16 * c.rt);
+    // (workgroups stride over row tiles beyond the grid's limit of 2^32 threads)
+    c.tiles = (int)std::max<int64_t>(1, std::min<int64_t>(c.rows ? wide : narrow, kMaxBlocks / pairs));
+    if (!c.rows) {
+        const int64_t blocks = pairs * c.tiles, most = std::min<int64_t>((span + 511) / 512, 512);
+        c.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(most, (4 * cus + blocks - 1) / blocks));
+    }
+    const int64_t each = (span + c.nsplit - 1) / c.nsplit;
+    c.chunk = (int)((each + 255) / 256 * 256);
+    c.nsplit = (int)std::max<int64_t>(1, (span + c.chunk - 1) / c.chunk);
+    return c;
+}
+
+template <bool BF16, int D, int RT>
+hipError_t launch(const Kv4AttentionProblem& p, const Cut& c, const Plan& plan, hipStream_t stream)
+{
+    const unsigned blocks = (unsigned)((int64_t)p.B * p.cache.Hkv * c.tiles * c.nsplit);
+    if (c.rows) {
+        rows_kernel<BF16, D, RT><<<blocks, 256, 0, stream>>>(p, plan);
+        return hipGetLastError();
+    }
+    split_kernel<BF16, D, RT><<<blocks, 256, 0, stream>>>(p, plan);
+    if (c.nsplit > 1) {
+        const unsigned rows = (unsigned)std::min<int64_t>(p.T * p.Hq, 1 << 22);
+        if (c.nsplit <= 8) join_kernel<BF16, D, 1><<<rows, 64, 0, stream>>>(p, plan);
+        else join_kernel<BF16, D, 8><<<rows, 512, 0, stream>>>(p, plan);
     }
     return hipGetLastError();
 }
 
+template <bool BF16>
+hipError_t launch(const Kv4AttentionProblem& p, const Cut& c, const Plan& plan, hipStream_t stream)
+{
+    switch (p.cache.D) {
+    case 64: return c.rt == 1 ? launch<BF16, 64, 1>(p, c, plan, stream) : launch<BF16, 64, 2>(p, c, plan, stream);
+    case 128: return c.rt == 1 ? launch<BF16, 128, 1>(p, c, plan, stream) : launch<BF16, 128, 2>(p, c, plan, stream);
+    default: return launch<BF16, 256, 1>(p, c, plan, stream);
+    }
+}
+
 }  // namespace
 
-size_t kv4_attention_workspace_bytes(const Kv4AttentionProblem&) { return 0; }
+size_t kv4_attention_workspace_bytes(const Kv4AttentionProblem& p)
+{
+    const Cut c = cut(p, p.max_kv);
+    return c.nsplit == 1 ? 0 : (size_t)c.nsplit * p.T * p.Hq * (p.cache.D + 2) * 4;
+}
 
 hipError_t launch_kv4_attention(const Kv4AttentionProblem& p, hipStream_t stream)
 {
-    return p.bf16 ? rows<true>(p, stream) : rows<false>(p, stream);
+    // (a window bounds the tokens of a row tile; never more shares than the workspace is for)
+    Cut c = cut(p, p.max_kv);
+    if (p.window) {
+        const int most = c.nsplit;
+        c = cut(p, std::min<int64_t>(p.max_kv, (int64_t)p.window + p.max_q + 64));
+        c.nsplit = std::min(c.nsplit, most);
+    }
+    Plan plan{c.tiles, c.nsplit, c.chunk, static_cast<float*>(p.ws), nullptr};
+    if (c.nsplit > 1) plan.part_ml = reinterpret_cast<float2*>(plan.part_o + (int64_t)c.nsplit * p.T * p.Hq * p.cache.D);
+    return p.bf16 ? launch<true>(p, c, plan, stream) : launch<false>(p, c, plan, stream);
 }
 
 }  // namespace apex4
