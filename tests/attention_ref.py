@@ -126,16 +126,16 @@ def attention(q, name, cache, table, kv_lens, cu_q, scale=None, causal=True, win
 
     The bound counts, for a row that sees n tokens, every rounding that the
     header allows:
-      - a query is held in fp16 beside codes up to 15 (its 16th of it for odd
-        ones): 2^-21 of its row's scale a number at the least, where that scale is
-        1 for rows whose largest number is between 2^-6 and 2^14, and brings the
-        others there;
-      - D products and the offset of 8 in every code sum in fp32:
-        2 D 2^-24 of sum |q| 16 s_k;
+      - a query is held in fp16 beside codes up to 15: 2^-25 of its row's scale a
+        number at the least, where that scale is 1 for rows whose largest number is
+        between 2^-6 and 2^14, and brings the others there;
+      - D products, and the offset of 8 in every code, sum in fp32: 2 D 2^-24 of
+        sum |q| 16 s_k; and each is cut below 2^-18 of its eight's largest |q|;
       - an exponent of size e is off by 4 e 2^-24, exp2, log2 and reciprocal by
         4 units of fp32: together `wrong`, which moves every p_j by that much of
         itself, twice (numerator and sum);
-      - p_j s_j is rounded to fp16, relative to 2^-11, or 2^-25 of the largest;
+      - p_j s_j is rounded to fp16, relative to 2^-11, or 2^-25 of the largest, and
+        its product with a code, and with the offset, cut below 2^-18 of that;
       - n / 32 sums of products of weights and codes up to 15, in fp32.
     """
     q = np.asarray(q, np.float64)
@@ -184,13 +184,14 @@ def attention(q, name, cache, table, kv_lens, cu_q, scale=None, causal=True, win
                 lse[start:start + n, h] = np.where(some, top + np.log(np.where(some, total, 1.0)), -np.inf)
                 most = np.abs(x).max(-1)
                 level = np.where((most >= 2.0 ** -6) & (most < 2.0 ** 14), 1.0, most * 2.0 ** -4)
-                held = 16 * D * 2.0 ** -21 * level + 2 * D * 2.0 ** -24 * 16 * np.abs(x).sum(-1)
+                held = 16 * D * 2.0 ** -25 * level + 2 * D * 2.0 ** -18 * most \
+                    + 2 * D * 2.0 ** -24 * 16 * np.abs(x).sum(-1)
                 with np.errstate(divide="ignore"):
                     e = np.abs(np.where(seen, t, 0.0)) * 1.45 + np.abs(np.log2(np.maximum(vs, 2.0 ** -80)))
                 wrong = (scale * held[:, None] * np.where(seen, ks, 0.0) + (4 * e + 16) * 2.0 ** -24).max(-1)
                 ps = pr * np.where(seen, vs, 0.0)
                 count = seen.sum(-1)
-                each = 8 * ps.sum(-1) * (2 * wrong + 2.0 ** -11) + 8 * count * 2.0 ** -25 * ps.max(-1) \
+                each = 8 * ps.sum(-1) * (2 * wrong + 2.0 ** -11) + count * (8 * 2.0 ** -25 + 2 * 2.0 ** -18) * ps.max(-1) \
                     + 15 * ps.sum(-1) * (count / 16 + 64) * 2.0 ** -24 + 15 * 2.0 ** -60
                 bound[start:start + n, h] = each[:, None] + rounding(r, name)
                 lse_bound[start:start + n, h] = wrong + (count / 16 + 64) * 2.0 ** -24 \

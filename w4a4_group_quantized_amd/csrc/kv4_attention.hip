@@ -14,13 +14,16 @@
 // M moves only when a tile exceeds it by 2^8 (fp16 holds that), which keeps the
 // rescaling of O out of most tiles.  l and M are fp32.
 //
-// Codes go to the matrix unit as they lie: the nibble u = c + 8 in the lowest
-// bits of an fp16 is the subnormal number u 2^-24, in bits 4..7 u 2^-20 (the
-// instruction takes subnormal operands exactly), so eight codes cost five
-// instructions.  Where u is a key's, the query's number beside it holds the other
-// 2^-4 and the accumulators start at -8 sum(q); where it is a value's, the factor
-// goes into the end, and 8 sum(w) comes from one more matrix instruction whose
-// first operand is 8 everywhere.
+// Codes go to the matrix unit nearly as they lie: the nibble u = c + 8 in bits
+// 4..7 of an fp16 is the subnormal number u 2^-20, which the instruction takes
+// exactly, so eight codes cost seven instructions.  The accumulators of S start at
+// -8 sum(q), and 8 sum(w) comes from one more matrix instruction whose first
+// operand is 8 everywhere.  Nibbles in bits 0..3 (u 2^-24) would cost five, but
+// the instruction adds eight neighbouring products aligned to the largest
+// product of their exponent fields and drops what lies more than 24 bits below:
+// with u 2^-24 that is 2^-14 of the largest weight for every product, and
+// 131072 tokens with weights of all sizes came out 2.5 times further off than by
+// the rounding of w; with u 2^-20 it is 2^-18, and does not show.
 //
 // Operands come straight from memory in the order that the instruction wants:
 // a lane's 32 numbers of a key are D/8 neighbouring bytes, and the values' layout
@@ -106,11 +109,11 @@ __device__ inline int seen_lo(const Kv4AttentionProblem& p, const Sequence& s, i
 template <int D, int RT>
 struct Rows {
     half8 q[RT][D / 32];
-    float4v bias[RT];       // -8 sum(q) 2^-24
+    float4v bias[RT];       // -8 sum(q) 2^-20
     float unit[RT];         // the power of two that was taken out of the query
     int lo[RT], hi[RT];
-    float4v o[RT][D / 16];  // sums of w u, 2^-24 (even tiles of 16 numbers) and 2^-20
-    float4v w[RT];          // 8 sum(w) 2^-24
+    float4v o[RT][D / 16];  // sums of w u 2^-20
+    float4v w[RT];          // 8 sum(w) 2^-20
     float m[RT], l[RT];
 };
 
@@ -157,9 +160,9 @@ __device__ inline void load_rows(const Kv4AttentionProblem& p, const Sequence& s
             constexpr int order[8] = {0, 4, 1, 5, 2, 6, 3, 7};
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                v[k] = (_Float16)__builtin_amdgcn_ldexpf(x[8 * f + order[k]], k & 2 ? e - 4 : e);
+                v[k] = (_Float16)__builtin_amdgcn_ldexpf(x[8 * f + order[k]], e);
             r.q[rt][f] = v;
-            r.bias[rt] = mfma(mfma_operand(0x80088008, 0x80808080, 0x80088008, 0x80808080), v, r.bias[rt]);
+            r.bias[rt] = mfma(mfma_operand(0x80808080, 0x80808080, 0x80808080, 0x80808080), v, r.bias[rt]);
         }
         r.lo[rt] = live ? seen_lo(p, s, i) : 0;
         r.hi[rt] = live ? seen_hi(p, s, i) : 0;
@@ -207,7 +210,7 @@ __device__ inline void load_values(Codes<D>& c, int s, const uint8_t* p)
     }
 }
 
-constexpr uint32_t kLow = 0x000F000F, kHigh = 0x00F000F0;
+constexpr uint32_t kNibble = 0x00F000F0;
 
 // The tokens [from, to) in tiles of 64, `step` apart; `lds`: 192 floats of the wave.
 template <int D, int RT>
@@ -218,7 +221,7 @@ __device__ inline void attend(const Kv4AttentionProblem& p, const Sequence& s, i
     const int lane = threadIdx.x & 63, quad = lane >> 4;
     const int32_t* table = p.table + s.b * p.cols;
     const int last = (int)p.cols - 1;
-    const float factor = p.scale * 1.44269504f * 0x1p24f;
+    const float factor = p.scale * 1.44269504f * 0x1p20f;
     const int key_at = (lane & 15) * (D / 2) + quad * (D == 64 ? 8 : 16), value_at = lane * (D / 8);
     bool scaled = false;
 #pragma unroll
@@ -274,8 +277,8 @@ __device__ inline void attend(const Kv4AttentionProblem& p, const Sequence& s, i
         for (int sub = 0; sub < 4; ++sub) {
 #pragma unroll
             for (int f = 0; f < D / 32; ++f) {
-                const uint32_t u = k.w[sub][f], u8 = u >> 8;
-                const half8 a = mfma_operand(u & kLow, u & kHigh, u8 & kLow, u8 & kHigh);
+                const uint32_t u = k.w[sub][f];
+                const half8 a = mfma_operand(u << 4 & kNibble, u & kNibble, u >> 4 & kNibble, u >> 8 & kNibble);
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) x[rt][sub] = mfma(a, r.q[rt][f], f == 0 ? r.bias[rt] : x[rt][sub]);
             }
@@ -342,12 +345,12 @@ __device__ inline void attend(const Kv4AttentionProblem& p, const Sequence& s, i
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
-                r.w[rt] = mfma(mfma_operand(0x00080008, 0x00080008, 0x00080008, 0x00080008), w[rt][i], r.w[rt]);
+                r.w[rt] = mfma(mfma_operand(0x00800080, 0x00800080, 0x00800080, 0x00800080), w[rt][i], r.w[rt]);
 #pragma unroll
             for (int n = 0; n < D / 32; ++n) {
-                const uint32_t a = v.w[2 * i][n], a8 = a >> 8, b = v.w[2 * i + 1][n], b8 = b >> 8;
-                const half8 even = mfma_operand(a & kLow, a8 & kLow, b & kLow, b8 & kLow);
-                const half8 odd = mfma_operand(a & kHigh, a8 & kHigh, b & kHigh, b8 & kHigh);
+                const uint32_t a = v.w[2 * i][n], b = v.w[2 * i + 1][n];
+                const half8 even = mfma_operand(a << 4 & kNibble, a >> 4 & kNibble, b << 4 & kNibble, b >> 4 & kNibble);
+                const half8 odd = mfma_operand(a & kNibble, a >> 8 & kNibble, b & kNibble, b >> 8 & kNibble);
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
                     r.o[rt][2 * n] = mfma(even, w[rt][i], r.o[rt][2 * n]);
@@ -366,8 +369,7 @@ __device__ inline void attend(const Kv4AttentionProblem& p, const Sequence& s, i
 template <int D, int RT>
 __device__ inline float4v row_values(const Rows<D, RT>& r, int rt, int t, float by)
 {
-    const float back = (t & 1 ? 16.0f : 1.0f) * r.w[rt][0], unit = by * (t & 1 ? 0x1p20f : 0x1p24f);
-    return (r.o[rt][t] - back) * unit;
+    return (r.o[rt][t] - r.w[rt][0]) * (by * 0x1p20f);
 }
 
 template <bool BF16>
