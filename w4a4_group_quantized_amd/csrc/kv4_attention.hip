@@ -64,6 +64,9 @@ __device__ inline half8 mfma_operand(uint32_t a, uint32_t b, uint32_t c, uint32_
 
 __device__ inline float4v mfma(half8 a, half8 b, float4v c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 
+// the operand that is 8 everywhere
+__device__ inline half8 eights() { return mfma_operand(0x00800080, 0x00800080, 0x00800080, 0x00800080); }
+
 // over the four lanes that hold a row
 __device__ inline float row_max(float x)
 {
@@ -212,21 +215,152 @@ __device__ inline void load_values(Codes<D>& c, int s, const uint8_t* p)
 
 constexpr uint32_t kNibble = 0x00F000F0;
 
-// The tokens [from, to) in tiles of 64, `step` apart; `lds`: 192 floats of the wave.
+// a word of eight codes as a key's operand, and two of values as the operands of
+// their low and high numbers
+__device__ inline half8 key_operand(uint32_t u)
+{
+    return mfma_operand(u << 4 & kNibble, u & kNibble, u >> 4 & kNibble, u >> 8 & kNibble);
+}
+__device__ inline uint2 value_low(uint32_t u) { return make_uint2(u << 4 & kNibble, u >> 4 & kNibble); }
+__device__ inline uint2 value_high(uint32_t u) { return make_uint2(u & kNibble, u >> 8 & kNibble); }
+
+// A token's three factors, in arrays of 64: of its scores, log2 of its values'
+// scale, and that scale's reciprocal; for a place that holds none, what makes its
+// weight zero.  A scale that is not finite shows through the second: a row that
+// does not see the token multiplies the third by zero.
+__device__ inline void put_factors(float* factors, int at, bool valid, float ks, float vs, float factor)
+{
+    const float v = vs < kTiny ? kTiny : vs;               // (a NaN stays)
+    factors[at] = valid ? ks * factor : 0.0f;
+    factors[64 + at] = valid ? __builtin_amdgcn_logf(v) : -INFINITY;
+    factors[128 + at] = valid && v < INFINITY ? __builtin_amdgcn_rcpf(v) : 0.0f;
+}
+
+// Scores of 64 tokens from t0 on times their factors; top: the largest that a
+// lane has of its rows.  EDGE: some row does not see all of them.
+template <int D, int RT, bool EDGE>
+__device__ inline void exponents(const Rows<D, RT>& r, float4v (&x)[RT][4], const float* factors, int t0,
+                                 float (&top)[RT])
+{
+    const int quad = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) top[rt] = -INFINITY;
+#pragma unroll
+    for (int sub = 0; sub < 4; ++sub) {
+        const float4v kf = *reinterpret_cast<const float4v*>(factors + 16 * sub + 4 * quad);
+        const float4v ls = *reinterpret_cast<const float4v*>(factors + 64 + 16 * sub + 4 * quad);
+        const int t = t0 + 16 * sub + 4 * quad;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[rt][sub][i] = fmaf(x[rt][sub][i], kf[i], ls[i]);
+                if (EDGE) {
+                    const bool seen = (t + i < r.hi[rt]) & (t + i >= r.lo[rt]) & (ls[i] != -INFINITY);
+                    x[rt][sub][i] = seen ? x[rt][sub][i] : -INFINITY;
+                }
+                top[rt] = fmaxf(top[rt], x[rt][sub][i]);
+            }
+        }
+    }
+}
+
+// Scores of 64 tokens to weights, the operands of the second product.
+template <int D, int RT>
+__device__ inline void weights(Rows<D, RT>& r, float4v (&x)[RT][4], const float* factors, int t0, bool scaled, bool edge,
+                               half8 (&w)[RT][2])
+{
+    const int quad = (threadIdx.x & 63) >> 4;
+    if (scaled) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int sub = 0; sub < 4; ++sub) x[rt][sub] *= r.unit[rt];
+    }
+    float top[RT];
+    if (edge) exponents<D, RT, true>(r, x, factors, t0, top);
+    else exponents<D, RT, false>(r, x, factors, t0, top);
+    bool above = false;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        top[rt] = row_max(top[rt]);
+        above |= top[rt] > r.m[rt] + kLazy;
+    }
+    if (__any(above)) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            const float m = top[rt] > r.m[rt] + kLazy ? top[rt] : r.m[rt];
+            float old = m == r.m[rt] ? 1.0f : __builtin_amdgcn_exp2f(r.m[rt] - m);
+            // (keeps the compiler from scaling every tile's sums into second registers and choosing)
+            asm volatile("" : "+v"(old));
+            r.m[rt] = m;
+            r.l[rt] *= old;
+            r.w[rt] *= old;
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t) r.o[rt][t] *= old;
+        }
+    }
+    float m[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) m[rt] = r.m[rt] == -INFINITY ? 0.0f : r.m[rt];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t packed[RT][4];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int sub = 2 * i + half;
+            const float4v iv = *reinterpret_cast<const float4v*>(factors + 128 + 16 * sub + 4 * quad);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                float e[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    e[k] = __builtin_amdgcn_exp2f(x[rt][sub][k] - m[rt]);
+                    r.l[rt] = fmaf(e[k], iv[k], r.l[rt]);
+                }
+                // (codes of tokens 0 and 2, and 1 and 3, share a register)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    packed[rt][2 * half + k] = __builtin_bit_cast(uint32_t, __builtin_convertvector((float2v{e[k], e[k + 2]}), half2v));
+            }
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+            w[rt][i] = mfma_operand(packed[rt][0], packed[rt][1], packed[rt][2], packed[rt][3]);
+    }
+}
+
+template <int RT>
+__device__ inline bool any_scaled(const float (&unit)[RT])
+{
+    bool scaled = false;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) scaled |= unit[rt] != 1.0f;
+    return __any(scaled);
+}
+
+__device__ inline void wave_sync()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+constexpr float kLog2e = 1.44269504f;
+
+// The tokens [from, to) in tiles of 64, `step` apart, each unpacked by the wave
+// for itself; `factors`: 192 floats of the wave.
 template <int D, int RT>
 __device__ inline void attend(const Kv4AttentionProblem& p, const Sequence& s, int g, int from, int to, int step,
-                              int lo_max, int hi_min, Rows<D, RT>& r, float* lds)
+                              int lo_max, int hi_min, Rows<D, RT>& r, float* factors)
 {
     const Kv4Cache& c = p.cache;
     const int lane = threadIdx.x & 63, quad = lane >> 4;
     const int32_t* table = p.table + s.b * p.cols;
     const int last = (int)p.cols - 1;
-    const float factor = p.scale * 1.44269504f * 0x1p20f;
+    const float factor = p.scale * kLog2e * 0x1p20f;
     const int key_at = (lane & 15) * (D / 2) + quad * (D == 64 ? 8 : 16), value_at = lane * (D / 8);
-    bool scaled = false;
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) scaled |= r.unit[rt] != 1.0f;
-    scaled = __any(scaled);
+    const bool scaled = any_scaled(r.unit);
     if (from >= to) return;
 
     // lane's token of the tile at t: its row in the cache (row 0 where there is none)
@@ -262,95 +396,32 @@ __device__ inline void attend(const Kv4AttentionProblem& p, const Sequence& s, i
     look(from + step);
 
     for (int t0 = from; t0 < to; t0 += step) {
-        // the tile's factors of the tokens, one token a lane, to all lanes
-        const float vsc = vs < kTiny ? kTiny : vs;
-        lds[lane] = valid ? ks * factor : 0.0f;
-        lds[64 + lane] = valid ? __builtin_amdgcn_logf(vsc) : -INFINITY;
-        lds[128 + lane] = valid ? __builtin_amdgcn_rcpf(vsc) : 0.0f;
+        put_factors(factors, lane, valid, ks, vs, factor);
         const bool edge = t0 + 64 > hi_min || t0 < lo_max || !__all(valid);
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-
+        wave_sync();
         float4v x[RT][4];
 #pragma unroll
         for (int sub = 0; sub < 4; ++sub) {
 #pragma unroll
             for (int f = 0; f < D / 32; ++f) {
-                const uint32_t u = k.w[sub][f];
-                const half8 a = mfma_operand(u << 4 & kNibble, u & kNibble, u >> 4 & kNibble, u >> 8 & kNibble);
+                const half8 a = key_operand(k.w[sub][f]);
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) x[rt][sub] = mfma(a, r.q[rt][f], f == 0 ? r.bias[rt] : x[rt][sub]);
             }
         }
         locate(t0 + step);
         load_k();
-
         half8 w[RT][2];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            if (scaled) {
-#pragma unroll
-                for (int sub = 0; sub < 4; ++sub) x[rt][sub] *= r.unit[rt];
-            }
-            float top = -INFINITY;
-#pragma unroll
-            for (int sub = 0; sub < 4; ++sub) {
-                const float4v kf = *reinterpret_cast<const float4v*>(lds + 16 * sub + 4 * quad);
-                const float4v ls = *reinterpret_cast<const float4v*>(lds + 64 + 16 * sub + 4 * quad);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[rt][sub][i] = fmaf(x[rt][sub][i], kf[i], ls[i]);
-                if (edge) {
-                    const int t = t0 + 16 * sub + 4 * quad;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (t + i >= r.hi[rt] || t + i < r.lo[rt] || ls[i] == -INFINITY) x[rt][sub][i] = -INFINITY;
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) top = fmaxf(top, x[rt][sub][i]);
-            }
-            top = row_max(top);
-            if (__any(top > r.m[rt] + kLazy)) {
-                const float m = top > r.m[rt] + kLazy ? top : r.m[rt];
-                const float old = m == r.m[rt] ? 1.0f : __builtin_amdgcn_exp2f(r.m[rt] - m);
-                r.m[rt] = m;
-                r.l[rt] *= old;
-                r.w[rt] *= old;
-#pragma unroll
-                for (int t = 0; t < D / 16; ++t) r.o[rt][t] *= old;
-            }
-            const float m = r.m[rt] == -INFINITY ? 0.0f : r.m[rt];
-            uint32_t packed[8];
-#pragma unroll
-            for (int sub = 0; sub < 4; ++sub) {
-                const float4v iv = *reinterpret_cast<const float4v*>(lds + 128 + 16 * sub + 4 * quad);
-                float e[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    e[i] = __builtin_amdgcn_exp2f(x[rt][sub][i] - m);
-                    // (what a row does not see may have a NaN for its scale)
-                    const float back = edge && x[rt][sub][i] == -INFINITY ? 0.0f : iv[i];
-                    r.l[rt] = fmaf(e[i], back, r.l[rt]);
-                }
-                // (codes of tokens 0 and 2, and 1 and 3, share a register)
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    packed[2 * sub + i] = __builtin_bit_cast(uint32_t, __builtin_convertvector((float2v{e[i], e[i + 2]}), half2v));
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                w[rt][i] = mfma_operand(packed[4 * i], packed[4 * i + 1], packed[4 * i + 2], packed[4 * i + 3]);
-        }
+        weights<D, RT>(r, x, factors, t0, scaled, edge, w);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-                r.w[rt] = mfma(mfma_operand(0x00800080, 0x00800080, 0x00800080, 0x00800080), w[rt][i], r.w[rt]);
+            for (int rt = 0; rt < RT; ++rt) r.w[rt] = mfma(eights(), w[rt][i], r.w[rt]);
 #pragma unroll
             for (int n = 0; n < D / 32; ++n) {
-                const uint32_t a = v.w[2 * i][n], b = v.w[2 * i + 1][n];
-                const half8 even = mfma_operand(a << 4 & kNibble, a >> 4 & kNibble, b << 4 & kNibble, b >> 4 & kNibble);
-                const half8 odd = mfma_operand(a & kNibble, a >> 8 & kNibble, b & kNibble, b >> 8 & kNibble);
+                const uint2 a = value_low(v.w[2 * i][n]), b = value_low(v.w[2 * i + 1][n]);
+                const uint2 c = value_high(v.w[2 * i][n]), d = value_high(v.w[2 * i + 1][n]);
+                const half8 even = mfma_operand(a.x, a.y, b.x, b.y), odd = mfma_operand(c.x, c.y, d.x, d.y);
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
                     r.o[rt][2 * n] = mfma(even, w[rt][i], r.o[rt][2 * n]);
@@ -360,6 +431,102 @@ __device__ inline void attend(const Kv4AttentionProblem& p, const Sequence& s, i
         }
         load_v();
         look(t0 + 2 * step);
+    }
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) r.l[rt] = row_sum(r.l[rt]);
+}
+
+// A tile of 64 tokens as operands, in the order in which the lanes take them.
+template <int D>
+struct Tile {
+    uint4 k[4][D / 32][64];         // [16 tokens][32 numbers][lane]
+    uint2 v[2][D / 16][64][2];      // [32 tokens][16 numbers][lane][16 tokens]
+    float factors[192];
+};
+
+// The same for a workgroup whose waves have rows of their own: wave i unpacks
+// tokens 16 i .. of each tile into LDS for all of them, a tile ahead.  from, to:
+// what some row of the workgroup sees.
+template <int D, int RT>
+__device__ inline void attend_shared(const Kv4AttentionProblem& p, const Sequence& s, int g, int from, int to, int lo_max,
+                                     int hi_min, Rows<D, RT>& r, Tile<D>* tiles)
+{
+    const Kv4Cache& c = p.cache;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, quad = lane >> 4;
+    const int32_t* table = p.table + s.b * p.cols;
+    const int last = (int)p.cols - 1;
+    const float factor = p.scale * kLog2e * 0x1p20f;
+    const int key_at = (lane & 15) * (D / 2) + quad * (D == 64 ? 8 : 16), value_at = lane * (D / 8);
+    const bool scaled = any_scaled(r.unit);
+
+    int page = 0;
+    bool valid = false;
+    Codes<D> k, v;                  // (the first row only)
+    float ks = 0.0f, vs = 0.0f;
+    // the wave's 16 tokens of the tile at t are of one page
+    const auto look = [&](int t) { page = table[min((t + 16 * wave) >> c.shift, last)]; };
+    const auto load = [&](int t) {
+        const int first = t + 16 * wave;
+        const bool some = first < to && page >= 0 && page < c.pages;
+        const int64_t row = some ? (((int64_t)page * c.Hkv + g) << c.shift) + (first & (c.page - 1)) : 0;
+        valid = some && first + (lane & 15) < to;
+        load_codes<D>(k, 0, c.k_codes + row * (D / 2) + key_at);
+        load_values<D>(v, 0, c.v_codes + row * (D / 2) + value_at);
+        ks = c.k_scales[row + (lane & 15)];
+        vs = c.v_scales[row + (lane & 15)];
+    };
+    const auto unpack = [&](Tile<D>& tile) {
+#pragma unroll
+        for (int f = 0; f < D / 32; ++f) {
+            tile.k[wave][f][lane] = __builtin_bit_cast(uint4, key_operand(k.w[0][f]));
+            tile.v[wave >> 1][2 * f][lane][wave & 1] = value_low(v.w[0][f]);
+            tile.v[wave >> 1][2 * f + 1][lane][wave & 1] = value_high(v.w[0][f]);
+        }
+        if (lane < 16) put_factors(tile.factors, 16 * wave + lane, valid, ks, vs, factor);
+    };
+    __syncthreads();                // (the rows before are done with the tiles)
+    if (from < to) {
+        look(from);
+        load(from);
+        look(from + 64);
+        unpack(tiles[0]);
+        load(from + 64);
+        look(from + 128);
+    }
+    int at = 0;
+    for (int t0 = from; t0 < to; t0 += 64, at ^= 1) {
+        __syncthreads();
+        // (what the load before this one brought; the tile that it replaces was read before the barrier)
+        unpack(tiles[at ^ 1]);
+        load(t0 + 128);
+        look(t0 + 192);
+        const Tile<D>& tile = tiles[at];
+        float4v x[RT][4];
+#pragma unroll
+        for (int sub = 0; sub < 4; ++sub) {
+#pragma unroll
+            for (int f = 0; f < D / 32; ++f) {
+                const half8 a = __builtin_bit_cast(half8, tile.k[sub][f][lane]);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) x[rt][sub] = mfma(a, r.q[rt][f], f == 0 ? r.bias[rt] : x[rt][sub]);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        half8 w[RT][2];
+        const bool edge = t0 + 64 > hi_min || t0 < lo_max || __any(tile.factors[64 + lane] == -INFINITY);
+        weights<D, RT>(r, x, tile.factors, t0, scaled, edge, w);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) r.w[rt] = mfma(eights(), w[rt][i], r.w[rt]);
+#pragma unroll
+            for (int n = 0; n < D / 16; ++n) {
+                const half8 a = __builtin_bit_cast(half8, *reinterpret_cast<const uint4*>(&tile.v[i][n][lane][0]));
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) r.o[rt][n] = mfma(a, w[rt][i], r.o[rt][n]);
+            }
+        }
     }
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) r.l[rt] = row_sum(r.l[rt]);
@@ -387,7 +554,7 @@ __device__ inline float log_sum(float m, float l) { return l == 0.0f ? -INFINITY
 template <bool BF16, int D, int RT>
 __global__ __launch_bounds__(256, 2) void rows_kernel(Kv4AttentionProblem p, Plan plan)
 {
-    __shared__ __attribute__((aligned(16))) float lds[kWaves][192];
+    __shared__ __attribute__((aligned(16))) Tile<D> buffers[2];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     int x = blockIdx.x;
     const int g = x % p.cache.Hkv;
@@ -397,13 +564,13 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(Kv4AttentionProblem p, Pla
     const int share = p.Hq / p.cache.Hkv, all = s.n * share, tiles = (all + 16 * RT * kWaves - 1) / (16 * RT * kWaves);
     for (int k = first; k < tiles; k += plan.tiles) {
         // (the last rows see the most tokens: first)
-        const int row0 = ((tiles - 1 - k) * kWaves + wave) * 16 * RT;
-        if (row0 >= all) continue;
+        const int top = (tiles - 1 - k) * kWaves * 16 * RT, row0 = top + wave * 16 * RT;
         Rows<D, RT> r;
         load_rows<BF16, D, RT>(p, s, g, row0, r);
         const int i0 = row0 / share, i1 = min(row0 + 16 * RT - 1, all - 1) / share;
-        attend<D, RT>(p, s, g, seen_lo(p, s, i0) & ~63, seen_hi(p, s, i1), 64, seen_lo(p, s, i1), seen_hi(p, s, i0), r,
-                      lds[wave]);
+        const int end = min(top + kWaves * 16 * RT, all) - 1;
+        attend_shared<D, RT>(p, s, g, seen_lo(p, s, top / share) & ~63, seen_hi(p, s, end / share), seen_lo(p, s, i1),
+                             seen_hi(p, s, i0), r, buffers);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
             const int row = row0 + 16 * rt + (lane & 15);
