@@ -67,11 +67,17 @@ __device__ inline float4v mfma(half8 a, half8 b, float4v c) { return __builtin_a
 // the operand that is 8 everywhere
 __device__ inline half8 eights() { return mfma_operand(0x00800080, 0x00800080, 0x00800080, 0x00800080); }
 
-// over the four lanes that hold a row
+// over the four lanes that hold a row (16 lanes apart).  The swaps exchange halves
+// and rows of two registers, here of one value's copies: then each lane has its
+// own and the other's.  (Written out: of the builtins' results the compiler kept
+// only the first.)
 __device__ inline float row_max(float x)
 {
-    x = fmaxf(x, __shfl_xor(x, 16));
-    return fmaxf(x, __shfl_xor(x, 32));
+    float y = x;
+    asm("s_nop 1\n\tv_permlane32_swap_b32 %0, %1" : "+v"(x), "+v"(y));
+    x = y = fmaxf(x, y);
+    asm("s_nop 1\n\tv_permlane16_swap_b32 %0, %1" : "+v"(x), "+v"(y));
+    return fmaxf(x, y);
 }
 __device__ inline float row_sum(float x)
 {
@@ -224,92 +230,103 @@ __device__ inline half8 key_operand(uint32_t u)
 __device__ inline uint2 value_low(uint32_t u) { return make_uint2(u << 4 & kNibble, u >> 4 & kNibble); }
 __device__ inline uint2 value_high(uint32_t u) { return make_uint2(u & kNibble, u >> 8 & kNibble); }
 
-// A token's three factors, in arrays of 64: of its scores, log2 of its values'
+// A token's three factors, in arrays of N: of its scores, log2 of its values'
 // scale, and that scale's reciprocal; for a place that holds none, what makes its
 // weight zero.  A scale that is not finite shows through the second: a row that
 // does not see the token multiplies the third by zero.
-__device__ inline void put_factors(float* factors, int at, bool valid, float ks, float vs, float factor)
+__device__ inline float key_factor(bool valid, float ks, float factor) { return valid ? ks * factor : 0.0f; }
+template <int N>
+__device__ inline void put_value_factors(float* factors, int at, bool valid, float vs)
 {
     const float v = vs < kTiny ? kTiny : vs;               // (a NaN stays)
-    factors[at] = valid ? ks * factor : 0.0f;
-    factors[64 + at] = valid ? __builtin_amdgcn_logf(v) : -INFINITY;
-    factors[128 + at] = valid && v < INFINITY ? __builtin_amdgcn_rcpf(v) : 0.0f;
+    factors[N + at] = valid ? __builtin_amdgcn_logf(v) : -INFINITY;
+    factors[2 * N + at] = valid && v < INFINITY ? __builtin_amdgcn_rcpf(v) : 0.0f;
 }
 
-// Scores of 64 tokens from t0 on times their factors; top: the largest that a
-// lane has of its rows.  EDGE: some row does not see all of them.
-template <int D, int RT, bool EDGE>
-__device__ inline void exponents(const Rows<D, RT>& r, float4v (&x)[RT][4], const float* factors, int t0,
-                                 float (&top)[RT])
+// Scores of 16 NS tokens times their factors; top: the largest that a lane has
+// of its rows.
+template <int D, int RT, int NS>
+__device__ inline void exponents(float4v (&x)[RT][NS], const float* factors, float (&top)[RT])
 {
     const int quad = (threadIdx.x & 63) >> 4;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) top[rt] = -INFINITY;
 #pragma unroll
-    for (int sub = 0; sub < 4; ++sub) {
+    for (int sub = 0; sub < NS; ++sub) {
         const float4v kf = *reinterpret_cast<const float4v*>(factors + 16 * sub + 4 * quad);
-        const float4v ls = *reinterpret_cast<const float4v*>(factors + 64 + 16 * sub + 4 * quad);
-        const int t = t0 + 16 * sub + 4 * quad;
+        const float4v ls = *reinterpret_cast<const float4v*>(factors + 16 * NS + 16 * sub + 4 * quad);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 x[rt][sub][i] = fmaf(x[rt][sub][i], kf[i], ls[i]);
-                if (EDGE) {
-                    const bool seen = (t + i < r.hi[rt]) & (t + i >= r.lo[rt]) & (ls[i] != -INFINITY);
-                    x[rt][sub][i] = seen ? x[rt][sub][i] : -INFINITY;
-                }
                 top[rt] = fmaxf(top[rt], x[rt][sub][i]);
             }
         }
     }
 }
 
-// Scores of 64 tokens to weights, the operands of the second product.
-template <int D, int RT>
-__device__ inline void weights(Rows<D, RT>& r, float4v (&x)[RT][4], const float* factors, int t0, bool scaled, bool edge,
-                               half8 (&w)[RT][2])
+// The same where some row does not see all the tokens from t0 on.
+template <int D, int RT, int NS>
+__device__ inline void mask(const Rows<D, RT>& r, float4v (&x)[RT][NS], const float* factors, int t0, float (&top)[RT])
 {
     const int quad = (threadIdx.x & 63) >> 4;
-    if (scaled) {
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
+    for (int rt = 0; rt < RT; ++rt) top[rt] = -INFINITY;
 #pragma unroll
-            for (int sub = 0; sub < 4; ++sub) x[rt][sub] *= r.unit[rt];
+    for (int sub = 0; sub < NS; ++sub) {
+        const float4v ls = *reinterpret_cast<const float4v*>(factors + 16 * NS + 16 * sub + 4 * quad);
+        const int t = t0 + 16 * sub + 4 * quad;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool seen = (t + i < r.hi[rt]) & (t + i >= r.lo[rt]) & (ls[i] != -INFINITY);
+                x[rt][sub][i] = seen ? x[rt][sub][i] : -INFINITY;
+                top[rt] = fmaxf(top[rt], x[rt][sub][i]);
+            }
+        }
     }
-    float top[RT];
-    if (edge) exponents<D, RT, true>(r, x, factors, t0, top);
-    else exponents<D, RT, false>(r, x, factors, t0, top);
+}
+
+// Moves the rows' maxima where a tile is above them, with what is relative to them.
+template <int D, int RT>
+__device__ inline void raise(Rows<D, RT>& r, float (&top)[RT])
+{
     bool above = false;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         top[rt] = row_max(top[rt]);
         above |= top[rt] > r.m[rt] + kLazy;
     }
-    if (__any(above)) {
+    if (!__any(above)) return;
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            const float m = top[rt] > r.m[rt] + kLazy ? top[rt] : r.m[rt];
-            float old = m == r.m[rt] ? 1.0f : __builtin_amdgcn_exp2f(r.m[rt] - m);
-            // (keeps the compiler from scaling every tile's sums into second registers and choosing)
-            asm volatile("" : "+v"(old));
-            r.m[rt] = m;
-            r.l[rt] *= old;
-            r.w[rt] *= old;
+    for (int rt = 0; rt < RT; ++rt) {
+        const float m = top[rt] > r.m[rt] + kLazy ? top[rt] : r.m[rt];
+        const float old = m == r.m[rt] ? 1.0f : __builtin_amdgcn_exp2f(r.m[rt] - m);
+        r.m[rt] = m;
+        r.l[rt] *= old;
+        r.w[rt] *= old;
 #pragma unroll
-            for (int t = 0; t < D / 16; ++t) r.o[rt][t] *= old;
-        }
+        for (int t = 0; t < D / 16; ++t) r.o[rt][t] *= old;
     }
+}
+
+// Exponents to weights, the operands of the second product.
+template <int D, int RT, int NS>
+__device__ inline void weights(Rows<D, RT>& r, const float4v (&x)[RT][NS], const float* factors, half8 (&w)[RT][NS / 2])
+{
+    const int quad = (threadIdx.x & 63) >> 4;
     float m[RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) m[rt] = r.m[rt] == -INFINITY ? 0.0f : r.m[rt];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NS / 2; ++i) {
         uint32_t packed[RT][4];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int sub = 2 * i + half;
-            const float4v iv = *reinterpret_cast<const float4v*>(factors + 128 + 16 * sub + 4 * quad);
+            const float4v iv = *reinterpret_cast<const float4v*>(factors + 32 * NS + 16 * sub + 4 * quad);
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
                 float e[4];
@@ -328,6 +345,15 @@ __device__ inline void weights(Rows<D, RT>& r, float4v (&x)[RT][4], const float*
         for (int rt = 0; rt < RT; ++rt)
             w[rt][i] = mfma_operand(packed[rt][0], packed[rt][1], packed[rt][2], packed[rt][3]);
     }
+}
+
+template <int D, int RT, int NS>
+__device__ inline void unscale(const Rows<D, RT>& r, float4v (&x)[RT][NS])
+{
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int sub = 0; sub < NS; ++sub) x[rt][sub] *= r.unit[rt];
 }
 
 template <int RT>
@@ -396,7 +422,8 @@ __device__ inline void attend(const Kv4AttentionProblem& p, const Sequence& s, i
     look(from + step);
 
     for (int t0 = from; t0 < to; t0 += step) {
-        put_factors(factors, lane, valid, ks, vs, factor);
+        factors[lane] = key_factor(valid, ks, factor);
+        put_value_factors<64>(factors, lane, valid, vs);
         const bool edge = t0 + 64 > hi_min || t0 < lo_max || !__all(valid);
         wave_sync();
         float4v x[RT][4];
@@ -411,8 +438,13 @@ __device__ inline void attend(const Kv4AttentionProblem& p, const Sequence& s, i
         }
         locate(t0 + step);
         load_k();
+        if (scaled) unscale<D, RT>(r, x);
+        float top[RT];
+        exponents<D, RT>(x, factors, top);
+        if (edge) mask<D, RT>(r, x, factors, t0, top);
+        raise<D, RT>(r, top);
         half8 w[RT][2];
-        weights<D, RT>(r, x, factors, t0, scaled, edge, w);
+        weights<D, RT>(r, x, factors, w);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
 #pragma unroll
@@ -452,7 +484,7 @@ __device__ inline void attend_shared(const Kv4AttentionProblem& p, const Sequenc
                                      int hi_min, Rows<D, RT>& r, Tile<D>* tiles)
 {
     const Kv4Cache& c = p.cache;
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, quad = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, quad = lane >> 4;
     const int32_t* table = p.table + s.b * p.cols;
     const int last = (int)p.cols - 1;
     const float factor = p.scale * kLog2e * 0x1p20f;
@@ -466,9 +498,9 @@ __device__ inline void attend_shared(const Kv4AttentionProblem& p, const Sequenc
     // the wave's 16 tokens of the tile at t are of one page
     const auto look = [&](int t) { page = table[min((t + 16 * wave) >> c.shift, last)]; };
     const auto load = [&](int t) {
-        const int first = t + 16 * wave;
-        const bool some = first < to && page >= 0 && page < c.pages;
-        const int64_t row = some ? (((int64_t)page * c.Hkv + g) << c.shift) + (first & (c.page - 1)) : 0;
+        const int first = t + 16 * wave, at = __builtin_amdgcn_readfirstlane(page);
+        const bool some = first < to && at >= 0 && at < c.pages;
+        const int64_t row = some ? (((int64_t)at * c.Hkv + g) << c.shift) + (first & (c.page - 1)) : 0;
         valid = some && first + (lane & 15) < to;
         load_codes<D>(k, 0, c.k_codes + row * (D / 2) + key_at);
         load_values<D>(v, 0, c.v_codes + row * (D / 2) + value_at);
@@ -482,7 +514,10 @@ __device__ inline void attend_shared(const Kv4AttentionProblem& p, const Sequenc
             tile.v[wave >> 1][2 * f][lane][wave & 1] = value_low(v.w[0][f]);
             tile.v[wave >> 1][2 * f + 1][lane][wave & 1] = value_high(v.w[0][f]);
         }
-        if (lane < 16) put_factors(tile.factors, 16 * wave + lane, valid, ks, vs, factor);
+        if (lane < 16) {
+            tile.factors[16 * wave + lane] = key_factor(valid, ks, factor);
+            put_value_factors<64>(tile.factors, 16 * wave + lane, valid, vs);
+        }
     };
     __syncthreads();                // (the rows before are done with the tiles)
     if (from < to) {
@@ -511,10 +546,15 @@ __device__ inline void attend_shared(const Kv4AttentionProblem& p, const Sequenc
                 for (int rt = 0; rt < RT; ++rt) x[rt][sub] = mfma(a, r.q[rt][f], f == 0 ? r.bias[rt] : x[rt][sub]);
             }
         }
-        __builtin_amdgcn_sched_barrier(0);
-        half8 w[RT][2];
         const bool edge = t0 + 64 > hi_min || t0 < lo_max || __any(tile.factors[64 + lane] == -INFINITY);
-        weights<D, RT>(r, x, tile.factors, t0, scaled, edge, w);
+        __builtin_amdgcn_sched_barrier(0);
+        if (scaled) unscale<D, RT>(r, x);
+        float top[RT];
+        exponents<D, RT>(x, tile.factors, top);
+        if (edge) mask<D, RT>(r, x, tile.factors, t0, top);
+        raise<D, RT>(r, top);
+        half8 w[RT][2];
+        weights<D, RT>(r, x, tile.factors, w);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -555,7 +595,7 @@ template <bool BF16, int D, int RT>
 __global__ __launch_bounds__(256, 2) void rows_kernel(Kv4AttentionProblem p, Plan plan)
 {
     __shared__ __attribute__((aligned(16))) Tile<D> buffers[2];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     int x = blockIdx.x;
     const int g = x % p.cache.Hkv;
     x /= p.cache.Hkv;
@@ -596,7 +636,7 @@ __global__ __launch_bounds__(256, 2) void split_kernel(Kv4AttentionProblem p, Pl
     __shared__ __attribute__((aligned(16))) float lds[kWaves][192];
     __shared__ __attribute__((aligned(16))) float sums[kWaves][R][PITCH];
     __shared__ float2 tops[kWaves][R];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     int x = blockIdx.x;
     const int g = x % p.cache.Hkv;
     x /= p.cache.Hkv;
@@ -665,7 +705,7 @@ __global__ __launch_bounds__(64 * WAVES) void join_kernel(Kv4AttentionProblem p,
     constexpr int EACH = D / 64;
     __shared__ float sums[WAVES][D];
     __shared__ float ls[WAVES];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int64_t rows = p.T * p.Hq;
     for (int64_t at = blockIdx.x; at < rows; at += gridDim.x) {
         const int64_t t = at / p.Hq;
