@@ -476,6 +476,20 @@ struct Tile {
     float factors[192];
 };
 
+// Asks the scheduler to keep the reads of N operands AHEAD before the RT matrix
+// instructions that take each.
+template <int N, int RT>
+__device__ inline void reads_ahead()
+{
+    constexpr int AHEAD = 6;
+    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, RT, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+}
+
 // The same for a workgroup whose waves have rows of their own: wave i unpacks
 // tokens 16 i .. of each tile into LDS for all of them, a tile ahead.  from, to:
 // what some row of the workgroup sees.
@@ -546,6 +560,7 @@ __device__ inline void attend_shared(const Kv4AttentionProblem& p, const Sequenc
                 for (int rt = 0; rt < RT; ++rt) x[rt][sub] = mfma(a, r.q[rt][f], f == 0 ? r.bias[rt] : x[rt][sub]);
             }
         }
+        reads_ahead<4 * (D / 32), RT>();
         const bool edge = t0 + 64 > hi_min || t0 < lo_max || __any(tile.factors[64 + lane] == -INFINITY);
         __builtin_amdgcn_sched_barrier(0);
         if (scaled) unscale<D, RT>(r, x);
@@ -567,6 +582,7 @@ __device__ inline void attend_shared(const Kv4AttentionProblem& p, const Sequenc
                 for (int rt = 0; rt < RT; ++rt) r.o[rt][n] = mfma(a, w[rt][i], r.o[rt][n]);
             }
         }
+        reads_ahead<2 * (D / 16), RT>();
     }
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) r.l[rt] = row_sum(r.l[rt]);
