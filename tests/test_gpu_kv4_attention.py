@@ -223,7 +223,7 @@ def test_rows_behind_the_last_sequence_and_parts_of_a_projection(dev):
 
 def test_same_bits_every_time_and_alone(dev):
     """The same call twice gives the same bits; on another stream too; a sequence's rows do not
-    depend on the others in a call of the same sizes."""
+    depend on the other queries, or on their pages' contents, in a call of the same lengths."""
     news, olds = [1] * 6, [3000, 10, 640, 64, 63, 1025]
     host, table, _ = make(news, olds, 2, 128, 64, 12)
     q = queries(6, 16, 128, "float16")
@@ -232,7 +232,9 @@ def test_same_bits_every_time_and_alone(dev):
     assert np.array_equal(first, again)
     other = q.clone()
     other[1:] = 0
-    alone, _ = run(dev, other, host, table, [3000, 0, 0, 0, 0, 0], None, max_kv=3000)
+    elsewhere = table.copy()
+    elsewhere[1:] = table[0]
+    alone, _ = run(dev, other, host, elsewhere, olds, None, max_kv=3000)
     assert np.array_equal(first[0], alone[0])
     s = torch.cuda.Stream()
     with torch.cuda.stream(s):

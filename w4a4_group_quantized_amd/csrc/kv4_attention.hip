@@ -49,12 +49,24 @@ constexpr int64_t kMaxBlocks = (1 << 24) - 1;
 constexpr float kTiny = 0x1p-80f;      // the least scale of values: 2^8 / kTiny, 2^30 times, stays finite
 constexpr float kLazy = 8.0f;
 
+// How a call is cut (launch_kv4_attention).
 struct Plan {
-    int tiles;          // row tiles of a sequence and key head that the grid holds (kernels stride over more)
-    int nsplit;         // shares of the cached tokens
-    int chunk;          // tokens of a share but the last
-    float* part_o;      // [nsplit, T * Hq, D], shares' sums relative to their M
-    float2* part_ml;    // [nsplit, T * Hq] of (M, l)
+    int tiles;          // row tiles of a sequence and key head that the grid holds (workgroups stride over more)
+    bool share;         // the workgroups share all units of the call evenly and leave the sums of the row tiles
+                        // that they have parts of; else each takes whole row tiles
+    bool sorted;        // (whole tiles) the longest of at most kSorted sequences first
+    float* part_o;      // [2 workgroups, rows of a tile, D], sums relative to their M
+    float2* part_ml;    // [2 workgroups, rows of a tile] of (M, l)
+    struct Split* splits;
+};
+
+// A row tile that several workgroups share.  Each of them keeps two records: of
+// the one that it goes on with, and of the one that it begins and others end.
+struct Split {
+    int64_t q0;         // first query of the sequence
+    int row0, rows;     // first row and live rows of the tile (rows 0: no record)
+    int g;              // key head
+    int first, last;    // its workgroups
 };
 
 __device__ inline half8 mfma_operand(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
@@ -134,8 +146,13 @@ __device__ inline int key_number(int quad, int f)
     return 128 * (f / 4) + 32 * quad + 8 * (f % 4);
 }
 
-template <bool BF16, int D, int RT>
-__device__ inline void load_rows(const Kv4AttentionProblem& p, const Sequence& s, int g, int row0, Rows<D, RT>& r)
+template <int D, int RT>
+struct RawRows {
+    uint4 q[RT][D / 32];
+};
+
+template <int D, int RT>
+__device__ inline void fetch_rows(const Kv4AttentionProblem& p, const Sequence& s, int g, int row0, RawRows<D, RT>& raw)
 {
     const int lane = threadIdx.x & 63, quad = lane >> 4;
     const int share = p.Hq / p.cache.Hkv;
@@ -143,19 +160,36 @@ __device__ inline void load_rows(const Kv4AttentionProblem& p, const Sequence& s
     for (int rt = 0; rt < RT; ++rt) {
         const int row = row0 + 16 * rt + (lane & 15);
         const bool live = row < s.n * share;
-        const int i = live ? row / share : 0, h = live ? row - i * share : 0;
-        const uint16_t* q = static_cast<const uint16_t*>(p.q) + (s.q0 + i) * p.ldq + (int64_t)(g * share + h) * D;
+        const int i = row / share;
+        const uint16_t* q = static_cast<const uint16_t*>(p.q) + (s.q0 + i) * p.ldq + (int64_t)(g * share + row - i * share) * D;
+#pragma unroll
+        for (int f = 0; f < D / 32; ++f) {
+            raw.q[rt][f] = make_uint4(0, 0, 0, 0);
+            if (live) raw.q[rt][f] = *reinterpret_cast<const uint4*>(q + key_number<D>(quad, f));
+        }
+    }
+}
+
+template <bool BF16, int D, int RT>
+__device__ inline void make_rows(const Kv4AttentionProblem& p, const Sequence& s, int row0, const RawRows<D, RT>& raw,
+                                 Rows<D, RT>& r)
+{
+    const int lane = threadIdx.x & 63;
+    const int share = p.Hq / p.cache.Hkv;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const int row = row0 + 16 * rt + (lane & 15);
+        const bool live = row < s.n * share;
+        const int i = live ? row / share : 0;
         float x[D / 4], most = 0.0f;
 #pragma unroll
         for (int f = 0; f < D / 32; ++f) {
-            if (live) {
-                rotary::load8<BF16 ? 2 : 1>(q, key_number<D>(quad, f), x + 8 * f);
-            } else {
+            const uint32_t words[4] = {raw.q[rt][f].x, raw.q[rt][f].y, raw.q[rt][f].z, raw.q[rt][f].w};
 #pragma unroll
-                for (int k = 0; k < 8; ++k) x[8 * f + k] = 0.0f;
+            for (int k = 0; k < 8; ++k) {
+                x[8 * f + k] = e4m3::from16<BF16>((uint16_t)(words[k / 2] >> (16 * (k % 2))));
+                most = fmaxf(most, fabsf(x[8 * f + k]));
             }
-#pragma unroll
-            for (int k = 0; k < 8; ++k) most = fmaxf(most, fabsf(x[8 * f + k]));
         }
         most = row_max(most);
         // rows outside fp16's comfortable range are brought to 16..32 by a power of two
@@ -168,8 +202,7 @@ __device__ inline void load_rows(const Kv4AttentionProblem& p, const Sequence& s
             half8 v;
             constexpr int order[8] = {0, 4, 1, 5, 2, 6, 3, 7};
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                v[k] = (_Float16)__builtin_amdgcn_ldexpf(x[8 * f + order[k]], e);
+            for (int k = 0; k < 8; ++k) v[k] = (_Float16)__builtin_amdgcn_ldexpf(x[8 * f + order[k]], e);
             r.q[rt][f] = v;
             r.bias[rt] = mfma(mfma_operand(0x80808080, 0x80808080, 0x80808080, 0x80808080), v, r.bias[rt]);
         }
@@ -375,9 +408,10 @@ __device__ inline void wave_sync()
 constexpr float kLog2e = 1.44269504f;
 
 // The tokens [from, to) in tiles of 64, `step` apart, each unpacked by the wave
-// for itself; `factors`: 192 floats of the wave.
-template <int D, int RT>
-__device__ inline void attend(const Kv4AttentionProblem& p, const Sequence& s, int g, int from, int to, int step,
+// for itself; `factors`: 192 floats of the wave.  The rows are fetched and made
+// in the shadow of the first tokens' loads.
+template <bool BF16, int D, int RT>
+__device__ inline void attend(const Kv4AttentionProblem& p, const Sequence& s, int g, int row0, int from, int to, int step,
                               int lo_max, int hi_min, Rows<D, RT>& r, float* factors)
 {
     const Kv4Cache& c = p.cache;
@@ -386,58 +420,69 @@ __device__ inline void attend(const Kv4AttentionProblem& p, const Sequence& s, i
     const int last = (int)p.cols - 1;
     const float factor = p.scale * kLog2e * 0x1p20f;
     const int key_at = (lane & 15) * (D / 2) + quad * (D == 64 ? 8 : 16), value_at = lane * (D / 8);
-    const bool scaled = any_scaled(r.unit);
-    if (from >= to) return;
 
+    // Tiles in flight besides the one at hand: with one, a wave's 9 KB do not cover
+    // the memory's latency; two do not fit the registers of the larger rows.
+    constexpr int DEPTH = 1;
     // lane's token of the tile at t: its row in the cache (row 0 where there is none)
+    struct Ahead {
+        Codes<D> k, v;
+        float ks, vs;
+        int64_t row;
+        bool valid;
+    } ahead[DEPTH];
     int page = 0;
-    int64_t row = 0;
-    bool valid = false;
-    Codes<D> k, v;
-    float ks = 0.0f, vs = 0.0f;
     const auto look = [&](int t) { page = table[min((t + lane) >> c.shift, last)]; };
-    const auto locate = [&](int t) {
-        valid = t + lane < to && page >= 0 && page < c.pages;
-        row = valid ? (((int64_t)page * c.Hkv + g) << c.shift) + ((t + lane) & (c.page - 1)) : 0;
+    const auto locate = [&](int t, Ahead& a) {
+        a.valid = t + lane < to && page >= 0 && page < c.pages;
+        a.row = a.valid ? (((int64_t)page * c.Hkv + g) << c.shift) + ((t + lane) & (c.page - 1)) : 0;
     };
-    const auto base = [&](int sub) {
-        const uint32_t a = __builtin_amdgcn_readlane((uint32_t)row, 16 * sub);
-        const uint32_t b = __builtin_amdgcn_readlane((uint32_t)(row >> 32), 16 * sub);
-        return (int64_t)((uint64_t)b << 32 | a) * (D / 2);
+    const auto base = [&](const Ahead& a, int sub) {
+        const uint32_t low = __builtin_amdgcn_readlane((uint32_t)a.row, 16 * sub);
+        const uint32_t high = __builtin_amdgcn_readlane((uint32_t)(a.row >> 32), 16 * sub);
+        return (int64_t)((uint64_t)high << 32 | low) * (D / 2);
     };
-    const auto load_k = [&]() {
-        ks = c.k_scales[row];
+    const auto load_k = [&](Ahead& a) {
+        a.ks = c.k_scales[a.row];
 #pragma unroll
-        for (int sub = 0; sub < 4; ++sub) load_codes<D>(k, sub, c.k_codes + base(sub) + key_at);
+        for (int sub = 0; sub < 4; ++sub) load_codes<D>(a.k, sub, c.k_codes + base(a, sub) + key_at);
     };
-    const auto load_v = [&]() {
-        vs = c.v_scales[row];
+    const auto load_v = [&](Ahead& a) {
+        a.vs = c.v_scales[a.row];
 #pragma unroll
-        for (int sub = 0; sub < 4; ++sub) load_values<D>(v, sub, c.v_codes + base(sub) + value_at);
+        for (int sub = 0; sub < 4; ++sub) load_values<D>(a.v, sub, c.v_codes + base(a, sub) + value_at);
     };
+    RawRows<D, RT> raw;
     look(from);
-    locate(from);
-    load_k();
-    load_v();
-    look(from + step);
+    fetch_rows<D, RT>(p, s, g, row0, raw);
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) {
+        locate(from + i * step, ahead[i]);
+        look(from + (i + 1) * step);
+        load_k(ahead[i]);
+        load_v(ahead[i]);
+    }
+    make_rows<BF16, D, RT>(p, s, row0, raw, r);
+    const bool scaled = any_scaled(r.unit);
 
-    for (int t0 = from; t0 < to; t0 += step) {
-        factors[lane] = key_factor(valid, ks, factor);
-        put_value_factors<64>(factors, lane, valid, vs);
-        const bool edge = t0 + 64 > hi_min || t0 < lo_max || !__all(valid);
+    const auto tile = [&](int t0, Ahead& a) {
+        factors[lane] = key_factor(a.valid, a.ks, factor);
+        put_value_factors<64>(factors, lane, a.valid, a.vs);
+        const bool edge = t0 + 64 > hi_min || t0 < lo_max || !__all(a.valid);
         wave_sync();
         float4v x[RT][4];
 #pragma unroll
         for (int sub = 0; sub < 4; ++sub) {
 #pragma unroll
             for (int f = 0; f < D / 32; ++f) {
-                const half8 a = key_operand(k.w[sub][f]);
+                const half8 key = key_operand(a.k.w[sub][f]);
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) x[rt][sub] = mfma(a, r.q[rt][f], f == 0 ? r.bias[rt] : x[rt][sub]);
+                for (int rt = 0; rt < RT; ++rt) x[rt][sub] = mfma(key, r.q[rt][f], f == 0 ? r.bias[rt] : x[rt][sub]);
             }
         }
-        locate(t0 + step);
-        load_k();
+        locate(t0 + DEPTH * step, a);
+        look(t0 + (DEPTH + 1) * step);
+        load_k(a);
         if (scaled) unscale<D, RT>(r, x);
         float top[RT];
         exponents<D, RT>(x, factors, top);
@@ -451,9 +496,9 @@ __device__ inline void attend(const Kv4AttentionProblem& p, const Sequence& s, i
             for (int rt = 0; rt < RT; ++rt) r.w[rt] = mfma(eights(), w[rt][i], r.w[rt]);
 #pragma unroll
             for (int n = 0; n < D / 32; ++n) {
-                const uint2 a = value_low(v.w[2 * i][n]), b = value_low(v.w[2 * i + 1][n]);
-                const uint2 c = value_high(v.w[2 * i][n]), d = value_high(v.w[2 * i + 1][n]);
-                const half8 even = mfma_operand(a.x, a.y, b.x, b.y), odd = mfma_operand(c.x, c.y, d.x, d.y);
+                const uint2 b0 = value_low(a.v.w[2 * i][n]), b1 = value_low(a.v.w[2 * i + 1][n]);
+                const uint2 c0 = value_high(a.v.w[2 * i][n]), c1 = value_high(a.v.w[2 * i + 1][n]);
+                const half8 even = mfma_operand(b0.x, b0.y, b1.x, b1.y), odd = mfma_operand(c0.x, c0.y, c1.x, c1.y);
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
                     r.o[rt][2 * n] = mfma(even, w[rt][i], r.o[rt][2 * n]);
@@ -461,8 +506,12 @@ __device__ inline void attend(const Kv4AttentionProblem& p, const Sequence& s, i
                 }
             }
         }
-        load_v();
-        look(t0 + 2 * step);
+        load_v(a);
+    };
+    for (int t0 = from; t0 < to; t0 += DEPTH * step) {
+#pragma unroll
+        for (int i = 0; i < DEPTH; ++i)
+            if (t0 + i * step < to) tile(t0 + i * step, ahead[i]);
     }
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) r.l[rt] = row_sum(r.l[rt]);
@@ -622,7 +671,9 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(Kv4AttentionProblem p, Pla
         // (the last rows see the most tokens: first)
         const int top = (tiles - 1 - k) * kWaves * 16 * RT, row0 = top + wave * 16 * RT;
         Rows<D, RT> r;
-        load_rows<BF16, D, RT>(p, s, g, row0, r);
+        RawRows<D, RT> raw;
+        fetch_rows<D, RT>(p, s, g, row0, raw);
+        make_rows<BF16, D, RT>(p, s, row0, raw, r);
         const int i0 = row0 / share, i1 = min(row0 + 16 * RT - 1, all - 1) / share;
         const int end = min(top + kWaves * 16 * RT, all) - 1;
         attend_shared<D, RT>(p, s, g, seen_lo(p, s, top / share) & ~63, seen_hi(p, s, end / share), seen_lo(p, s, i1),
@@ -642,165 +693,318 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(Kv4AttentionProblem p, Pla
     }
 }
 
-// Few rows: the waves of a workgroup have the same rows and every fourth tile
-// of its share of the tokens; their sums meet in LDS.  With one share the rows
-// are written, with more the sums go to the workspace.
-template <bool BF16, int D, int RT>
-__global__ __launch_bounds__(256, 2) void split_kernel(Kv4AttentionProblem p, Plan plan)
-{
-    constexpr int R = 16 * RT, PITCH = D + 4;
-    __shared__ __attribute__((aligned(16))) float lds[kWaves][192];
-    __shared__ __attribute__((aligned(16))) float sums[kWaves][R][PITCH];
-    __shared__ float2 tops[kWaves][R];
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    int x = blockIdx.x;
-    const int g = x % p.cache.Hkv;
-    x /= p.cache.Hkv;
-    const int first = x % plan.tiles;
-    x /= plan.tiles;
-    const int part = x % plan.nsplit;
-    const Sequence s = sequence(p, x / plan.nsplit);
-    const int share = p.Hq / p.cache.Hkv, all = s.n * share, tiles = (all + R - 1) / R;
-    for (int k = first; k < tiles; k += plan.tiles) {
-        const int row0 = k * R;
-        const int i0 = row0 / share, i1 = min(row0 + R - 1, all - 1) / share;
-        const int begin = (seen_lo(p, s, i0) & ~63) + part * plan.chunk, end = seen_hi(p, s, i1);
-        const int to = part == plan.nsplit - 1 ? end : min(end, begin + plan.chunk);
-        Rows<D, RT> r;
-        load_rows<BF16, D, RT>(p, s, g, row0, r);
-        attend<D, RT>(p, s, g, begin + 64 * wave, to, 64 * kWaves, seen_lo(p, s, i1), seen_hi(p, s, i0), r, lds[wave]);
-        __syncthreads();                                   // (the rows before are out of LDS)
-        if (lane < 16) {
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) tops[wave][16 * rt + lane] = make_float2(r.m[rt], r.l[rt]);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            const int row = 16 * rt + (lane & 15);
-            float m = tops[0][row].x;
-#pragma unroll
-            for (int v = 1; v < kWaves; ++v) m = fmaxf(m, tops[v][row].x);
-            const float by = r.m[rt] == m ? 1.0f : __builtin_amdgcn_exp2f(r.m[rt] - m);
-#pragma unroll
-            for (int t = 0; t < D / 16; ++t)
-                *reinterpret_cast<float4v*>(&sums[wave][row][16 * t + 4 * (lane >> 4)]) = row_values(r, rt, t, by);
-        }
-        __syncthreads();
-        for (int e = threadIdx.x; e < R * (D / 4); e += 256) {
-            const int row = e / (D / 4), d = e % (D / 4) * 4;
-            if (row0 + row >= all) continue;
-            float m = tops[0][row].x, l = 0.0f;
-#pragma unroll
-            for (int v = 1; v < kWaves; ++v) m = fmaxf(m, tops[v][row].x);
-            float4v o = {};
-#pragma unroll
-            for (int v = 0; v < kWaves; ++v) {
-                const float2 ml = tops[v][row];
-                l += ml.y * (ml.x == m ? 1.0f : __builtin_amdgcn_exp2f(ml.x - m));
-                o += *reinterpret_cast<const float4v*>(&sums[v][row][d]);
-            }
-            const int i = (row0 + row) / share;
-            const int64_t at = (s.q0 + i) * p.Hq + g * share + (row0 + row - i * share);
-            if (plan.nsplit == 1) {
-                store4<BF16>(p.out, at * D + d, o * (l == 0.0f ? 0.0f : 1.0f / l));
-                if (p.lse && d == 0) p.lse[at] = log_sum(m, l);
-            } else {
-                const int64_t slot = (int64_t)part * (p.T * p.Hq) + at;
-                *reinterpret_cast<float4v*>(plan.part_o + slot * D + d) = o;
-                if (d == 0) plan.part_ml[slot] = make_float2(m, l);
-            }
-        }
-    }
-}
+// Few rows: the waves of a workgroup have the same rows and every fourth 64
+// tokens; their sums meet in LDS.  256 tokens of a row tile are a unit.
+constexpr int kUnit = 64 * kWaves;
+constexpr int kSorted = 256;     // sequences that a workgroup sorts: one a thread
 
-// The shares of one row added in their order, WAVES waves a row.
-template <bool BF16, int D, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void join_kernel(Kv4AttentionProblem p, Plan plan)
-{
-    constexpr int EACH = D / 64;
-    __shared__ float sums[WAVES][D];
-    __shared__ float ls[WAVES];
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int64_t rows = p.T * p.Hq;
-    for (int64_t at = blockIdx.x; at < rows; at += gridDim.x) {
-        const int64_t t = at / p.Hq;
-        if (p.cu_q && (t < p.cu_q[0] || t >= p.cu_q[p.B])) continue;    // no sequence's
-        float m = -INFINITY;
-        for (int i = lane; i < plan.nsplit; i += 64) m = fmaxf(m, plan.part_ml[i * rows + at].x);
-#pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-        float o[EACH] = {}, l = 0.0f;
-#pragma unroll 4
-        for (int i = wave; i < plan.nsplit; i += WAVES) {
-            const float2 ml = plan.part_ml[i * rows + at];
-            const float by = ml.x == m ? 1.0f : __builtin_amdgcn_exp2f(ml.x - m);
-            const float* from = plan.part_o + (i * rows + at) * D + lane * EACH;
-            l = fmaf(ml.y, by, l);
-#pragma unroll
-            for (int e = 0; e < EACH; ++e) o[e] = fmaf(from[e], by, o[e]);
-        }
-#pragma unroll
-        for (int e = 0; e < EACH; ++e) sums[wave][lane * EACH + e] = o[e];
-        if (lane == 0) ls[wave] = l;
-        __syncthreads();
-        l = 0.0f;
-#pragma unroll
-        for (int v = 0; v < WAVES; ++v) l += ls[v];
-        const float by = l == 0.0f ? 0.0f : 1.0f / l;
-        for (int d = threadIdx.x; d < D; d += 64 * WAVES) {
-            float sum = 0.0f;
-#pragma unroll
-            for (int v = 0; v < WAVES; ++v) sum += sums[v][d];
-            static_cast<uint16_t*>(p.out)[at * D + d] = e4m3::to16<BF16>(sum * by);
-        }
-        if (p.lse && threadIdx.x == 0) p.lse[at] = log_sum(m, l);
-        __syncthreads();                                   // (the next row's sums)
-    }
-}
-
-// How a call of these sizes is cut: waves with rows of their own where their
-// workgroups fill the chip, else shares of the tokens.
-struct Cut {
-    bool rows;
-    int rt, tiles, nsplit, chunk;
+template <int D, int RT>
+struct Meeting {
+    float factors[kWaves][192];
+    float sums[kWaves][16 * RT][D + 4];
+    float2 tops[kWaves][16 * RT];
 };
 
-Cut cut(const Kv4AttentionProblem& p, int64_t span)
+// Units [u0, u1) of a row tile, counted from the token `base`.  slot < 0: those
+// are all, and the rows are written; else the sums go to the workspace.
+template <bool BF16, int D, int RT>
+__device__ inline void few_rows(const Kv4AttentionProblem& p, const Plan& plan, const Sequence& s, int g, int row0, int base,
+                                int u0, int u1, int slot, Meeting<D, RT>& lds)
 {
-    const int64_t share = p.Hq / p.cache.Hkv, all = (int64_t)p.max_q * share, pairs = (int64_t)p.B * p.cache.Hkv;
+    constexpr int R = 16 * RT;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int share = p.Hq / p.cache.Hkv, all = s.n * share;
+    const int i0 = row0 / share, i1 = min(row0 + R - 1, all - 1) / share;
+    // (tokens that no row of the tile sees are passed over)
+    const int from = max(base + u0 * kUnit, seen_lo(p, s, i0) & ~(kUnit - 1)) + 64 * wave;
+    const int to = (int)min((int64_t)seen_hi(p, s, i1), base + (int64_t)u1 * kUnit);
+    Rows<D, RT> r;
+    attend<BF16, D, RT>(p, s, g, row0, from, to, kUnit, seen_lo(p, s, i1), seen_hi(p, s, i0), r, lds.factors[wave]);
+    __syncthreads();                                       // (the rows before are out of LDS)
+    if (lane < 16) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) lds.tops[wave][16 * rt + lane] = make_float2(r.m[rt], r.l[rt]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const int row = 16 * rt + (lane & 15);
+        float m = lds.tops[0][row].x;
+#pragma unroll
+        for (int v = 1; v < kWaves; ++v) m = fmaxf(m, lds.tops[v][row].x);
+        const float by = r.m[rt] == m ? 1.0f : __builtin_amdgcn_exp2f(r.m[rt] - m);
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t)
+            *reinterpret_cast<float4v*>(&lds.sums[wave][row][16 * t + 4 * (lane >> 4)]) = row_values(r, rt, t, by);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < R * (D / 4); e += 64 * kWaves) {
+        const int row = e / (D / 4), d = e % (D / 4) * 4;
+        if (row0 + row >= all) break;
+        float m = lds.tops[0][row].x, l = 0.0f;
+#pragma unroll
+        for (int v = 1; v < kWaves; ++v) m = fmaxf(m, lds.tops[v][row].x);
+        float4v o = {};
+#pragma unroll
+        for (int v = 0; v < kWaves; ++v) {
+            const float2 ml = lds.tops[v][row];
+            l += ml.y * (ml.x == m ? 1.0f : __builtin_amdgcn_exp2f(ml.x - m));
+            o += *reinterpret_cast<const float4v*>(&lds.sums[v][row][d]);
+        }
+        if (slot < 0) {
+            const int i = (row0 + row) / share;
+            const int64_t at = (s.q0 + i) * p.Hq + g * share + (row0 + row - i * share);
+            store4<BF16>(p.out, at * D + d, o * (l == 0.0f ? 0.0f : 1.0f / l));
+            if (p.lse && d == 0) p.lse[at] = log_sum(m, l);
+        } else {
+            *reinterpret_cast<float4v*>(plan.part_o + ((int64_t)slot * R + row) * D + d) = o;
+            if (d == 0) plan.part_ml[slot * R + row] = make_float2(m, l);
+        }
+    }
+}
+
+// The first token of a sequence's first unit, its row tiles, the units of one.
+struct Extent {
+    int base, tiles, units;
+};
+template <int R>
+__device__ inline Extent extent(const Kv4AttentionProblem& p, const Sequence& s)
+{
+    const int base = seen_lo(p, s, 0) & ~(kUnit - 1);
+    // (at least one: rows that see nothing are written too)
+    return {base, (s.n * (p.Hq / p.cache.Hkv) + R - 1) / R, max(1, (s.kv - base + kUnit - 1) / kUnit)};
+}
+
+// sum over the workgroup; `lds`: a number a wave
+__device__ inline int64_t block_sum(int64_t x, int64_t* lds)
+{
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) x += __shfl_xor(x, o);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = 0;
+#pragma unroll
+    for (int v = 0; v < kWaves; ++v) x += lds[v];
+    return x;
+}
+
+template <bool BF16, int D, int RT>
+__global__ __launch_bounds__(256, 2) void few_kernel(Kv4AttentionProblem p, Plan plan)
+{
+    constexpr int R = 16 * RT;
+    __shared__ __attribute__((aligned(16))) Meeting<D, RT> lds;
+    const int Hkv = p.cache.Hkv;
+    if (!plan.share) {
+        int x = blockIdx.x;
+        const int g = x % Hkv;
+        x /= Hkv;
+        const int first = x % plan.tiles;
+        x /= plan.tiles;
+        if (plan.sorted) {
+            // workgroup x takes the x-th longest sequence
+            __shared__ __attribute__((aligned(16))) int lengths[kSorted];
+            __shared__ int chosen;
+            const int b = threadIdx.x;
+            int mine = -1, rank = 0;
+            if (b < p.B) mine = extent<R>(p, sequence(p, b)).units;
+            lengths[b] = mine;
+            __syncthreads();
+            for (int i = 0; i < p.B; i += 4) {
+                const int4 other = *reinterpret_cast<const int4*>(lengths + i);
+                rank += (other.x > mine || (other.x == mine && i < b)) + (other.y > mine || (other.y == mine && i + 1 < b)) +
+                        (other.z > mine || (other.z == mine && i + 2 < b)) + (other.w > mine || (other.w == mine && i + 3 < b));
+            }
+            if (b < p.B && rank == x) chosen = b;
+            __syncthreads();
+            x = __builtin_amdgcn_readfirstlane(chosen);
+        }
+        const Sequence s = sequence(p, x);
+        const Extent e = extent<R>(p, s);
+        for (int k = first; k < e.tiles; k += plan.tiles) few_rows<BF16, D, RT>(p, plan, s, g, k * R, e.base, 0, e.units, -1, lds);
+        return;
+    }
+    // Units of all sequences in a row, an even share for each workgroup.
+    __shared__ int64_t sums[kWaves];
+    __shared__ int64_t before;
+    __shared__ int start;
+    const auto units = [&](int b) {
+        const Sequence s = sequence(p, b);
+        const Extent e = extent<R>(p, s);
+        return (int64_t)Hkv * e.tiles * e.units;
+    };
+    int64_t total = 0;
+    for (int b = threadIdx.x; b < p.B; b += 64 * kWaves) total += units(b);
+    total = block_sum(total, sums);
+    const int64_t each = max((int64_t)1, (total + gridDim.x - 1) / gridDim.x);
+    int64_t u = blockIdx.x * each;
+    const int64_t end = min(total, u + each);
+    if (threadIdx.x == 0) plan.splits[2 * blockIdx.x].rows = plan.splits[2 * blockIdx.x + 1].rows = 0;
+    if (u >= end) return;
+    // the sequence that holds unit u
+    int64_t seen = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 64 * kWaves) {
+        const int b = b0 + threadIdx.x, lane = threadIdx.x & 63;
+        const int64_t mine = b < p.B ? units(b) : 0;
+        int64_t upto = mine;                               // (with the lanes before)
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int64_t x = __shfl_up(upto, o);
+            if (lane >= o) upto += x;
+        }
+        __syncthreads();
+        if (lane == 63) sums[threadIdx.x >> 6] = upto;
+        __syncthreads();
+        int64_t ahead = seen;
+        for (int v = 0; v < kWaves; ++v) {
+            if (v < (int)(threadIdx.x >> 6)) ahead += sums[v];
+            seen += sums[v];
+        }
+        if (ahead + upto - mine <= u && u < ahead + upto) before = ahead + upto - mine, start = b;
+        if (seen > u) break;
+    }
+    __syncthreads();
+    int b = start;
+    int64_t rest = u - before;                             // units of the sequence before u
+    while (u < end) {
+        const Sequence s = sequence(p, b);
+        const Extent e = extent<R>(p, s);
+        const int64_t whole = (int64_t)e.tiles * e.units;
+        if (rest >= Hkv * whole) {
+            rest -= Hkv * whole;
+            ++b;
+            continue;
+        }
+        const int g = (int)(rest / whole), k = (int)((rest - g * whole) / e.units);
+        const int u0 = (int)(rest - g * whole - (int64_t)k * e.units);
+        const int n = (int)min((int64_t)(e.units - u0), end - u);
+        int slot = -1;
+        if (n < e.units) {
+            slot = 2 * blockIdx.x + (u0 == 0);
+            const int rows = min(R, s.n * (p.Hq / Hkv) - k * R);
+            const int64_t at = u - u0;                     // its first unit
+            if (threadIdx.x == 0) plan.splits[slot] = {s.q0, k * R, rows, g, (int)(at / each), (int)((at + e.units - 1) / each)};
+        }
+        few_rows<BF16, D, RT>(p, plan, s, g, k * R, e.base, u0, u0 + n, slot, lds);
+        u += n;
+        rest += n;
+    }
+}
+
+// The sums of the row tiles that several workgroups share, in the order of the
+// tokens.  The workgroups here stand for those: each takes every n-th row of the
+// tiles that it was one of n for.  PARTS waves a row, WAVES in all.
+template <bool BF16, int D, int RT, int WAVES, int PARTS>
+__global__ __launch_bounds__(64 * WAVES) void join_kernel(Kv4AttentionProblem p, Plan plan)
+{
+    constexpr int EACH = D / 64, R = 16 * RT;
+    static_assert(PARTS == 1 || PARTS == WAVES, "");
+    __shared__ float sums[PARTS][D];
+    __shared__ float ls[PARTS];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int part = PARTS == 1 ? 0 : wave;
+    const int share = p.Hq / p.cache.Hkv;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        const Split s = plan.splits[2 * blockIdx.x + which];
+        if (s.rows == 0) continue;
+        const int n = s.last - s.first + 1;
+        // (the first workgroup's sums are its second ones)
+        const auto slot = [&](int i) { return (int64_t)(2 * (s.first + i) + (i == 0)) * R; };
+        for (int row = (int)blockIdx.x - s.first + (PARTS == 1 ? wave * n : 0); row < s.rows; row += n * (WAVES / PARTS)) {
+            float m = -INFINITY, l = 0.0f, o[EACH] = {};
+            for (int i = lane; i < n; i += 64) m = fmaxf(m, plan.part_ml[slot(i) + row].x);
+#pragma unroll
+            for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
+#pragma unroll 4
+            for (int i = part; i < n; i += PARTS) {
+                const float2 ml = plan.part_ml[slot(i) + row];
+                const float by = ml.x == m ? 1.0f : __builtin_amdgcn_exp2f(ml.x - m);
+                const float* from = plan.part_o + (slot(i) + row) * D + lane * EACH;
+                l = fmaf(ml.y, by, l);
+#pragma unroll
+                for (int e = 0; e < EACH; ++e) o[e] = fmaf(from[e], by, o[e]);
+            }
+            if (PARTS > 1) {
+                __syncthreads();                           // (the row before is out of LDS)
+#pragma unroll
+                for (int e = 0; e < EACH; ++e) sums[part][lane * EACH + e] = o[e];
+                if (lane == 0) ls[part] = l;
+                __syncthreads();
+                if (part != 0) continue;
+                l = 0.0f;
+#pragma unroll
+                for (int e = 0; e < EACH; ++e) o[e] = 0.0f;
+#pragma unroll
+                for (int v = 0; v < PARTS; ++v) {
+                    l += ls[v];
+#pragma unroll
+                    for (int e = 0; e < EACH; ++e) o[e] += sums[v][lane * EACH + e];
+                }
+            }
+            const float by = l == 0.0f ? 0.0f : 1.0f / l;
+            const int i = (s.row0 + row) / share;
+            const int64_t at = (s.q0 + i) * p.Hq + s.g * share + (s.row0 + row - i * share);
+#pragma unroll
+            for (int e = 0; e < EACH; ++e)
+                static_cast<uint16_t*>(p.out)[at * D + lane * EACH + e] = e4m3::to16<BF16>(o[e] * by);
+            if (p.lse && lane == 0) p.lse[at] = log_sum(m, l);
+        }
+    }
+}
+
+// How a call of these sizes is cut.
+struct Cut {
+    bool rows;                  // waves have rows of their own
+    bool share, sorted;
+    int rt, tiles;
+    int64_t blocks;
+    bool deep;                  // a row tile may be in many parts
+};
+
+Cut cut(const Kv4AttentionProblem& p)
+{
+    const int64_t all = (int64_t)p.max_q * (p.Hq / p.cache.Hkv), pairs = (int64_t)p.B * p.cache.Hkv;
     const int cus = compute_units() > 0 ? compute_units() : 256;
     Cut c{};
     c.rt = p.cache.D == 256 || all <= 16 ? 1 : 2;
-    c.nsplit = 1;
     const int64_t wide = (all + 16 * c.rt * kWaves - 1) / (16 * c.rt * kWaves);
     c.rows = all > 16 * c.rt && pairs * wide >= cus;
     const int64_t narrow = (all + 16 * c.rt - 1) / (16 * c.rt);
     // (workgroups stride over row tiles beyond the grid's limit of 2^32 threads)
     c.tiles = (int)std::max<int64_t>(1, std::min<int64_t>(c.rows ? wide : narrow, kMaxBlocks / pairs));
-    if (!c.rows) {
-        const int64_t blocks = pairs * c.tiles, most = std::min<int64_t>((span + 511) / 512, 512);
-        c.nsplit = (int)std::max<int64_t>(1, std::min<int64_t>(most, (4 * cus + blocks - 1) / blocks));
+    c.blocks = pairs * c.tiles;
+    if (c.rows) return c;
+    // Row tiles of more than 5 units are shared where whole ones leave room for two
+    // workgroups a compute unit: 1 x 2048 tokens of 32 heads 11.5 us against 14, 1 x
+    // 131071 of 8 heads 34.5 against 675; up to 5 units the second launch costs more
+    // (1 x 517 of 32 heads 11.6 us against 8.7), and where the chip is full without it
+    // the starts of the parts do (64 x 4096 of 8 heads 54 us against 50).
+    const int64_t units = (p.max_kv + kUnit - 1) / kUnit, total = c.blocks * units;
+    if (units > 5 && c.blocks < 2 * cus) {
+        c.share = true;
+        c.blocks = std::min<int64_t>(total, 2 * cus);
+        // (16 waves for each row where a tile is in more than 8 parts)
+        c.deep = units * c.blocks > 8 * total;
     }
-    const int64_t each = (span + c.nsplit - 1) / c.nsplit;
-    c.chunk = (int)((each + 255) / 256 * 256);
-    c.nsplit = (int)std::max<int64_t>(1, (span + c.chunk - 1) / c.chunk);
+    // Whole ones of uneven sequences: the longest first (64 x up to 8192 tokens of 8
+    // heads 77 us to 66; not for few units, 64 x up to 512 10 us to 12).
+    c.sorted = !c.share && units > 5 && p.B > 1 && p.B <= kSorted;
     return c;
 }
 
 template <bool BF16, int D, int RT>
 hipError_t launch(const Kv4AttentionProblem& p, const Cut& c, const Plan& plan, hipStream_t stream)
 {
-    const unsigned blocks = (unsigned)((int64_t)p.B * p.cache.Hkv * c.tiles * c.nsplit);
+    const unsigned blocks = (unsigned)c.blocks;
     if (c.rows) {
         rows_kernel<BF16, D, RT><<<blocks, 256, 0, stream>>>(p, plan);
         return hipGetLastError();
     }
-    split_kernel<BF16, D, RT><<<blocks, 256, 0, stream>>>(p, plan);
-    if (c.nsplit > 1) {
-        const unsigned rows = (unsigned)std::min<int64_t>(p.T * p.Hq, 1 << 22);
-        if (c.nsplit <= 8) join_kernel<BF16, D, 1><<<rows, 64, 0, stream>>>(p, plan);
-        else join_kernel<BF16, D, 8><<<rows, 512, 0, stream>>>(p, plan);
+    few_kernel<BF16, D, RT><<<blocks, 256, 0, stream>>>(p, plan);
+    if (c.share) {
+        if (c.deep) join_kernel<BF16, D, RT, 16, 16><<<blocks, 1024, 0, stream>>>(p, plan);
+        else join_kernel<BF16, D, RT, 8, 1><<<blocks, 512, 0, stream>>>(p, plan);
     }
     return hipGetLastError();
 }
@@ -815,25 +1019,26 @@ hipError_t launch(const Kv4AttentionProblem& p, const Cut& c, const Plan& plan, 
     }
 }
 
+// the workspace: sums of two row tiles a workgroup, their (M, l), records of them
+size_t parts(const Cut& c) { return (size_t)c.blocks * 2 * 16 * c.rt; }
+
 }  // namespace
 
 size_t kv4_attention_workspace_bytes(const Kv4AttentionProblem& p)
 {
-    const Cut c = cut(p, p.max_kv);
-    return c.nsplit == 1 ? 0 : (size_t)c.nsplit * p.T * p.Hq * (p.cache.D + 2) * 4;
+    const Cut c = cut(p);
+    return c.share ? parts(c) * (p.cache.D + 2) * 4 + 2 * (size_t)c.blocks * sizeof(Split) : 0;
 }
 
 hipError_t launch_kv4_attention(const Kv4AttentionProblem& p, hipStream_t stream)
 {
-    // (a window bounds the tokens of a row tile; never more shares than the workspace is for)
-    Cut c = cut(p, p.max_kv);
-    if (p.window) {
-        const int most = c.nsplit;
-        c = cut(p, std::min<int64_t>(p.max_kv, (int64_t)p.window + p.max_q + 64));
-        c.nsplit = std::min(c.nsplit, most);
+    const Cut c = cut(p);
+    Plan plan{c.tiles, c.share, c.sorted, nullptr, nullptr, nullptr};
+    if (c.share) {
+        plan.part_o = static_cast<float*>(p.ws);
+        plan.part_ml = reinterpret_cast<float2*>(plan.part_o + parts(c) * p.cache.D);
+        plan.splits = reinterpret_cast<Split*>(plan.part_ml + parts(c));
     }
-    Plan plan{c.tiles, c.nsplit, c.chunk, static_cast<float*>(p.ws), nullptr};
-    if (c.nsplit > 1) plan.part_ml = reinterpret_cast<float2*>(plan.part_o + (int64_t)c.nsplit * p.T * p.Hq * p.cache.D);
     return p.bf16 ? launch<true>(p, c, plan, stream) : launch<false>(p, c, plan, stream);
 }
 
