@@ -532,7 +532,7 @@ apex4_status apex4_kv4_append(const void* q, const void* k, const void* v, int32
  * apex4_kv4_read: the values c * s (rounded to `type`: APEX4_F32, APEX4_F16 or
  * APEX4_BF16) of T cached tokens, k and v [T, Hkv, D], 16-byte aligned.  slots
  * [T] int64, in any order, repeated or not; a slot that is negative or behind
- * the last page gives zeros.  Limits as above, T * Hkv * D < 2^36.
+ * the last page gives zeros.  Limits as above, T * Hkv < 2^28.
  */
 apex4_status apex4_kv4_read(const void* k_codes, const float* k_scales, const void* v_codes, const float* v_scales,
                             int64_t pages, int32_t page, int32_t Hkv, int32_t D, const int64_t* slots, int64_t T,

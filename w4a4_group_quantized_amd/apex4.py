@@ -609,34 +609,72 @@ def linear_e4m3(x, qw8, sw, *, want_y32: bool = False, y=None, y32=None, workspa
     return (y, y32) if want_y32 else y
 
 
-def _rows3(t, name: str, dtype=None, shape=None, device=None) -> int:
+def _index(t, name: str) -> int:
+    """The GPU that a tensor is on."""
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name} must be a GPU tensor (this library has no CPU path)")
+    return index
+
+
+def _is(t, dtype, shape, index: int) -> bool:
+    """_need_gpu's checks as one expression, the cheapest ones that torch has: most of the time of
+    the smallest calls is these.  Where it is false, _refuse says why."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()
+
+
+def _refuse(index: int, **expected) -> None:
+    import torch
+    for name, (t, dtype, shape) in expected.items():
+        _need_gpu(t, name, dtype, shape, torch.device("cuda", index))
+    raise AssertionError(expected)
+
+
+def _rows3(t, name: str, dtype, shape, index: int) -> int:
     """Checks rows [T, heads, D] whose heads are contiguous; returns the elements between two of
     them (parts of a fused projection's output pass as they are)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor (this library has no CPU path)")
-    if t.dim() != 3 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{name} must have shape {'[T, heads, D]' if shape is None else tuple(shape)}, "
-                         f"got {tuple(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the call runs on cuda:{index}")
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
-    (T, H, D), (row, head, one) = t.shape, t.stride()
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    T, H, D = shape
+    row, head, one = t.stride()
     if (one != 1 and D > 1) or (head != D and H > 1) or (row < H * D and T > 1):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
     return row if T > 1 else H * D
 
 
-def _rotation(positions, inv_freq, T: int, device):
+def _three(t, name: str):
+    shape = t.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must have shape [T, heads, D], got {tuple(shape)}")
+    return shape
+
+
+def _rotation(positions, inv_freq, T: int, index: int):
     """(positions, frequencies, rotated numbers) as the library takes them."""
     import torch
     if positions is None or inv_freq is None:
         raise ValueError("positions and inv_freq belong together")
-    _need(positions, "positions", torch.int64, (T,), device)
-    _need_gpu(inv_freq, "inv_freq", torch.float64, None, device)
-    if inv_freq.dim() != 1:
-        raise ValueError(f"inv_freq must be [R/2], got {tuple(inv_freq.shape)}")
-    return positions.data_ptr(), inv_freq.data_ptr(), 2 * inv_freq.shape[0]
+    half = inv_freq.numel()
+    if not (_is(positions, torch.int64, (T,), index) and _is(inv_freq, torch.float64, (half,), index)):
+        _refuse(index, positions=(positions, torch.int64, (T,)), inv_freq=(inv_freq, torch.float64, (half,)))
+    return positions.data_ptr(), inv_freq.data_ptr(), 2 * half
+
+
+def _run(fn: str, index: int, *args) -> None:
+    """_call with the device by its number."""
+    import torch
+    f = getattr(lib(), fn)
+    if torch._C._cuda_getDevice() == index:
+        status = f(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = f(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != OK:
+        raise Apex4Error(fn, status)
 
 
 def rope(x, positions, inv_freq, *, interleaved: bool = False, scale: float = 1.0, out=None):
@@ -646,17 +684,18 @@ def rope(x, positions, inv_freq, *, interleaved: bool = False, scale: float = 1.
     multiplied by `scale`.  `out`: where to write, x itself to turn in place (a new contiguous
     tensor when None)."""
     import torch
-    ldx = _rows3(x, "x")
+    index = _index(x, "x")
+    T, H, D = shape = _three(x, "x")
     code = _type_code(x, "x")
-    (T, H, D), dev = x.shape, x.device
-    pos, freq, R = _rotation(positions, inv_freq, T, dev)
+    ldx = _rows3(x, "x", x.dtype, shape, index)
+    pos, freq, R = _rotation(positions, inv_freq, T, index)
     if out is None:
-        out = torch.empty((T, H, D), dtype=x.dtype, device=dev)
+        out = x.new_empty(shape)
         ldy = H * D
     else:
-        ldy = _rows3(out, "out", x.dtype, (T, H, D), dev)
-    _call("apex4_rope", dev, x.data_ptr(), code, T, H, D, ldx, pos, freq, R, int(bool(interleaved)), scale,
-          out.data_ptr(), ldy)
+        ldy = _rows3(out, "out", x.dtype, shape, index)
+    _run("apex4_rope", index, x.data_ptr(), code, T, H, D, ldx, pos, freq, R, 1 if interleaved else 0, scale,
+         out.data_ptr(), ldy)
     return out
 
 
@@ -674,17 +713,21 @@ def kv4_cache(pages: int, kv_heads: int, head_dim: int, page: int = 64, device="
 
 
 def _kv4(cache):
-    """((k_codes, k_scales, v_codes, v_scales) pointers, pages, page, heads, head dim, device)"""
+    """((k_codes, k_scales, v_codes, v_scales) pointers, pages, page, heads, head dim, GPU)"""
     import torch
     k, ks, v, vs = cache
-    if k.dim() != 4:
-        raise ValueError(f"k_codes must be [pages, heads, page, D/2], got {tuple(k.shape)}")
-    (pages, heads, page, half), dev = k.shape, k.device
-    _need(k, "k_codes", torch.uint8, (pages, heads, page, half), dev)
-    _need(ks, "k_scales", torch.float32, (pages, heads, page), dev)
-    _need(v, "v_codes", torch.uint8, (pages, heads, page // 16, 16 * half), dev)
-    _need(vs, "v_scales", torch.float32, (pages, heads, page), dev)
-    return (k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr()), pages, page, heads, 2 * half, dev
+    shape = k.shape
+    if len(shape) != 4:
+        raise ValueError(f"k_codes must be [pages, heads, page, D/2], got {tuple(shape)}")
+    index = _index(k, "k_codes")
+    pages, heads, page, half = shape
+    rows, values = (pages, heads, page), (pages, heads, page // 16, 16 * half)
+    u8, f32 = torch.uint8, torch.float32
+    if not (_is(k, u8, shape, index) and _is(ks, f32, rows, index) and _is(v, u8, values, index)
+            and _is(vs, f32, rows, index)):
+        _refuse(index, k_codes=(k, u8, shape), k_scales=(ks, f32, rows), v_codes=(v, u8, values),
+                v_scales=(vs, f32, rows))
+    return (k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr()), pages, page, heads, 2 * half, index
 
 
 def kv4_append(cache, k, v, slots, *, positions=None, inv_freq=None, interleaved: bool = False,
@@ -695,32 +738,34 @@ def kv4_append(cache, k, v, slots, *, positions=None, inv_freq=None, interleaved
     so are the queries q [T, Hq, D], which are returned (in q_out where it is given; None
     without q)."""
     import torch
-    ptrs, pages, page, heads, D, dev = _kv4(cache)
-    ldk = _rows3(k, "k", None, None, dev)
-    T, dtype = k.shape[0], k.dtype
-    if tuple(k.shape[1:]) != (heads, D):
-        raise ValueError(f"k must be [T, {heads}, {D}], got {tuple(k.shape)}")
+    ptrs, pages, page, heads, D, index = _kv4(cache)
+    shape = _three(k, "k")
+    T, dtype = shape[0], k.dtype
+    if shape != (T, heads, D):
+        raise ValueError(f"k must be [T, {heads}, {D}], got {tuple(shape)}")
     code = _type_code(k, "k", _HALVES)
-    ldv = _rows3(v, "v", dtype, (T, heads, D), dev)
-    _need(slots, "slots", torch.int64, (T,), dev)
+    ldk = _rows3(k, "k", dtype, shape, index)
+    ldv = _rows3(v, "v", dtype, shape, index)
+    if not _is(slots, torch.int64, (T,), index):
+        _refuse(index, slots=(slots, torch.int64, (T,)))
     pos = freq = q_ptr = out_ptr = None
     R = Hq = ldq = 0
     if positions is not None or inv_freq is not None:
-        pos, freq, R = _rotation(positions, inv_freq, T, dev)
+        pos, freq, R = _rotation(positions, inv_freq, T, index)
     if q is not None:
-        if q.dim() != 3 or pos is None:
-            raise ValueError("q must be [T, Hq, D], and is turned: it needs positions and inv_freq")
-        Hq = q.shape[1]
-        ldq = _rows3(q, "q", dtype, (T, Hq, D), dev)
+        if pos is None:
+            raise ValueError("q is turned: it needs positions and inv_freq")
+        Hq = _three(q, "q")[1]
+        ldq = _rows3(q, "q", dtype, (T, Hq, D), index)
         if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=dtype, device=dev)
-        else:
-            _need(q_out, "q_out", dtype, (T, Hq, D), dev)
+            q_out = q.new_empty((T, Hq, D))
+        elif not _is(q_out, dtype, (T, Hq, D), index):
+            _refuse(index, q_out=(q_out, dtype, (T, Hq, D)))
         q_ptr, out_ptr = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _call("apex4_kv4_append", dev, q_ptr, k.data_ptr(), v.data_ptr(), code, T, Hq, heads, D, ldq, ldk, ldv, pos, freq,
-          R, int(bool(interleaved)), rope_scale, slots.data_ptr(), pages, page, *ptrs, out_ptr)
+    _run("apex4_kv4_append", index, q_ptr, k.data_ptr(), v.data_ptr(), code, T, Hq, heads, D, ldq, ldk, ldv, pos, freq,
+         R, 1 if interleaved else 0, rope_scale, slots.data_ptr(), pages, page, *ptrs, out_ptr)
     return q_out
 
 
@@ -730,20 +775,21 @@ def kv4_read(cache, slots, dtype=None, out=None):
     write."""
     import torch
     dtype = torch.float16 if dtype is None else dtype
-    ptrs, pages, page, heads, D, dev = _kv4(cache)
-    _need_gpu(slots, "slots", torch.int64, None, dev)
-    if slots.dim() != 1:
-        raise ValueError(f"slots must be [T], got {tuple(slots.shape)}")
-    T = slots.shape[0]
+    ptrs, pages, page, heads, D, index = _kv4(cache)
+    T = slots.numel()
+    if not _is(slots, torch.int64, (T,), index):
+        _refuse(index, slots=(slots, torch.int64, (T,)))
+    shape = (T, heads, D)
     if out is None:
-        k = torch.empty((T, heads, D), dtype=dtype, device=dev)
-        v = torch.empty((T, heads, D), dtype=dtype, device=dev)
+        device = slots.device
+        k = torch.empty(shape, dtype=dtype, device=device)
+        v = torch.empty(shape, dtype=dtype, device=device)
     else:
         k, v = out
-        _need(k, "k", dtype, (T, heads, D), dev)
-        _need(v, "v", dtype, (T, heads, D), dev)
-    _call("apex4_kv4_read", dev, *ptrs, pages, page, heads, D, slots.data_ptr(), T, _type_code(k, "k"), k.data_ptr(),
-          v.data_ptr())
+        if not (_is(k, dtype, shape, index) and _is(v, dtype, shape, index)):
+            _refuse(index, k=(k, dtype, shape), v=(v, dtype, shape))
+    _run("apex4_kv4_read", index, *ptrs, pages, page, heads, D, slots.data_ptr(), T, _type_code(k, "k"), k.data_ptr(),
+         v.data_ptr())
     return k, v
 
 
@@ -764,42 +810,46 @@ def kv4_attention(q, cache, table, kv_lens, cu_q=None, *, scale: float | None = 
     table can hold).  Returns o [T, Hq, D] (rows that no sequence owns are not written), or
     (o, lse [T, Hq] float32) with want_lse."""
     import torch
-    ptrs, pages, page, heads, D, dev = _kv4(cache)
-    ldq = _rows3(q, "q", None, None, dev)
-    T, Hq = q.shape[:2]
-    if q.shape[2] != D:
-        raise ValueError(f"q must be [T, Hq, {D}], got {tuple(q.shape)}")
-    code = _type_code(q, "q", _HALVES)
+    ptrs, pages, page, heads, D, index = _kv4(cache)
+    shape = _three(q, "q")
+    T, Hq = shape[:2]
+    if shape[2] != D:
+        raise ValueError(f"q must be [T, Hq, {D}], got {tuple(shape)}")
+    code, dtype = _type_code(q, "q", _HALVES), q.dtype
+    ldq = _rows3(q, "q", dtype, shape, index)
     if table.dim() != 2:
         raise ValueError(f"table must be [B, cols], got {tuple(table.shape)}")
     B, cols = table.shape
-    _need(table, "table", torch.int32, (B, cols), dev)
-    _need(kv_lens, "kv_lens", torch.int32, (B,), dev)
-    if cu_q is not None:
-        _need(cu_q, "cu_q", torch.int32, (B + 1,), dev)
+    i32 = torch.int32
+    if not (_is(table, i32, (B, cols), index) and _is(kv_lens, i32, (B,), index)
+            and (cu_q is None or _is(cu_q, i32, (B + 1,), index))):
+        _refuse(index, table=(table, i32, (B, cols)), kv_lens=(kv_lens, i32, (B,)),
+                cu_q=(kv_lens if cu_q is None else cu_q, i32, (B + (cu_q is not None),)))
     # caller buffers are checked before anything is allocated
-    if out is not None:
-        _need(out, "out", q.dtype, (T, Hq, D), dev)
-    if lse is not None:
-        _need(lse, "lse", torch.float32, (T, Hq), dev)
-    if workspace is not None:
-        _need_gpu(workspace, "workspace", torch.uint8, None, dev)
+    if out is not None and not _is(out, dtype, shape, index):
+        _refuse(index, out=(out, dtype, shape))
+    if lse is not None and not _is(lse, torch.float32, (T, Hq), index):
+        _refuse(index, lse=(lse, torch.float32, (T, Hq)))
+    if workspace is not None and not _is(workspace, torch.uint8, workspace.shape, index):
+        _refuse(index, workspace=(workspace, torch.uint8, None))
     if max_q is None:
         max_q = 1 if cu_q is None else max(1, -(-T // max(B, 1)))
     if max_kv is None:
         max_kv = max(1, cols * page)
-    if max(max_q, max_kv, window) >> 31 or min(max_q, max_kv, window) < 0:
+    if (max_q | max_kv | window) >> 31:
         raise ValueError(f"max_q, max_kv and window must fit 31 bits, got {max_q, max_kv, window}")
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=dev)
+        out = q.new_empty(shape)
     if want_lse and lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
     if workspace is None:
-        need = _size("apex4_kv4_attention_workspace_size", dev, T, B, Hq, heads, D, max_q, max_kv)
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    _call("apex4_kv4_attention", dev, q.data_ptr(), code, T, B, Hq, heads, D, ldq, _ptr(cu_q), kv_lens.data_ptr(),
-          table.data_ptr(), cols, *ptrs, pages, page, D ** -0.5 if scale is None else scale, int(bool(causal)), window,
-          max_q, max_kv, out.data_ptr(), _ptr(lse), _ptr(workspace), 0 if workspace is None else workspace.numel())
+        need = _size("apex4_kv4_attention_workspace_size", q.device, T, B, Hq, heads, D, max_q, max_kv)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    _run("apex4_kv4_attention", index, q.data_ptr(), code, T, B, Hq, heads, D, ldq,
+         None if cu_q is None else cu_q.data_ptr(), kv_lens.data_ptr(), table.data_ptr(), cols, *ptrs, pages, page,
+         D ** -0.5 if scale is None else scale, 1 if causal else 0, window, max_q, max_kv, out.data_ptr(),
+         None if lse is None else lse.data_ptr(), None if workspace is None else workspace.data_ptr(),
+         0 if workspace is None else workspace.numel())
     return (out, lse) if want_lse else out
 
 

@@ -164,7 +164,7 @@ apex4_status apex4_kv4_read(const void* k_codes, const float* k_scales, const vo
 {
     const apex4_status sizes = cache_sizes(pages, page, Hkv, D);
     if (sizes != APEX4_OK) return sizes;
-    if (T < 0 || T > kMaxTokens || T * Hkv * D >= (int64_t(1) << 36)) return APEX4_ERR_INVALID_ARG;
+    if (T < 0 || T > kMaxTokens || T * Hkv >= (int64_t(1) << 28)) return APEX4_ERR_INVALID_ARG;
     if (type != APEX4_F32 && !half_type(type)) return APEX4_ERR_UNSUPPORTED;
     if (T == 0) return APEX4_OK;
     apex4::Kv4ReadProblem p{};

@@ -145,35 +145,91 @@ __global__ __launch_bounds__(256) void append_kernel(Kv4AppendProblem p, int par
     }
 }
 
-// 16 dims of one key and value head a lane.
-template <int TYPE>
-__global__ __launch_bounds__(256) void read_kernel(Kv4ReadProblem p, int64_t n)
+// N / 2 dwords (one number of 4 bytes, or two of 2) at the places of a value
+// head's numbers r + 16 h, h < N: the 16 lanes of a head write 64 neighbouring
+// bytes at a time.
+template <int TYPE, int N>
+__device__ inline void store_values(void* base, int64_t at, int r, const float (&v)[N])
 {
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n) return;
-    const Kv4Cache& c = p.cache;
-    const int lanes = c.D / 16;
-    const int64_t row = i / lanes, t = row / c.Hkv;
-    const int j = (int)(i - row * lanes), g = (int)(row - t * c.Hkv);
-    const int64_t slot = p.slots[t], pg = slot >> c.shift;
-    const int off = (int)(slot & (c.page - 1));
-    float k[16] = {}, v[16] = {};
-    if (slot >= 0 && pg < c.pages) {
-        const int64_t page = pg * c.Hkv + g, at = page * c.page + off;
-        const float ks = c.k_scales[at], vs = c.v_scales[at];
-        const uint2 w = *reinterpret_cast<const uint2*>(c.k_codes + at * (c.D / 2) + 8 * j);
-        const uint8_t* in = c.v_codes + page * c.page * (c.D / 2) + value_byte(off, j / 2, c.D);
+    if (TYPE == 0) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            k[e] = (float)((int)((e < 8 ? w.x >> (4 * e) : w.y >> (4 * e - 32)) & 15) - 8) * ks;
-            v[e] = (float)((int)((in[e * (c.D / 8)] >> (4 * (j & 1))) & 15) - 8) * vs;
+        for (int h = 0; h < N; ++h) static_cast<float*>(base)[at + r + 16 * h] = v[h];
+    } else {
+        // lanes r and r + 1 exchange: the even one writes the pairs of even h, the odd one of odd h
+        uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(base) + at + (r & 1 ? 15 + r : r));
+#pragma unroll
+        for (int h = 0; h < N; h += 2) {
+            const uint32_t a = e4m3::to16<TYPE == 2>(v[h]), b = e4m3::to16<TYPE == 2>(v[h + 1]);
+            const uint32_t other = __builtin_amdgcn_update_dpp(0, r & 1 ? a : b, 0xB1, 0xF, 0xF, false);
+            out[8 * h] = r & 1 ? other | b << 16 : a | other << 16;
         }
     }
-    const int64_t y = row * c.D + 16 * j;
-    rotary::store8<TYPE>(p.k, y, k);
-    rotary::store8<TYPE>(p.k, y + 8, k + 8);
-    rotary::store8<TYPE>(p.v, y, v);
-    rotary::store8<TYPE>(p.v, y + 8, v + 8);
+}
+
+// 16 lanes a head: of its key D / 16 neighbours each, of its value the numbers r +
+// 16 h, whose bytes lie together in the cache (with those of three other tokens).
+template <int TYPE, int D>
+__global__ __launch_bounds__(256) void read_kernel(Kv4ReadProblem p, int64_t n)
+{
+    constexpr int N = D / 16;
+    const int64_t row = (int64_t)blockIdx.x * 16 + threadIdx.x / 16;
+    const int r = threadIdx.x % 16;
+    if (row >= n) return;
+    const Kv4Cache& c = p.cache;
+    const int64_t t = row / c.Hkv;
+    const int g = (int)(row - t * c.Hkv);
+    const int64_t slot = p.slots[t], pg = slot >> c.shift;
+    const int off = (int)(slot & (c.page - 1));
+    float k[N] = {}, v[N] = {};
+    if (slot >= 0 && pg < c.pages) {
+        const int64_t page = pg * c.Hkv + g, at = page * c.page + off;
+        const uint8_t* keys = c.k_codes + at * (D / 2) + r * (N / 2);
+        const uint32_t* values = reinterpret_cast<const uint32_t*>(c.v_codes + page * c.page * (D / 2) + (off >> 4) * 8 * D +
+                                                                   (((off >> 2) & 3) * 16 + r) * (D / 8));
+        uint32_t kw[(N + 7) / 8], vw[N / 2];
+        if (N == 4) {
+            kw[0] = *reinterpret_cast<const uint16_t*>(keys);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N / 8; ++i) kw[i] = reinterpret_cast<const uint32_t*>(keys)[i];
+        }
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) vw[i] = values[i];
+        const float ks = c.k_scales[at], vs = c.v_scales[at];
+#pragma unroll
+        for (int e = 0; e < N; ++e) k[e] = (float)((int)((kw[e / 8] >> (4 * (e % 8))) & 15) - 8) * ks;
+        // byte off % 4 of each word: the number of the even h in its low half, of the odd one in its high half
+        const int shift = 8 * (off & 3);
+#pragma unroll
+        for (int h = 0; h < N; ++h) v[h] = (float)((int)((vw[h / 2] >> (shift + 4 * (h & 1))) & 15) - 8) * vs;
+    }
+    const int64_t y = row * D;
+    if (N == 4) {
+        if (TYPE == 0) {
+            *reinterpret_cast<float4*>(static_cast<float*>(p.k) + y + N * r) = make_float4(k[0], k[1], k[2], k[3]);
+        } else {
+            const uint32_t a = e4m3::to16<TYPE == 2>(k[0]) | (uint32_t)e4m3::to16<TYPE == 2>(k[1]) << 16;
+            const uint32_t b = e4m3::to16<TYPE == 2>(k[2]) | (uint32_t)e4m3::to16<TYPE == 2>(k[3]) << 16;
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.k) + y + N * r) = make_uint2(a, b);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 8) rotary::store8<TYPE>(p.k, y + N * r + i, k + i);
+    }
+    store_values<TYPE, N>(p.v, y, r, v);
+}
+
+template <int TYPE>
+hipError_t read(const Kv4ReadProblem& p, hipStream_t stream)
+{
+    const int64_t n = p.T * p.cache.Hkv;
+    const unsigned blocks = (unsigned)((n + 15) / 16);
+    switch (p.cache.D) {
+    case 64: read_kernel<TYPE, 64><<<blocks, 256, 0, stream>>>(p, n); break;
+    case 128: read_kernel<TYPE, 128><<<blocks, 256, 0, stream>>>(p, n); break;
+    default: read_kernel<TYPE, 256><<<blocks, 256, 0, stream>>>(p, n); break;    // checked by the caller
+    }
+    return hipGetLastError();
 }
 
 template <bool BF16>
@@ -210,14 +266,11 @@ hipError_t launch_kv4_append(const Kv4AppendProblem& p, hipStream_t stream)
 
 hipError_t launch_kv4_read(const Kv4ReadProblem& p, hipStream_t stream)
 {
-    const int64_t n = p.T * p.cache.Hkv * (p.cache.D / 16);
-    const unsigned blocks = (unsigned)((n + 255) / 256);
     switch (p.type) {
-    case 0: read_kernel<0><<<blocks, 256, 0, stream>>>(p, n); break;
-    case 1: read_kernel<1><<<blocks, 256, 0, stream>>>(p, n); break;
-    default: read_kernel<2><<<blocks, 256, 0, stream>>>(p, n); break;
+    case 0: return read<0>(p, stream);
+    case 1: return read<1>(p, stream);
+    default: return read<2>(p, stream);
     }
-    return hipGetLastError();
 }
 
 }  // namespace apex4
