@@ -145,89 +145,119 @@ __global__ __launch_bounds__(256) void append_kernel(Kv4AppendProblem p, int par
     }
 }
 
-// N / 2 dwords (one number of 4 bytes, or two of 2) at the places of a value
-// head's numbers r + 16 h, h < N: the 16 lanes of a head write 64 neighbouring
-// bytes at a time.
+// Stores a value head whose lane r of 16 has the numbers r + 16 h, h < N: by way
+// of `lds` (the head's own, 16-byte aligned), so that a lane writes 16 neighbouring
+// bytes at a time (written where the lanes have them, 64 neighbouring bytes a
+// head and store, the call took half as long again).
 template <int TYPE, int N>
-__device__ inline void store_values(void* base, int64_t at, int r, const float (&v)[N])
+__device__ inline void store_values(void* base, int64_t at, int r, const float (&v)[N], uint32_t* lds)
 {
+    constexpr int WORDS = (TYPE == 0 ? 16 : 8) * N, EACH = WORDS / 16;      // of the head, of a lane
     if (TYPE == 0) {
 #pragma unroll
-        for (int h = 0; h < N; ++h) static_cast<float*>(base)[at + r + 16 * h] = v[h];
+        for (int h = 0; h < N; ++h) lds[r + 16 * h] = __builtin_bit_cast(uint32_t, v[h]);
     } else {
         // lanes r and r + 1 exchange: the even one writes the pairs of even h, the odd one of odd h
-        uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(base) + at + (r & 1 ? 15 + r : r));
 #pragma unroll
         for (int h = 0; h < N; h += 2) {
             const uint32_t a = e4m3::to16<TYPE == 2>(v[h]), b = e4m3::to16<TYPE == 2>(v[h + 1]);
             const uint32_t other = __builtin_amdgcn_update_dpp(0, r & 1 ? a : b, 0xB1, 0xF, 0xF, false);
-            out[8 * h] = r & 1 ? other | b << 16 : a | other << 16;
+            lds[8 * h + (r & 1 ? 7 + (r + 1) / 2 : r / 2)] = r & 1 ? other | b << 16 : a | other << 16;
         }
+    }
+    // (the 16 lanes are of one wave)
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    uint32_t* out = static_cast<uint32_t*>(base) + at / (TYPE == 0 ? 1 : 2) + r * EACH;
+    if (EACH == 2) {
+        *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(lds + r * EACH);
+    } else {
+#pragma unroll
+        for (int e = 0; e < EACH; e += 4)
+            *reinterpret_cast<uint4*>(out + e) = *reinterpret_cast<const uint4*>(lds + r * EACH + e);
     }
 }
 
 // 16 lanes a head: of its key D / 16 neighbours each, of its value the numbers r +
 // 16 h, whose bytes lie together in the cache (with those of three other tokens).
-template <int TYPE, int D>
-__global__ __launch_bounds__(256) void read_kernel(Kv4ReadProblem p, int64_t n)
+template <int TYPE, int D, int ROWS>
+__global__ __launch_bounds__(256) void read_kernel(Kv4ReadProblem p, int n)
 {
-    constexpr int N = D / 16;
-    const int64_t row = (int64_t)blockIdx.x * 16 + threadIdx.x / 16;
-    const int r = threadIdx.x % 16;
-    if (row >= n) return;
+    constexpr int N = D / 16, WORDS = TYPE == 0 ? D : D / 2;
+    __shared__ __attribute__((aligned(16))) uint32_t lds[16][ROWS][WORDS + 4];
+    const int first = blockIdx.x * 16 * ROWS + threadIdx.x / 16, r = threadIdx.x % 16;
     const Kv4Cache& c = p.cache;
-    const int64_t t = row / c.Hkv;
-    const int g = (int)(row - t * c.Hkv);
-    const int64_t slot = p.slots[t], pg = slot >> c.shift;
-    const int off = (int)(slot & (c.page - 1));
-    float k[N] = {}, v[N] = {};
-    if (slot >= 0 && pg < c.pages) {
-        const int64_t page = pg * c.Hkv + g, at = page * c.page + off;
+    int64_t slot[ROWS];
+    int g[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int row = min(first + 16 * i, n - 1), t = (unsigned)row / (unsigned)c.Hkv;
+        g[i] = row - t * c.Hkv;
+        slot[i] = p.slots[t];
+    }
+    uint32_t kw[ROWS][(N + 7) / 8], vw[ROWS][N / 2];
+    float ks[ROWS], vs[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        // (a slot that is none reads the cache's first token, and counts it as zeros)
+        const bool live = slot[i] >= 0 && (slot[i] >> c.shift) < c.pages;
+        const int64_t pg = live ? slot[i] >> c.shift : 0;
+        const int off = live ? (int)(slot[i] & (c.page - 1)) : 0;
+        const int64_t page = pg * c.Hkv + g[i], at = page * c.page + off;
         const uint8_t* keys = c.k_codes + at * (D / 2) + r * (N / 2);
         const uint32_t* values = reinterpret_cast<const uint32_t*>(c.v_codes + page * c.page * (D / 2) + (off >> 4) * 8 * D +
                                                                    (((off >> 2) & 3) * 16 + r) * (D / 8));
-        uint32_t kw[(N + 7) / 8], vw[N / 2];
         if (N == 4) {
-            kw[0] = *reinterpret_cast<const uint16_t*>(keys);
+            kw[i][0] = *reinterpret_cast<const uint16_t*>(keys);
         } else {
 #pragma unroll
-            for (int i = 0; i < N / 8; ++i) kw[i] = reinterpret_cast<const uint32_t*>(keys)[i];
+            for (int e = 0; e < N / 8; ++e) kw[i][e] = reinterpret_cast<const uint32_t*>(keys)[e];
         }
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) vw[i] = values[i];
-        const float ks = c.k_scales[at], vs = c.v_scales[at];
+        for (int e = 0; e < N / 2; ++e) vw[i][e] = values[e];
+        ks[i] = c.k_scales[at], vs[i] = c.v_scales[at];
+        if (!live) ks[i] = vs[i] = 0.0f;
+    }
 #pragma unroll
-        for (int e = 0; e < N; ++e) k[e] = (float)((int)((kw[e / 8] >> (4 * (e % 8))) & 15) - 8) * ks;
+    for (int i = 0; i < ROWS; ++i) {
+        const int row = first + 16 * i;
+        if (row >= n) break;
+        float k[N], v[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) k[e] = (float)((int)((kw[i][e / 8] >> (4 * (e % 8))) & 15) - 8) * ks[i];
         // byte off % 4 of each word: the number of the even h in its low half, of the odd one in its high half
-        const int shift = 8 * (off & 3);
+        const int shift = 8 * (int)(slot[i] & 3);
 #pragma unroll
-        for (int h = 0; h < N; ++h) v[h] = (float)((int)((vw[h / 2] >> (shift + 4 * (h & 1))) & 15) - 8) * vs;
-    }
-    const int64_t y = row * D;
-    if (N == 4) {
-        if (TYPE == 0) {
-            *reinterpret_cast<float4*>(static_cast<float*>(p.k) + y + N * r) = make_float4(k[0], k[1], k[2], k[3]);
+        for (int h = 0; h < N; ++h) v[h] = (float)((int)((vw[i][h / 2] >> (shift + 4 * (h & 1))) & 15) - 8) * vs[i];
+        const int64_t y = (int64_t)row * D;
+        if (N == 4) {
+            if (TYPE == 0) {
+                *reinterpret_cast<float4*>(static_cast<float*>(p.k) + y + N * r) = make_float4(k[0], k[1], k[2], k[3]);
+            } else {
+                const uint32_t a = e4m3::to16<TYPE == 2>(k[0]) | (uint32_t)e4m3::to16<TYPE == 2>(k[1]) << 16;
+                const uint32_t b = e4m3::to16<TYPE == 2>(k[2]) | (uint32_t)e4m3::to16<TYPE == 2>(k[3]) << 16;
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.k) + y + N * r) = make_uint2(a, b);
+            }
         } else {
-            const uint32_t a = e4m3::to16<TYPE == 2>(k[0]) | (uint32_t)e4m3::to16<TYPE == 2>(k[1]) << 16;
-            const uint32_t b = e4m3::to16<TYPE == 2>(k[2]) | (uint32_t)e4m3::to16<TYPE == 2>(k[3]) << 16;
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.k) + y + N * r) = make_uint2(a, b);
-        }
-    } else {
 #pragma unroll
-        for (int i = 0; i < N; i += 8) rotary::store8<TYPE>(p.k, y + N * r + i, k + i);
+            for (int e = 0; e < N; e += 8) rotary::store8<TYPE>(p.k, y + N * r + e, k + e);
+        }
+        store_values<TYPE, N>(p.v, y, r, v, lds[threadIdx.x / 16][i]);
     }
-    store_values<TYPE, N>(p.v, y, r, v);
 }
 
 template <int TYPE>
 hipError_t read(const Kv4ReadProblem& p, hipStream_t stream)
 {
-    const int64_t n = p.T * p.cache.Hkv;
-    const unsigned blocks = (unsigned)((n + 15) / 16);
+    const int n = (int)(p.T * p.cache.Hkv);
+    // several heads' loads in flight where there are enough of them
+    constexpr int ROWS = 4;
+    const unsigned blocks = (unsigned)((n + 16 * ROWS - 1) / (16 * ROWS));
     switch (p.cache.D) {
-    case 64: read_kernel<TYPE, 64><<<blocks, 256, 0, stream>>>(p, n); break;
-    case 128: read_kernel<TYPE, 128><<<blocks, 256, 0, stream>>>(p, n); break;
-    default: read_kernel<TYPE, 256><<<blocks, 256, 0, stream>>>(p, n); break;    // checked by the caller
+    case 64: read_kernel<TYPE, 64, ROWS><<<blocks, 256, 0, stream>>>(p, n); break;
+    case 128: read_kernel<TYPE, 128, ROWS><<<blocks, 256, 0, stream>>>(p, n); break;
+    default: read_kernel<TYPE, 256, ROWS><<<blocks, 256, 0, stream>>>(p, n); break;    // checked by the caller
     }
     return hipGetLastError();
 }
