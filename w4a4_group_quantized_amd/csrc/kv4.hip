@@ -252,7 +252,7 @@ hipError_t read(const Kv4ReadProblem& p, hipStream_t stream)
 {
     const int n = (int)(p.T * p.cache.Hkv);
     // several heads' loads in flight where there are enough of them
-    constexpr int ROWS = 4;
+    constexpr int ROWS = 2;
     const unsigned blocks = (unsigned)((n + 16 * ROWS - 1) / (16 * ROWS));
     switch (p.cache.D) {
     case 64: read_kernel<TYPE, 64, ROWS><<<blocks, 256, 0, stream>>>(p, n); break;
