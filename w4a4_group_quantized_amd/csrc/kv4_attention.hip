@@ -471,10 +471,11 @@ __device__ inline void attend(const Kv4AttentionProblem& p, const Sequence& s, i
         const bool edge = t0 + 64 > hi_min || t0 < lo_max || !__all(a.valid);
         wave_sync();
         float4v x[RT][4];
+        // (four accumulators between two instructions on the same one)
 #pragma unroll
-        for (int sub = 0; sub < 4; ++sub) {
+        for (int f = 0; f < D / 32; ++f) {
 #pragma unroll
-            for (int f = 0; f < D / 32; ++f) {
+            for (int sub = 0; sub < 4; ++sub) {
                 const half8 key = key_operand(a.k.w[sub][f]);
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) x[rt][sub] = mfma(key, r.q[rt][f], f == 0 ? r.bias[rt] : x[rt][sub]);
@@ -600,10 +601,11 @@ __device__ inline void attend_shared(const Kv4AttentionProblem& p, const Sequenc
         look(t0 + 192);
         const Tile<D>& tile = tiles[at];
         float4v x[RT][4];
+        // (four accumulators between two instructions on the same one)
 #pragma unroll
-        for (int sub = 0; sub < 4; ++sub) {
+        for (int f = 0; f < D / 32; ++f) {
 #pragma unroll
-            for (int f = 0; f < D / 32; ++f) {
+            for (int sub = 0; sub < 4; ++sub) {
                 const half8 a = __builtin_bit_cast(half8, tile.k[sub][f][lane]);
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) x[rt][sub] = mfma(a, r.q[rt][f], f == 0 ? r.bias[rt] : x[rt][sub]);
@@ -969,7 +971,7 @@ Cut cut(const Kv4AttentionProblem& p)
     Cut c{};
     c.rt = p.cache.D == 256 || all <= 16 ? 1 : 2;
     const int64_t wide = (all + 16 * c.rt * kWaves - 1) / (16 * c.rt * kWaves);
-    c.rows = all > 16 * c.rt && pairs * wide >= cus;
+    c.rows = all > 16 * c.rt && 2 * pairs * wide >= 3 * cus;
     const int64_t narrow = (all + 16 * c.rt - 1) / (16 * c.rt);
     // (workgroups stride over row tiles beyond the grid's limit of 2^32 threads)
     c.tiles = (int)std::max<int64_t>(1, std::min<int64_t>(c.rows ? wide : narrow, kMaxBlocks / pairs));
