@@ -566,7 +566,7 @@ apex4_status apex4_kv4_read(const void* k_codes, const float* k_scales, const vo
  *   workspace: at least apex4_kv4_attention_workspace_size() bytes (NULL allowed
  *   when that is 0; 0 for invalid or empty sizes), 16-byte aligned, caller-owned,
  *   overwritten; calls that share one race.
- *   0 <= B <= 65536, 0 <= T < 2^24 (either 0: no-op), T * Hq < 2^31, B * Hkv < 2^23, Hkv
+ *   0 <= B <= 65536, 0 <= T < 2^24 (either 0: no-op), T * Hq < 2^30, B * Hkv < 2^23, Hkv
  *   divides Hq, Hq <= 1024, D 64, 128 or 256, cols * page <= 2^30, max_q and max_kv >= 1, scale finite.
  * No atomics: the results do not depend on timing.  Asynchronous on `stream`.
  */

@@ -283,3 +283,63 @@ def test_refusals(dev):
         with pytest.raises(apex4.Apex4Error):
             apex4.kv4_attention(**{**base, **bad})
     assert apex4.kv4_attention(q[:0], cache, table[:0], lens[:0]).shape == (0, 4, 64)
+
+
+def test_more_sequences_than_a_workgroup_sorts(dev):
+    """300 sequences of one key head: shared out by a sum over all lengths; and 600: whole, unsorted."""
+    for B, longest in ((300, 2000), (600, 1700)):
+        rng = np.random.default_rng(B)
+        olds = [int(x) for x in rng.integers(0, 40, B)]
+        olds[B - 2], olds[17], olds[18] = longest, 0, 700
+        host, table, _ = make([1] * B, olds, 1, 64, 64, B)
+        q = queries(B, 2, 64, "float16", B)
+        check(dev, "float16", q, host, table, olds, None, max_kv=longest)
+    news = [int(x) for x in np.random.default_rng(5).integers(0, 4, 300)]
+    news[7] = 40
+    olds = [n + 3 * i % 50 for i, n in enumerate(news)]
+    olds[7], olds[299] = 1600, 1400
+    host, table, cu = make(news, olds, 1, 64, 64, 7)
+    check(dev, "bfloat16", queries(sum(news), 3, 64, "bfloat16"), host, table, olds, cu, max_q=2, max_kv=1600)
+
+
+def test_very_many_query_heads_and_lengths_beyond_the_table(dev):
+    host, table, _ = make([1, 1], [300, 77], 1, 64, 16, 3)
+    check(dev, "float16", queries(2, 512, 64, "float16"), host, table, [300, 77], None)
+    # kv_lens beyond what the table holds count as that
+    table = table[:, :5].copy()
+    q = queries(2, 4, 64, "float16")
+    check(dev, "float16", q, host, table, [300, 77], None)
+    check(dev, "float16", q, host, table, [2 ** 31 - 1, 77], None)
+
+
+def test_two_streams_at_once(dev):
+    """Calls that overlap take workspaces of their own."""
+    host, table, _ = make([1], [20000], 2, 128, 64, 21)
+    to = lambda a: torch.from_numpy(np.asarray(a)).to(dev)  # noqa: E731
+    cache, tab, lens = tuple(to(a) for a in host.arrays()), to(table), to(np.array([20000], np.int32))
+    qs = [queries(1, 8, 128, "float16", i).to(dev) for i in range(2)]
+    want = [apex4.kv4_attention(q, cache, tab, lens) for q in qs]
+    streams = [torch.cuda.Stream() for _ in qs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(apex4.kv4_attention(qs[i], cache, tab, lens))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i]) for o in got[i])
+
+
+def test_a_workspace_of_the_callers(dev):
+    host, table, _ = make([1], [5000], 1, 64, 64, 22)
+    to = lambda a: torch.from_numpy(np.asarray(a)).to(dev)  # noqa: E731
+    cache, tab, lens = tuple(to(a) for a in host.arrays()), to(table), to(np.array([5000], np.int32))
+    q = queries(1, 4, 64, "float16").to(dev)
+    need = apex4.kv4_attention_workspace_size(1, 1, 4, 1, 64, 1, tab.shape[1] * 64)
+    assert need > 0
+    ws = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device=dev)          # (NaN wherever it is read unwritten)
+    got = apex4.kv4_attention(q, cache, tab, lens, workspace=ws[:need])
+    assert torch.equal(got, apex4.kv4_attention(q, cache, tab, lens)) and (ws[need:] == 0xFF).all()
+    with pytest.raises(apex4.Apex4Error):
+        apex4.kv4_attention(q, cache, tab, lens, workspace=ws[:need - 1])

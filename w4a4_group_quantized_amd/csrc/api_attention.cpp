@@ -70,7 +70,7 @@ bool cache_aligned(const apex4::Kv4Cache& c)
 apex4_status attention_sizes(int64_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t max_q, int32_t max_kv)
 {
     if (!heads_ok(T, Hq) || B < 0 || B > 65536 || Hkv < 1 || Hq % Hkv != 0 || D < 1) return APEX4_ERR_INVALID_ARG;
-    if (T * Hq >= (int64_t(1) << 31) || (int64_t)B * Hkv >= (int64_t(1) << 23) || max_q < 1 || max_kv < 1)
+    if (T * Hq >= (int64_t(1) << 30) || (int64_t)B * Hkv >= (int64_t(1) << 23) || max_q < 1 || max_kv < 1)
         return APEX4_ERR_INVALID_ARG;
     return head_dim_ok(D) ? APEX4_OK : APEX4_ERR_UNSUPPORTED;
 }
