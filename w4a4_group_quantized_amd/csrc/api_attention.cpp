@@ -82,6 +82,7 @@ apex4::Kv4AttentionProblem attention_problem(int64_t T, int32_t B, int32_t Hq, i
     p.T = T;
     p.B = B;
     p.Hq = Hq;
+    p.share = Hq / Hkv;
     p.cache.Hkv = Hkv;
     p.cache.D = D;
     // (no fewer than the mean, no more than there are)

@@ -68,6 +68,7 @@ struct Kv4AttentionProblem {
     bool bf16;
     int64_t T;
     int32_t B, Hq;
+    int32_t share;              // query heads of a key head
     int64_t ldq;
     const int32_t* cu_q;        // null: one query a sequence (T == B)
     const int32_t* kv_lens;

@@ -155,7 +155,7 @@ template <int D, int RT>
 __device__ inline void fetch_rows(const Kv4AttentionProblem& p, const Sequence& s, int g, int row0, RawRows<D, RT>& raw)
 {
     const int lane = threadIdx.x & 63, quad = lane >> 4;
-    const int share = p.Hq / p.cache.Hkv;
+    const int share = p.share;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         const int row = row0 + 16 * rt + (lane & 15);
@@ -175,7 +175,7 @@ __device__ inline void make_rows(const Kv4AttentionProblem& p, const Sequence& s
                                  Rows<D, RT>& r)
 {
     const int lane = threadIdx.x & 63;
-    const int share = p.Hq / p.cache.Hkv;
+    const int share = p.share;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         const int row = row0 + 16 * rt + (lane & 15);
@@ -668,7 +668,7 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(Kv4AttentionProblem p, Pla
     x /= p.cache.Hkv;
     const int first = x % plan.tiles;
     const Sequence s = sequence(p, x / plan.tiles);
-    const int share = p.Hq / p.cache.Hkv, all = s.n * share, tiles = (all + 16 * RT * kWaves - 1) / (16 * RT * kWaves);
+    const int share = p.share, all = s.n * share, tiles = (all + 16 * RT * kWaves - 1) / (16 * RT * kWaves);
     for (int k = first; k < tiles; k += plan.tiles) {
         // (the last rows see the most tokens: first)
         const int top = (tiles - 1 - k) * kWaves * 16 * RT, row0 = top + wave * 16 * RT;
@@ -715,7 +715,7 @@ __device__ inline void few_rows(const Kv4AttentionProblem& p, const Plan& plan, 
 {
     constexpr int R = 16 * RT;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int share = p.Hq / p.cache.Hkv, all = s.n * share;
+    const int share = p.share, all = s.n * share;
     const int i0 = row0 / share, i1 = min(row0 + R - 1, all - 1) / share;
     // (tokens that no row of the tile sees are passed over)
     const int from = max(base + u0 * kUnit, seen_lo(p, s, i0) & ~(kUnit - 1)) + 64 * wave;
@@ -774,7 +774,7 @@ __device__ inline Extent extent(const Kv4AttentionProblem& p, const Sequence& s)
 {
     const int base = seen_lo(p, s, 0) & ~(kUnit - 1);
     // (at least one: rows that see nothing are written too)
-    return {base, (s.n * (p.Hq / p.cache.Hkv) + R - 1) / R, max(1, (s.kv - base + kUnit - 1) / kUnit)};
+    return {base, (s.n * p.share + R - 1) / R, max(1, (s.kv - base + kUnit - 1) / kUnit)};
 }
 
 // sum over the workgroup; `lds`: a number a wave
@@ -883,7 +883,7 @@ __global__ __launch_bounds__(256, 2) void few_kernel(Kv4AttentionProblem p, Plan
         int slot = -1;
         if (n < e.units) {
             slot = 2 * blockIdx.x + (u0 == 0);
-            const int rows = min(R, s.n * (p.Hq / Hkv) - k * R);
+            const int rows = min(R, s.n * p.share - k * R);
             const int64_t at = u - u0;                     // its first unit
             if (threadIdx.x == 0) plan.splits[slot] = {s.q0, k * R, rows, g, (int)(at / each), (int)((at + e.units - 1) / each)};
         }
@@ -902,46 +902,52 @@ __global__ __launch_bounds__(64 * WAVES) void join_kernel(Kv4AttentionProblem p,
     constexpr int EACH = D / 64, R = 16 * RT;
     static_assert(PARTS == 1 || PARTS == WAVES, "");
     __shared__ float sums[PARTS][D];
-    __shared__ float ls[PARTS];
+    __shared__ float2 tops[PARTS];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int part = PARTS == 1 ? 0 : wave;
-    const int share = p.Hq / p.cache.Hkv;
+    const int share = p.share;
+    const Split records[2] = {plan.splits[2 * blockIdx.x], plan.splits[2 * blockIdx.x + 1]};
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-        const Split s = plan.splits[2 * blockIdx.x + which];
+        const Split& s = records[which];
         if (s.rows == 0) continue;
         const int n = s.last - s.first + 1;
         // (the first workgroup's sums are its second ones)
         const auto slot = [&](int i) { return (int64_t)(2 * (s.first + i) + (i == 0)) * R; };
         for (int row = (int)blockIdx.x - s.first + (PARTS == 1 ? wave * n : 0); row < s.rows; row += n * (WAVES / PARTS)) {
+            // one pass over the wave's parts with a maximum of its own
             float m = -INFINITY, l = 0.0f, o[EACH] = {};
-            for (int i = lane; i < n; i += 64) m = fmaxf(m, plan.part_ml[slot(i) + row].x);
-#pragma unroll
-            for (int off = 32; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor(m, off));
 #pragma unroll 4
             for (int i = part; i < n; i += PARTS) {
                 const float2 ml = plan.part_ml[slot(i) + row];
-                const float by = ml.x == m ? 1.0f : __builtin_amdgcn_exp2f(ml.x - m);
                 const float* from = plan.part_o + (slot(i) + row) * D + lane * EACH;
-                l = fmaf(ml.y, by, l);
+                const float top = fmaxf(m, ml.x);
+                const float old = m == top ? 1.0f : __builtin_amdgcn_exp2f(m - top);
+                const float by = ml.x == top ? 1.0f : __builtin_amdgcn_exp2f(ml.x - top);
+                l = l * old + ml.y * by;
 #pragma unroll
-                for (int e = 0; e < EACH; ++e) o[e] = fmaf(from[e], by, o[e]);
+                for (int e = 0; e < EACH; ++e) o[e] = o[e] * old + from[e] * by;
+                m = top;
             }
             if (PARTS > 1) {
                 __syncthreads();                           // (the row before is out of LDS)
 #pragma unroll
                 for (int e = 0; e < EACH; ++e) sums[part][lane * EACH + e] = o[e];
-                if (lane == 0) ls[part] = l;
+                if (lane == 0) tops[part] = make_float2(m, l);
                 __syncthreads();
                 if (part != 0) continue;
+#pragma unroll
+                for (int v = 0; v < PARTS; ++v) m = fmaxf(m, tops[v].x);
                 l = 0.0f;
 #pragma unroll
                 for (int e = 0; e < EACH; ++e) o[e] = 0.0f;
 #pragma unroll
                 for (int v = 0; v < PARTS; ++v) {
-                    l += ls[v];
+                    const float2 ml = tops[v];
+                    const float by = ml.x == m ? 1.0f : __builtin_amdgcn_exp2f(ml.x - m);
+                    l += ml.y * by;
 #pragma unroll
-                    for (int e = 0; e < EACH; ++e) o[e] += sums[v][lane * EACH + e];
+                    for (int e = 0; e < EACH; ++e) o[e] += sums[v][lane * EACH + e] * by;
                 }
             }
             const float by = l == 0.0f ? 0.0f : 1.0f / l;
@@ -966,7 +972,7 @@ struct Cut {
 
 Cut cut(const Kv4AttentionProblem& p)
 {
-    const int64_t all = (int64_t)p.max_q * (p.Hq / p.cache.Hkv), pairs = (int64_t)p.B * p.cache.Hkv;
+    const int64_t all = (int64_t)p.max_q * p.share, pairs = (int64_t)p.B * p.cache.Hkv;
     const int cus = compute_units() > 0 ? compute_units() : 256;
     Cut c{};
     c.rt = p.cache.D == 256 || all <= 16 ? 1 : 2;
