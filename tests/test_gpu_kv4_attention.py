@@ -221,6 +221,37 @@ def test_rows_behind_the_last_sequence_and_parts_of_a_projection(dev):
     assert torch.isfinite(out.float()).all()
 
 
+def uneven(kind):
+    """(new tokens, cached tokens, query heads, key heads, window): prompts among sequences of few tokens."""
+    rng = np.random.default_rng(len(kind))
+    news = rng.integers(0, 3, 70)
+    olds = news + rng.integers(0, 200, 70)
+    if kind == "many rows":
+        news[[3, 64]] = 900, 811
+        olds[[3, 64]] = 900, 1000
+        return news, olds, 16, 4, 0
+    if kind == "many sequences":
+        news = (np.arange(4500) % 3 == 1).astype(int)
+        olds = news + np.arange(4500) % 2
+        news[[0, 4095, 4499]] = 300, 129, 140
+        olds[[0, 4095, 4499]] = 300, 200, 140
+        return news, olds, 1, 1, 0
+    news[[0, 69]] = 60, 33
+    olds[[0, 69]] = {"few rows": (70, 1200), "shared": (2500, 100), "window": (2500, 2100)}[kind]
+    return news, olds, 16, 4, 1100 if kind == "window" else 0
+
+
+@pytest.mark.parametrize("kind", ["many rows", "few rows", "shared", "window", "many sequences"])
+def test_prompts_among_sequences_of_few_tokens(dev, kind):
+    """Row tiles are numbered over all sequences; rows before the first and behind the last have none."""
+    news, olds, Hq, Hkv, window = uneven(kind)
+    host, table, cu = make(list(news), list(olds), Hkv, 64, 16, 17)
+    q = queries(int(cu[-1]) + 50, Hq, 64, "float16", 17)
+    check(dev, "float16", q, host, table, olds, cu + 37, max_q=int(max(news)), max_kv=int(max(olds)), window=window)
+    if kind != "many rows":                                      # (a guess too low costs time only)
+        check(dev, "float16", q, host, table, olds, cu + 37, max_q=1, max_kv=1, window=window)
+
+
 def test_same_bits_every_time_and_alone(dev):
     """The same call twice gives the same bits; on another stream too; a sequence's rows do not
     depend on the other queries, or on their pages' contents, in a call of the same lengths."""

@@ -30,6 +30,17 @@
 // puts a lane's 4 tokens of all its numbers side by side.  S leaves the matrix
 // unit with 4 tokens of one row in a lane, which is how the second product wants
 // w: nothing goes through LDS but a token's three factors.
+//
+// Few rows (decoding): bound by the cache's bytes.  64 sequences of 4096 tokens, 8
+// key heads of 128, 64 query heads: 50 us (5.7 TB/s of a read's 5.7-6.2); lengths
+// up to 8192 at random 70 us (4.7 TB/s: the longest end last); one of 131071 tokens
+// 29 us and 5 us for the join (5.0 TB/s).  A wave alone takes 1.3 us for 64 tokens,
+// 420 vector instructions of which unpacking is 224.
+// Many rows (prompts): 4096 tokens, 64 and 8 heads, 303 us (909 TFLOP/s of 275 GFLOP
+// seen; the library's plain product of 8192^3 reaches 1164).  The vector ALU is
+// busy 59% of the time and the matrix unit 39%, and on a SIMD the two overlap little
+// (64 matrix instructions of one wave beside 256 fmas of another take 1.4 times as
+// long as either alone): the sum is the bound.
 #include <algorithm>
 
 #include "attention.h"
@@ -51,7 +62,8 @@ constexpr float kLazy = 8.0f;
 
 // How a call is cut (launch_kv4_attention).
 struct Plan {
-    int tiles;          // row tiles of a sequence and key head that the grid holds (workgroups stride over more)
+    int tiles;          // row tiles of a sequence and key head that the grid holds (workgroups stride over more);
+                        // 0: as many as each sequence has (see place)
     bool share;         // the workgroups share all units of the call evenly and leave the sums of the row tiles
                         // that they have parts of; else each takes whole row tiles
     bool sorted;        // (whole tiles) the longest of at most kSorted sequences first
@@ -527,7 +539,7 @@ struct Tile {
 };
 
 // Asks the scheduler to keep the reads of N operands AHEAD before the RT matrix
-// instructions that take each.
+// instructions that take each (it kept two: 326 us for the prompt against 303).
 template <int N, int RT>
 __device__ inline void reads_ahead()
 {
@@ -657,19 +669,44 @@ __device__ inline void store4(void* out, int64_t at, float4v v)
 
 __device__ inline float log_sum(float m, float l) { return l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.693147181f; }
 
+// The row tile of workgroup x, of R rows: key heads beside each other, then the
+// tiles of a sequence, then the sequences.  Uneven sequences (a prompt beside
+// decoding ones) have a tile k of sequence b at floor(its first row / R) + b + k:
+// no two at one place, and at most B places empty.
+struct Place {
+    int b, g, k;        // k outside the sequence's tiles: an empty place
+};
+template <int R>
+__device__ inline Place place(const Kv4AttentionProblem& p, int tiles, int x)
+{
+    const int g = x % p.cache.Hkv;
+    x /= p.cache.Hkv;
+    if (tiles) return {x / tiles, g, x % tiles};
+    const auto first = [&](int b) { return (int)(min(sequence(p, b).q0, p.T) * p.share / R) + b; };
+    int b = 0;
+    for (int n = p.B; n > 1;) {                            // the last of n that begins at or before x, 64 at a time
+        const int step = (n + 63) / 64, at = (threadIdx.x & 63) * step;
+        const int upto = max(1, __popcll(__ballot(at < n && first(min(b + at, p.B - 1)) <= x))) - 1;
+        b += upto * step;
+        n = min(step, n - upto * step);
+    }
+    b = __builtin_amdgcn_readfirstlane(b);
+    return {b, g, x - first(b)};
+}
+
 // Many rows: every wave has rows of its own and walks all the tokens they see.
+// (Unpacking for itself, without LDS and barriers, it takes 355 us for the prompt
+// against 322 on one box; 64 rows a wave do not fit the registers: 650 us.)
 template <bool BF16, int D, int RT>
 __global__ __launch_bounds__(256, 2) void rows_kernel(Kv4AttentionProblem p, Plan plan)
 {
     __shared__ __attribute__((aligned(16))) Tile<D> buffers[2];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    int x = blockIdx.x;
-    const int g = x % p.cache.Hkv;
-    x /= p.cache.Hkv;
-    const int first = x % plan.tiles;
-    const Sequence s = sequence(p, x / plan.tiles);
-    const int share = p.share, all = s.n * share, tiles = (all + 16 * RT * kWaves - 1) / (16 * RT * kWaves);
-    for (int k = first; k < tiles; k += plan.tiles) {
+    const Place own = place<16 * RT * kWaves>(p, plan.tiles, blockIdx.x);
+    const Sequence s = sequence(p, own.b);
+    const int g = own.g, share = p.share, all = s.n * share, tiles = (all + 16 * RT * kWaves - 1) / (16 * RT * kWaves);
+    if (own.k < 0) return;
+    for (int k = own.k; k < tiles; k += plan.tiles ? plan.tiles : tiles) {
         // (the last rows see the most tokens: first)
         const int top = (tiles - 1 - k) * kWaves * 16 * RT, row0 = top + wave * 16 * RT;
         Rows<D, RT> r;
@@ -798,13 +835,9 @@ __global__ __launch_bounds__(256, 2) void few_kernel(Kv4AttentionProblem p, Plan
     __shared__ __attribute__((aligned(16))) Meeting<D, RT> lds;
     const int Hkv = p.cache.Hkv;
     if (!plan.share) {
-        int x = blockIdx.x;
-        const int g = x % Hkv;
-        x /= Hkv;
-        const int first = x % plan.tiles;
-        x /= plan.tiles;
+        Place own = place<R>(p, plan.tiles, blockIdx.x);
         if (plan.sorted) {
-            // workgroup x takes the x-th longest sequence
+            // in place of sequence b the b-th longest
             __shared__ __attribute__((aligned(16))) int lengths[kSorted];
             __shared__ int chosen;
             const int b = threadIdx.x;
@@ -817,13 +850,15 @@ __global__ __launch_bounds__(256, 2) void few_kernel(Kv4AttentionProblem p, Plan
                 rank += (other.x > mine || (other.x == mine && i < b)) + (other.y > mine || (other.y == mine && i + 1 < b)) +
                         (other.z > mine || (other.z == mine && i + 2 < b)) + (other.w > mine || (other.w == mine && i + 3 < b));
             }
-            if (b < p.B && rank == x) chosen = b;
+            if (b < p.B && rank == own.b) chosen = b;
             __syncthreads();
-            x = __builtin_amdgcn_readfirstlane(chosen);
+            own.b = __builtin_amdgcn_readfirstlane(chosen);
         }
-        const Sequence s = sequence(p, x);
+        const Sequence s = sequence(p, own.b);
         const Extent e = extent<R>(p, s);
-        for (int k = first; k < e.tiles; k += plan.tiles) few_rows<BF16, D, RT>(p, plan, s, g, k * R, e.base, 0, e.units, -1, lds);
+        if (own.k < 0) return;
+        for (int k = own.k; k < e.tiles; k += plan.tiles ? plan.tiles : e.tiles)
+            few_rows<BF16, D, RT>(p, plan, s, own.g, k * R, e.base, 0, e.units, -1, lds);
         return;
     }
     // Units of all sequences in a row, an even share for each workgroup.
@@ -976,19 +1011,27 @@ Cut cut(const Kv4AttentionProblem& p)
     const int cus = compute_units() > 0 ? compute_units() : 256;
     Cut c{};
     c.rt = p.cache.D == 256 || all <= 16 ? 1 : 2;
-    const int64_t wide = (all + 16 * c.rt * kWaves - 1) / (16 * c.rt * kWaves);
-    c.rows = all > 16 * c.rt && 2 * pairs * wide >= 3 * cus;
-    const int64_t narrow = (all + 16 * c.rt - 1) / (16 * c.rt);
-    // (workgroups stride over row tiles beyond the grid's limit of 2^32 threads)
-    c.tiles = (int)std::max<int64_t>(1, std::min<int64_t>(c.rows ? wide : narrow, kMaxBlocks / pairs));
-    c.blocks = pairs * c.tiles;
+    // Row tiles of R rows: max_q's for every sequence, or fewer places where the
+    // tokens can fill no more (63 decoding sequences and a prompt of 4096: 460 us
+    // against 889, a prompt of 512: 165 against 566).  Workgroups stride over what passes the grid's 2^32 threads.
+    const auto tile = [&](int64_t R) {
+        const int64_t each = (all + R - 1) / R, places = (p.T * p.share / R + p.B) * p.cache.Hkv;
+        const bool uneven = places < pairs * each && places <= kMaxBlocks;
+        c.tiles = uneven ? 0 : (int)std::max<int64_t>(1, std::min<int64_t>(each, kMaxBlocks / pairs));
+        c.blocks = uneven ? places : pairs * c.tiles;
+    };
+    tile(16 * c.rt * kWaves);
+    c.rows = all > 16 * c.rt && 2 * c.blocks >= 3 * cus;
+    if (!c.rows) tile(16 * c.rt);
     if (c.rows) return c;
     // Row tiles of more than 5 units are shared where whole ones leave room for two
     // workgroups a compute unit: 1 x 2048 tokens of 32 heads 11.5 us against 14, 1 x
     // 131071 of 8 heads 34.5 against 675; up to 5 units the second launch costs more
     // (1 x 517 of 32 heads 11.6 us against 8.7), and where the chip is full without it
     // the starts of the parts do (64 x 4096 of 8 heads 54 us against 50).
-    const int64_t units = (p.max_kv + kUnit - 1) / kUnit, total = c.blocks * units;
+    // (The tokens that a tile sees count, with a window fewer than those cached.)
+    const int64_t seen = p.window ? std::min<int64_t>(p.max_kv, (int64_t)p.window + 16 * c.rt / p.share) : p.max_kv;
+    const int64_t units = (seen + kUnit - 1) / kUnit, total = c.blocks * units;
     if (units > 5 && c.blocks < 2 * cus) {
         c.share = true;
         c.blocks = std::min<int64_t>(total, 2 * cus);
@@ -997,7 +1040,7 @@ Cut cut(const Kv4AttentionProblem& p)
     }
     // Whole ones of uneven sequences: the longest first (64 x up to 8192 tokens of 8
     // heads 77 us to 66; not for few units, 64 x up to 512 10 us to 12).
-    c.sorted = !c.share && units > 5 && p.B > 1 && p.B <= kSorted;
+    c.sorted = !c.share && c.tiles && units > 5 && p.B > 1 && p.B <= kSorted;
     return c;
 }
 
