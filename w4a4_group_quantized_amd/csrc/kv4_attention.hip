@@ -694,44 +694,6 @@ __device__ inline Place place(const Kv4AttentionProblem& p, int tiles, int x)
     return {b, g, x - first(b)};
 }
 
-// Many rows: every wave has rows of its own and walks all the tokens they see.
-// (Unpacking for itself, without LDS and barriers, it takes 355 us for the prompt
-// against 322 on one box; 64 rows a wave do not fit the registers: 650 us.)
-template <bool BF16, int D, int RT>
-__global__ __launch_bounds__(256, 2) void rows_kernel(Kv4AttentionProblem p, Plan plan)
-{
-    __shared__ __attribute__((aligned(16))) Tile<D> buffers[2];
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const Place own = place<16 * RT * kWaves>(p, plan.tiles, blockIdx.x);
-    const Sequence s = sequence(p, own.b);
-    const int g = own.g, share = p.share, all = s.n * share, tiles = (all + 16 * RT * kWaves - 1) / (16 * RT * kWaves);
-    if (own.k < 0) return;
-    for (int k = own.k; k < tiles; k += plan.tiles ? plan.tiles : tiles) {
-        // (the last rows see the most tokens: first)
-        const int top = (tiles - 1 - k) * kWaves * 16 * RT, row0 = top + wave * 16 * RT;
-        Rows<D, RT> r;
-        RawRows<D, RT> raw;
-        fetch_rows<D, RT>(p, s, g, row0, raw);
-        make_rows<BF16, D, RT>(p, s, row0, raw, r);
-        const int i0 = row0 / share, i1 = min(row0 + 16 * RT - 1, all - 1) / share;
-        const int end = min(top + kWaves * 16 * RT, all) - 1;
-        attend_shared<D, RT>(p, s, g, seen_lo(p, s, top / share) & ~63, seen_hi(p, s, end / share), seen_lo(p, s, i1),
-                             seen_hi(p, s, i0), r, buffers);
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            const int row = row0 + 16 * rt + (lane & 15);
-            if (row >= all) continue;
-            const int i = row / share;
-            const int64_t at = (s.q0 + i) * p.Hq + g * share + (row - i * share);
-            const float by = r.l[rt] == 0.0f ? 0.0f : 1.0f / r.l[rt];
-#pragma unroll
-            for (int t = 0; t < D / 16; ++t)
-                store4<BF16>(p.out, at * D + 16 * t + 4 * (lane >> 4), row_values(r, rt, t, by));
-            if (p.lse && lane < 16) p.lse[at] = log_sum(r.m[rt], r.l[rt]);
-        }
-    }
-}
-
 // Few rows: the waves of a workgroup have the same rows and every fourth 64
 // tokens; their sums meet in LDS.  256 tokens of a row tile are a unit.
 constexpr int kUnit = 64 * kWaves;
@@ -812,6 +774,56 @@ __device__ inline Extent extent(const Kv4AttentionProblem& p, const Sequence& s)
     const int base = seen_lo(p, s, 0) & ~(kUnit - 1);
     // (at least one: rows that see nothing are written too)
     return {base, (s.n * p.share + R - 1) / R, max(1, (s.kv - base + kUnit - 1) / kUnit)};
+}
+
+// Many rows: every wave has rows of its own and walks all the tokens they see.
+// (Unpacking for itself, without LDS and barriers, it takes 355 us for the prompt
+// against 322 on one box; 64 rows a wave do not fit the registers: 650 us.)
+// UNEVEN: the batch may hold sequences of few rows (an instance of its own: the
+// prompt takes 325 us with both in one against 302).
+template <bool BF16, int D, int RT, bool UNEVEN>
+__global__ __launch_bounds__(256, 2) void rows_kernel(Kv4AttentionProblem p, Plan plan)
+{
+    __shared__ union __attribute__((aligned(16))) {
+        Tile<D> buffers[2];
+        Meeting<D, 1> meeting;
+    } lds;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const Place own = place<16 * RT * kWaves>(p, UNEVEN ? 0 : plan.tiles, blockIdx.x);
+    const Sequence s = sequence(p, own.b);
+    const int g = own.g, share = p.share, all = s.n * share, tiles = (all + 16 * RT * kWaves - 1) / (16 * RT * kWaves);
+    if (own.k < 0) return;
+    if (UNEVEN && all <= 16) {
+        // A decoding sequence beside a prompt: its tokens for all waves (63 of 4096
+        // tokens and a prompt of 512 take 64 us, with the rows in one wave 164).
+        const Extent e = extent<16>(p, s);
+        if (own.k < e.tiles) few_rows<BF16, D, 1>(p, plan, s, g, 0, e.base, 0, e.units, -1, lds.meeting);
+        return;
+    }
+    for (int k = own.k; k < tiles; k += UNEVEN ? tiles : plan.tiles) {
+        // (the last rows see the most tokens: first)
+        const int top = (tiles - 1 - k) * kWaves * 16 * RT, row0 = top + wave * 16 * RT;
+        Rows<D, RT> r;
+        RawRows<D, RT> raw;
+        fetch_rows<D, RT>(p, s, g, row0, raw);
+        make_rows<BF16, D, RT>(p, s, row0, raw, r);
+        const int i0 = row0 / share, i1 = min(row0 + 16 * RT - 1, all - 1) / share;
+        const int end = min(top + kWaves * 16 * RT, all) - 1;
+        attend_shared<D, RT>(p, s, g, seen_lo(p, s, top / share) & ~63, seen_hi(p, s, end / share), seen_lo(p, s, i1),
+                             seen_hi(p, s, i0), r, lds.buffers);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+            const int row = row0 + 16 * rt + (lane & 15);
+            if (row >= all) continue;
+            const int i = row / share;
+            const int64_t at = (s.q0 + i) * p.Hq + g * share + (row - i * share);
+            const float by = r.l[rt] == 0.0f ? 0.0f : 1.0f / r.l[rt];
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t)
+                store4<BF16>(p.out, at * D + 16 * t + 4 * (lane >> 4), row_values(r, rt, t, by));
+            if (p.lse && lane < 16) p.lse[at] = log_sum(r.m[rt], r.l[rt]);
+        }
+    }
 }
 
 // sum over the workgroup; `lds`: a number a wave
@@ -1012,8 +1024,8 @@ Cut cut(const Kv4AttentionProblem& p)
     Cut c{};
     c.rt = p.cache.D == 256 || all <= 16 ? 1 : 2;
     // Row tiles of R rows: max_q's for every sequence, or fewer places where the
-    // tokens can fill no more (63 decoding sequences and a prompt of 4096: 460 us
-    // against 889, a prompt of 512: 165 against 566).  Workgroups stride over what passes the grid's 2^32 threads.
+    // tokens can fill no more (63 decoding sequences and a prompt of 4096: 373 us
+    // against 889, a prompt of 512: 64 against 566).  Workgroups stride over what passes the grid's 2^32 threads.
     const auto tile = [&](int64_t R) {
         const int64_t each = (all + R - 1) / R, places = (p.T * p.share / R + p.B) * p.cache.Hkv;
         const bool uneven = places < pairs * each && places <= kMaxBlocks;
@@ -1049,7 +1061,8 @@ hipError_t launch(const Kv4AttentionProblem& p, const Cut& c, const Plan& plan, 
 {
     const unsigned blocks = (unsigned)c.blocks;
     if (c.rows) {
-        rows_kernel<BF16, D, RT><<<blocks, 256, 0, stream>>>(p, plan);
+        if (c.tiles) rows_kernel<BF16, D, RT, false><<<blocks, 256, 0, stream>>>(p, plan);
+        else rows_kernel<BF16, D, RT, true><<<blocks, 256, 0, stream>>>(p, plan);
         return hipGetLastError();
     }
     few_kernel<BF16, D, RT><<<blocks, 256, 0, stream>>>(p, plan);
