@@ -62,8 +62,8 @@ def rope_frequencies(rotary: int, base: float = 10000.0, *, scaling: str | None 
 class BatchPlan:
     """Where the newest tokens of a batch stand: table int32 [B, cols] of pages, kv_lens int32 [B]
     cached tokens with the new ones, cu_q int32 [B + 1] where each sequence's new tokens begin
-    (None: one a sequence).  `tokens` is the number of rows of a step, with the padding behind the
-    last sequence.  From them, on the GPU and without a copy to the host: positions and slots
+    (None: one a sequence).  `tokens` is the number of rows of a step, with the padding before the
+    first sequence and behind the last.  From them, on the GPU and without a copy to the host: positions and slots
     int64 [tokens] (slot -1: nothing is stored).  max_q, max_kv: see apex4.kv4_attention."""
 
     def __init__(self, table, kv_lens, cu_q=None, *, page: int, tokens: int | None = None, max_q: int | None = None,
@@ -82,6 +82,8 @@ class BatchPlan:
         owner = sequence.clamp_max(B - 1)
         position = kv_lens.long()[owner] - new
         live = (sequence < B) & (position >= 0) & (position < cols * page)
+        if cu_q is not None:
+            live &= row >= cu_q[0]
         held = position.clamp(0, cols * page - 1)
         at = table.long()[owner, held // page]
         self.positions = torch.where(live, position, torch.zeros_like(position))
