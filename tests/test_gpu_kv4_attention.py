@@ -106,6 +106,14 @@ def test_queries_ahead_of_the_cache_see_nothing(dev):
     check(dev, "float16", q, host, table, [4, 0, 70], cu, causal=False)
 
 
+def test_the_widest_window_is_none(dev):
+    """Also for queries before the first token, whose position less the window passes 32 bits."""
+    host, table, cu = make([9, 40, 300], [4, 11, 290], 2, 64, 16, 18)
+    q = queries(349, 4, 64, "float16")
+    check(dev, "float16", q, host, table, [4, 11, 290], cu, window=2 ** 31 - 1)
+    check(dev, "float16", q[:9], host, table[:1], [4], cu[:2], window=2 ** 31 - 1)
+
+
 @pytest.mark.parametrize("news", [[1, 1, 1], [30, 1, 90]])
 def test_pages_that_are_none(dev, news):
     """Numbers outside the cache are pages that hold nothing: not seen, not read."""
@@ -248,7 +256,7 @@ def test_prompts_among_sequences_of_few_tokens(dev, kind):
     host, table, cu = make(list(news), list(olds), Hkv, 64, 16, 17)
     q = queries(int(cu[-1]) + 50, Hq, 64, "float16", 17)
     check(dev, "float16", q, host, table, olds, cu + 37, max_q=int(max(news)), max_kv=int(max(olds)), window=window)
-    if not kind.startswith("many rows"):                                   # (a guess too low costs time only)
+    if not kind.startswith("many rows"):                         # (a guess too low costs time only)
         check(dev, "float16", q, host, table, olds, cu + 37, max_q=1, max_kv=1, window=window)
 
 

@@ -219,7 +219,7 @@ apex4_status apex4_kv4_attention(const void* q, int32_t type, int64_t T, int32_t
     p.cols = cols;
     p.scale = scale;
     p.causal = causal != 0;
-    p.window = window;
+    p.window = std::min(window, 1 << 30);      // (all tokens; positions less a window stay within 32 bits)
     p.out = o;
     p.lse = lse;
     p.ws = workspace;
