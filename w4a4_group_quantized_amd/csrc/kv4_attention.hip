@@ -34,9 +34,9 @@
 // Few rows (decoding): bound by the cache's bytes.  64 sequences of 4096 tokens, 8
 // key heads of 128, 64 query heads: 50 us (5.7 TB/s of a read's 5.7-6.2); lengths
 // up to 8192 at random 70 us (4.7 TB/s: the longest end last); one of 131071 tokens
-// 29 us and 5 us for the join (5.0 TB/s).  A wave alone takes 1.3 us for 64 tokens,
+// 29 us and 4 us for the join (5.0 TB/s).  A wave alone takes 1.3 us for 64 tokens,
 // 420 vector instructions of which unpacking is 224.
-// Many rows (prompts): 4096 tokens, 64 and 8 heads, 303 us (909 TFLOP/s of 275 GFLOP
+// Many rows (prompts): 4096 tokens, 64 and 8 heads, 300 us (917 TFLOP/s of 275 GFLOP
 // seen; the library's plain product of 8192^3 reaches 1164).  The vector ALU is
 // busy 59% of the time and the matrix unit 39%, and on a SIMD the two overlap little
 // (64 matrix instructions of one wave beside 256 fmas of another take 1.4 times as
