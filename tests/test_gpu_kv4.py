@@ -192,3 +192,23 @@ def test_refusals(dev):
         apex4.kv4_read(cache, slots, torch.float64)
     assert apex4.kv4_read(cache, slots[:0])[0].shape == (0, 2, 64)
     assert apex4.kv4_append(cache, k[:0], k[:0], slots[:0]) is None
+
+
+@pytest.mark.parametrize("dtype,D,T", [("float16", 128, 40001), ("bfloat16", 64, 70003), ("float32", 64, 40001),
+                                       ("float32", 128, 20001), ("bfloat16", 256, 20001)])
+def test_reads_beyond_the_caches(dev, dtype, D, T):
+    """More than 128 MB of values: the bits of the same tokens read in parts, and nothing beside them."""
+    dtype = getattr(torch, dtype)
+    cache = apex4.kv4_cache(33, 8, D, 64)
+    g = torch.Generator(device=dev).manual_seed(D)
+    for c in cache:
+        if c.dtype == torch.uint8:
+            c.random_(0, 256, generator=g)
+        else:
+            c.uniform_(0.01, 1.0, generator=g)
+    slots = torch.randint(-5, 33 * 64 + 5, (T,), device=dev, generator=g)
+    room = [torch.full((T + 2, 8, D), 7.0, dtype=dtype, device=dev) for _ in range(2)]
+    apex4.kv4_read(cache, slots, dtype, out=tuple(x[1:-1] for x in room))
+    parts = [apex4.kv4_read(cache, s, dtype) for s in slots.split(5000)]
+    for x, y in zip(room, zip(*parts)):
+        assert torch.equal(x[1:-1], torch.cat(y)) and (x[[0, -1]] == 7).all()

@@ -8,7 +8,8 @@
 // find the head's largest number by lane moves.  Measured: 4096 tokens x 64 heads
 // x 128 bf16 turned in 22 us (6.0 TB/s, the last-level cache holds part of it);
 // 4096 tokens of 64 query and 8 key heads appended in 30 us (160 MB, 5.3 TB/s);
-// 65521 tokens of 8 heads read in 78 us (340 MB, 4.4 TB/s).
+// 65521 tokens of 8 heads read in 55 us again and again, 63 with other work between
+// (340 MB, 5.4-6.2 TB/s).
 #include "attention.h"
 #include "quant_rule.h"
 #include "rotary.h"
@@ -158,7 +159,7 @@ __global__ __launch_bounds__(256) void append_kernel(Kv4AppendProblem p, int par
 // of `lds` (the head's own, 16-byte aligned), so that a lane writes 16 neighbouring
 // bytes at a time (written where the lanes have them, 64 neighbouring bytes a
 // head and store, the call took half as long again).
-template <int TYPE, int N>
+template <int TYPE, int N, bool FAR>
 __device__ inline void store_values(void* base, int64_t at, int r, const float (&v)[N], uint32_t* lds)
 {
     constexpr int WORDS = (TYPE == 0 ? 16 : 8) * N, EACH = WORDS / 16;      // of the head, of a lane
@@ -180,17 +181,17 @@ __device__ inline void store_values(void* base, int64_t at, int r, const float (
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
     uint32_t* out = static_cast<uint32_t*>(base) + at / (TYPE == 0 ? 1 : 2) + r * EACH;
     if (EACH == 2) {
-        *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(lds + r * EACH);
+        rotary::put<FAR>(out, *reinterpret_cast<const uint2*>(lds + r * EACH));
     } else {
 #pragma unroll
         for (int e = 0; e < EACH; e += 4)
-            *reinterpret_cast<uint4*>(out + e) = *reinterpret_cast<const uint4*>(lds + r * EACH + e);
+            rotary::put<FAR>(out + e, *reinterpret_cast<const uint4*>(lds + r * EACH + e));
     }
 }
 
 // 16 lanes a head: of its key D / 16 neighbours each, of its value the numbers r +
 // 16 h, whose bytes lie together in the cache (with those of three other tokens).
-template <int TYPE, int D, int ROWS>
+template <int TYPE, int D, int ROWS, bool FAR>
 __global__ __launch_bounds__(256) void read_kernel(Kv4ReadProblem p, int n)
 {
     constexpr int N = D / 16, WORDS = TYPE == 0 ? D : D / 2;
@@ -242,31 +243,45 @@ __global__ __launch_bounds__(256) void read_kernel(Kv4ReadProblem p, int n)
         const int64_t y = (int64_t)row * D;
         if (N == 4) {
             if (TYPE == 0) {
-                *reinterpret_cast<float4*>(static_cast<float*>(p.k) + y + N * r) = make_float4(k[0], k[1], k[2], k[3]);
+                rotary::put<FAR>(static_cast<float*>(p.k) + y + N * r,
+                                 __builtin_bit_cast(uint4, make_float4(k[0], k[1], k[2], k[3])));
             } else {
                 const uint32_t a = e4m3::to16<TYPE == 2>(k[0]) | (uint32_t)e4m3::to16<TYPE == 2>(k[1]) << 16;
                 const uint32_t b = e4m3::to16<TYPE == 2>(k[2]) | (uint32_t)e4m3::to16<TYPE == 2>(k[3]) << 16;
-                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.k) + y + N * r) = make_uint2(a, b);
+                rotary::put<FAR>(static_cast<uint16_t*>(p.k) + y + N * r, make_uint2(a, b));
             }
         } else {
 #pragma unroll
-            for (int e = 0; e < N; e += 8) rotary::store8<TYPE>(p.k, y + N * r + e, k + e);
+            for (int e = 0; e < N; e += 8) rotary::store8<TYPE, FAR>(p.k, y + N * r + e, k + e);
         }
-        store_values<TYPE, N>(p.v, y, r, v, lds[threadIdx.x / 16][i]);
+        store_values<TYPE, N, FAR>(p.v, y, r, v, lds[threadIdx.x / 16][i]);
     }
+}
+
+template <int TYPE, int D>
+void read(const Kv4ReadProblem& p, hipStream_t stream)
+{
+    // several heads' loads in flight where there are enough of them
+    constexpr int ROWS = 2;
+    const int n = (int)(p.T * p.cache.Hkv);
+    const unsigned blocks = (unsigned)((n + 16 * ROWS - 1) / (16 * ROWS));
+    // More than 128 MB, half the last-level cache, are stored past it (65521 tokens of
+    // 8 heads, 268 MB, 79 us to 55; 49152 and a copy of them 147 to 128; of 67 MB the
+    // read gains a few percent and a copy of it loses more: 38.6 to 40.8).  Only heads
+    // of up to 256 bytes, which a store of 16 lanes writes whole: in pieces such
+    // stores cost far more (heads of 256 in fp32 96 us to 322).
+    constexpr int64_t head = D * (TYPE == 0 ? 4 : 2);
+    if (head <= 256 && 2 * n * head > (int64_t(1) << 27)) read_kernel<TYPE, D, ROWS, head <= 256><<<blocks, 256, 0, stream>>>(p, n);
+    else read_kernel<TYPE, D, ROWS, false><<<blocks, 256, 0, stream>>>(p, n);
 }
 
 template <int TYPE>
 hipError_t read(const Kv4ReadProblem& p, hipStream_t stream)
 {
-    const int n = (int)(p.T * p.cache.Hkv);
-    // several heads' loads in flight where there are enough of them
-    constexpr int ROWS = 2;
-    const unsigned blocks = (unsigned)((n + 16 * ROWS - 1) / (16 * ROWS));
     switch (p.cache.D) {
-    case 64: read_kernel<TYPE, 64, ROWS><<<blocks, 256, 0, stream>>>(p, n); break;
-    case 128: read_kernel<TYPE, 128, ROWS><<<blocks, 256, 0, stream>>>(p, n); break;
-    default: read_kernel<TYPE, 256, ROWS><<<blocks, 256, 0, stream>>>(p, n); break;    // checked by the caller
+    case 64: read<TYPE, 64>(p, stream); break;
+    case 128: read<TYPE, 128>(p, stream); break;
+    default: read<TYPE, 256>(p, stream); break;    // checked by the caller
     }
     return hipGetLastError();
 }

@@ -123,19 +123,36 @@ __device__ inline void load8(const void* base, int64_t at, float* v)
     }
 }
 
-template <int TYPE>
+// A store of two or four words; FAR: past the caches (what is written is more
+// than they hold, so that nothing would find it there).
+template <bool FAR>
+__device__ inline void put(void* out, uint2 v)
+{
+    typedef uint32_t Two __attribute__((ext_vector_type(2)));
+    if (FAR) __builtin_nontemporal_store(Two{v.x, v.y}, static_cast<Two*>(out));
+    else *static_cast<uint2*>(out) = v;
+}
+template <bool FAR>
+__device__ inline void put(void* out, uint4 v)
+{
+    typedef uint32_t Four __attribute__((ext_vector_type(4)));
+    if (FAR) __builtin_nontemporal_store(Four{v.x, v.y, v.z, v.w}, static_cast<Four*>(out));
+    else *static_cast<uint4*>(out) = v;
+}
+
+template <int TYPE, bool FAR = false>
 __device__ inline void store8(void* base, int64_t at, const float* v)
 {
     if (TYPE == 0) {
-        float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
-        p[0] = make_float4(v[0], v[1], v[2], v[3]);
-        p[1] = make_float4(v[4], v[5], v[6], v[7]);
+        float* p = static_cast<float*>(base) + at;
+        put<FAR>(p, __builtin_bit_cast(uint4, make_float4(v[0], v[1], v[2], v[3])));
+        put<FAR>(p + 4, __builtin_bit_cast(uint4, make_float4(v[4], v[5], v[6], v[7])));
     } else {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             w[i] = e4m3::to16<TYPE == 2>(v[2 * i]) | (uint32_t)e4m3::to16<TYPE == 2>(v[2 * i + 1]) << 16;
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+        put<FAR>(static_cast<uint16_t*>(base) + at, make_uint4(w[0], w[1], w[2], w[3]));
     }
 }
 
