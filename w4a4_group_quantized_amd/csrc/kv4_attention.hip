@@ -31,11 +31,11 @@
 // unit with 4 tokens of one row in a lane, which is how the second product wants
 // w: nothing goes through LDS but a token's three factors.
 //
-// Few rows (decoding): bound by the cache's bytes.  64 sequences of 4096 tokens, 8
-// key heads of 128, 64 query heads: 50 us (5.7 TB/s of a read's 5.7-6.2); lengths
-// up to 8192 at random 70 us (4.7 TB/s: the longest end last); one of 131071 tokens
-// 29 us and 4 us for the join (5.0 TB/s).  A wave alone takes 1.3 us for 64 tokens,
-// 420 vector instructions of which unpacking is 224.
+// Few rows (decoding): bound by the cache's bytes.  64 sequences of up to 8192
+// tokens at random, 8 key heads of 128, 64 query heads: 62 us (5.3 TB/s of a
+// read's 5.7-6.2); of 4096 each, several layers in turn, 60 us (4.8 TB/s); one of
+// 131071 tokens 33 us with the join's 4 (4.9 TB/s in the first launch).  A wave
+// alone takes 1.3 us for 64 tokens, 420 vector instructions of which unpacking is 224.
 // Many rows (prompts): 4096 tokens, 64 and 8 heads, 300 us (917 TFLOP/s of 275 GFLOP
 // seen; the library's plain product of 8192^3 reaches 1164).  The vector ALU is
 // busy 59% of the time and the matrix unit 39%, and on a SIMD the two overlap little
@@ -234,33 +234,46 @@ struct Codes {
     uint32_t w[4][D / 32];
 };
 
-template <int D>
+// ONCE: for one row tile, so they need not stay in the caches (where sequences share
+// pages the time is the same): what they would push out is read again sooner (64 sequences of 4096
+// tokens in each of five layers in turn 66.5 us a layer to 60, 8 of 4096 in 34
+// layers 17.7 to 16.5; but 143 MB read by one call after the other 34 to 35.5).
+template <bool ONCE, typename T>
+__device__ inline T load(const uint8_t* p)
+{
+    const T* at = reinterpret_cast<const T*>(p);
+    return ONCE ? __builtin_nontemporal_load(at) : *at;
+}
+typedef uint32_t Two __attribute__((ext_vector_type(2)));
+typedef uint32_t Four __attribute__((ext_vector_type(4)));
+
+template <int D, bool ONCE>
 __device__ inline void load_codes(Codes<D>& c, int s, const uint8_t* p)
 {
     if (D == 64) {
-        const uint2 a = *reinterpret_cast<const uint2*>(p);
+        const Two a = load<ONCE, Two>(p);
         c.w[s][0] = a.x, c.w[s][1] = a.y;
     } else {
 #pragma unroll
         for (int k = 0; k < D / 128; ++k) {
-            const uint4 a = *reinterpret_cast<const uint4*>(p + (D / 128 == 2 ? 64 * k : 0));
+            const Four a = load<ONCE, Four>(p + (D / 128 == 2 ? 64 * k : 0));
             c.w[s][4 * k] = a.x, c.w[s][4 * k + 1] = a.y, c.w[s][4 * k + 2] = a.z, c.w[s][4 * k + 3] = a.w;
         }
     }
 }
 
 // (a lane's values are D/8 neighbouring bytes)
-template <int D>
+template <int D, bool ONCE>
 __device__ inline void load_values(Codes<D>& c, int s, const uint8_t* p)
 {
     if (D == 256) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const uint4 a = *reinterpret_cast<const uint4*>(p + 16 * k);
+            const Four a = load<ONCE, Four>(p + 16 * k);
             c.w[s][4 * k] = a.x, c.w[s][4 * k + 1] = a.y, c.w[s][4 * k + 2] = a.z, c.w[s][4 * k + 3] = a.w;
         }
     } else {
-        load_codes<D>(c, s, p);
+        load_codes<D, ONCE>(c, s, p);
     }
 }
 
@@ -426,6 +439,8 @@ template <bool BF16, int D, int RT>
 __device__ inline void attend(const Kv4AttentionProblem& p, const Sequence& s, int g, int row0, int from, int to, int step,
                               int lo_max, int hi_min, Rows<D, RT>& r, float* factors)
 {
+    // (a lane reads a value of 256 numbers in two pieces, which would fetch its lines twice)
+    constexpr bool ONCE = RT == 1 && D <= 128;
     const Kv4Cache& c = p.cache;
     const int lane = threadIdx.x & 63, quad = lane >> 4;
     const int32_t* table = p.table + s.b * p.cols;
@@ -457,12 +472,12 @@ __device__ inline void attend(const Kv4AttentionProblem& p, const Sequence& s, i
     const auto load_k = [&](Ahead& a) {
         a.ks = c.k_scales[a.row];
 #pragma unroll
-        for (int sub = 0; sub < 4; ++sub) load_codes<D>(a.k, sub, c.k_codes + base(a, sub) + key_at);
+        for (int sub = 0; sub < 4; ++sub) load_codes<D, ONCE>(a.k, sub, c.k_codes + base(a, sub) + key_at);
     };
     const auto load_v = [&](Ahead& a) {
         a.vs = c.v_scales[a.row];
 #pragma unroll
-        for (int sub = 0; sub < 4; ++sub) load_values<D>(a.v, sub, c.v_codes + base(a, sub) + value_at);
+        for (int sub = 0; sub < 4; ++sub) load_values<D, ONCE>(a.v, sub, c.v_codes + base(a, sub) + value_at);
     };
     RawRows<D, RT> raw;
     look(from);
@@ -578,8 +593,8 @@ __device__ inline void attend_shared(const Kv4AttentionProblem& p, const Sequenc
         const bool some = first < to && at >= 0 && at < c.pages;
         const int64_t row = some ? (((int64_t)at * c.Hkv + g) << c.shift) + (first & (c.page - 1)) : 0;
         valid = some && first + (lane & 15) < to;
-        load_codes<D>(k, 0, c.k_codes + row * (D / 2) + key_at);
-        load_values<D>(v, 0, c.v_codes + row * (D / 2) + value_at);
+        load_codes<D, false>(k, 0, c.k_codes + row * (D / 2) + key_at);
+        load_values<D, false>(v, 0, c.v_codes + row * (D / 2) + value_at);
         ks = c.k_scales[row + (lane & 15)];
         vs = c.v_scales[row + (lane & 15)];
     };
