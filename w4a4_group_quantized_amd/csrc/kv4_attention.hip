@@ -34,7 +34,7 @@
 // Few rows (decoding): bound by the cache's bytes.  64 sequences of up to 8192
 // tokens at random, 8 key heads of 128, 64 query heads: 62 us (5.3 TB/s of a
 // read's 5.7-6.2); of 4096 each, several layers in turn, 60 us (4.8 TB/s); one of
-// 131071 tokens 33 us with the join's 4 (4.9 TB/s in the first launch).  A wave
+// 131071 tokens 33 us with the join's 4 (5.1 TB/s in the first launch).  A wave
 // alone takes 1.3 us for 64 tokens, 420 vector instructions of which unpacking is 224.
 // Many rows (prompts): 4096 tokens, 64 and 8 heads, 300 us (917 TFLOP/s of 275 GFLOP
 // seen; the library's plain product of 8192^3 reaches 1164).  The vector ALU is
