@@ -666,11 +666,12 @@ __device__ inline void attend_shared(const Kv4AttentionProblem& p, const Sequenc
     for (int rt = 0; rt < RT; ++rt) r.l[rt] = row_sum(r.l[rt]);
 }
 
-// numbers 16 t + 4 quad .. + 3 of a lane's row, times `by`
+// numbers 16 t + 4 quad .. + 3 of a lane's row, times `by` (last: with values' scales
+// of 2^108 and more, 1 / l times 2^20 is beyond fp32)
 template <int D, int RT>
 __device__ inline float4v row_values(const Rows<D, RT>& r, int rt, int t, float by)
 {
-    return (r.o[rt][t] - r.w[rt][0]) * (by * 0x1p20f);
+    return (r.o[rt][t] - r.w[rt][0]) * 0x1p20f * by;
 }
 
 template <bool BF16>
