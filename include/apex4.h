@@ -560,7 +560,8 @@ apex4_status apex4_kv4_read(const void* k_codes, const float* k_scales, const vo
  *   only slower.
  *   Products of codes and queries, and of weights and codes, run on the fp16
  *   matrix units and sum in fp32; a weight p_j times the scale of v_j is rounded to
- *   fp16, relative to the largest so far.  A value's scale below 2^-80 counts as
+ *   fp16 for the product with the codes (2^-11 of itself, or 2^-32 of the largest so
+ *   far), and counts unrounded in the sum below it.  A value's scale below 2^-80 counts as
  *   2^-80; |scale| times a key's scale has to stay below 2^100.
  *   Queries and scales that are not finite show in the rows that see them only.
  *   workspace: at least apex4_kv4_attention_workspace_size() bytes (NULL allowed

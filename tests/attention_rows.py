@@ -17,8 +17,9 @@ def attention_rows(q, name, cache, table, kv_lens, cu_q, rows, scale=None, causa
         moves P_j c_j in the numerator and p_j in the sum by that much of themselves;
       - a weight is rounded to fp16: 2^-11 of itself, or half fp16's smallest step where the row's largest
         weight is at least 2^7, so 2^-32 of `largest`;
-      - products of 32 tokens, with the code and with the offset, cut below 2^-18 of their largest weight;
-      - run / 8 + 64 additions of fp32 of up to 23 of the weights, run / 4 + 64 of the row's sum.
+      - products of 32 tokens, with the code (up to 15) and with the offset of 8, cut below 2^-18 of their
+        largest weight each, and by no more than there is of them;
+      - run / 8 + 64 additions of fp32 to the sums of P_j (c_j + 8) and 8 P_j, run / 4 + 64 to the row's.
     """
     T, Hq, D = q.shape
     share = Hq // cache.kc.shape[1]
@@ -54,10 +55,11 @@ def attention_rows(q, name, cache, table, kv_lens, cu_q, rows, scale=None, causa
         largest = P.max()
         chunks = np.zeros(int(j[-1]) // 32 + 1)
         np.maximum.at(chunks, j // 32, P)
+        dropped = np.minimum(23 * P, 2 * 2.0 ** -18 * chunks[j // 32]).sum()
         sizes = np.abs(c)
         bound[at] = (wrong * P) @ sizes + np.abs(o[at]) * (wrong @ pr) \
-            + np.maximum(2.0 ** -11 * P, 2.0 ** -32 * largest) @ sizes + 64 * 2.0 ** -18 * chunks.sum() \
-            + (many / 8 + 64) * 2.0 ** -24 * 23 * P.sum() + (many / 4 + 64) * 2.0 ** -24 * np.abs(o[at]) \
+            + np.maximum(2.0 ** -11 * P, 2.0 ** -32 * largest) @ sizes + dropped \
+            + (many / 8 + 64) * 2.0 ** -24 * (P @ (c + 16)) + (many / 4 + 64) * 2.0 ** -24 * np.abs(o[at]) \
             + 8 * 2.0 ** -80 + rounding(o[at], name)
         lse_bound[at] = wrong.max() + (many / 4 + 64) * 2.0 ** -24 + np.abs(lse[at]) * 2.0 ** -22
     return o, lse, bound, lse_bound

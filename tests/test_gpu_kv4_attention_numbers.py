@@ -53,3 +53,27 @@ def test_values_of_any_size(dev, D, T, Hq, kernel, power):
     got = run(dev, q, host, table, [900], [0, T], max_q=T, max_kv=900)
     rows = [(t, h) for t in sorted({0, 1, T // 2, T - 1}) for h in (0, Hq // 2, Hq - 1)]
     close(*got, attention_rows(q.double().numpy(), "bfloat16", host, table, [900], [0, T], rows), "bfloat16", rows)
+
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+@pytest.mark.parametrize("B,T,Hq,Hkv,kernel,waves", [(1, 800, 64, 8, "rows", 1), (64, 64, 64, 8, "few", 4)])
+def test_many_small_weights_beside_a_large_one(dev, dtype, B, T, Hq, Hkv, kernel, waves):
+    """One token with 2^25.05 times the weight of every other and a value of zero: the output is the
+    others'.  (Four waves share the tokens of few rows; one of them has the large weight.)"""
+    kv, D = 8192, 64
+    way = cut(T, B, Hq, Hkv, D, T // B, kv, cus=cus())
+    assert way["kernel"] == kernel and not way["share"]
+    host = ref.Cache(kv // 64, Hkv, 64, D, 7)
+    table = np.random.default_rng(8).permutation(kv // 64)[None].repeat(B, 0).astype(np.int32)
+    first = (table[0, 0], slice(None), 0)                    # token 0 of all heads
+    host.kc[:], host.ks[:], host.vs[:] = 1, 0, 1
+    host.ks[first] = 25.05 * np.log(2.0) / D
+    host.vc[:] = 7
+    host.vc[first] = 0
+    q = torch.ones((T, Hq, D)).to(getattr(torch, dtype))
+    lens, cu = [kv] * B, np.arange(B + 1) * (T // B)
+    got = run(dev, q, host, table, lens, cu, max_q=T // B, max_kv=kv, scale=1.0)
+    rows = [(0, 0), (T // 2, Hq // 2), (T - 1, Hq - 1)]
+    want = attention_rows(q.double().numpy(), dtype, host, table, lens, cu, rows, scale=1.0, run=kv // waves)
+    assert (want[2] < want[0] / waves).all()                 # (what they lose without the others' weights)
+    close(*got, want, dtype, rows)

@@ -9,10 +9,13 @@
 //     O += V^T w  numbers x rows   the same instruction, w rounded to fp16
 //     l += w / s_v
 //
-// M is the row's running maximum of t, so the weights that the matrix unit sees
-// carry the values' scales and the largest of them is near 1 whatever those are;
-// M moves only when a tile exceeds it by 2^8 (fp16 holds that), which keeps the
-// rescaling of O out of most tiles.  l and M are fp32.
+// M follows the row's running maximum of t, so the weights that the matrix unit sees
+// carry the values' scales and the largest of them is 2^7 to 2^15 whatever those are:
+// M is the maximum less 7 when it moves, and moves only when a tile exceeds that
+// maximum by 8, which keeps the rescaling of O out of most tiles.  fp16's smallest
+// step is then 2^-31 of the largest weight or less; with weights of at most 1 it was
+// 2^-24, and thousands of tokens below half of that beside a large one left O, but
+// not l.  l (of the weights before they are rounded) and M are fp32.
 //
 // Codes go to the matrix unit nearly as they lie: the nibble u = c + 8 in bits
 // 4..7 of an fp16 is the subnormal number u 2^-20, which the instruction takes
@@ -57,8 +60,8 @@ typedef float float4v __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 4;
 constexpr int64_t kMaxBlocks = (1 << 24) - 1;
-constexpr float kTiny = 0x1p-80f;      // the least scale of values: 2^8 / kTiny, 2^30 times, stays finite
-constexpr float kLazy = 8.0f;
+constexpr float kTiny = 0x1p-80f;      // the least scale of values: 2^15 / kTiny, 2^30 times, stays finite
+constexpr float kLazy = 8.0f, kRoom = 7.0f;     // (fp16 holds weights of 2^(kLazy + kRoom))
 
 // How a call is cut (launch_kv4_attention).
 struct Plan {
@@ -347,7 +350,7 @@ __device__ inline void mask(const Rows<D, RT>& r, float4v (&x)[RT][NS], const fl
     }
 }
 
-// Moves the rows' maxima where a tile is above them, with what is relative to them.
+// Moves the rows' M where a tile is far above it, with what is relative to it.
 template <int D, int RT>
 __device__ inline void raise(Rows<D, RT>& r, float (&top)[RT])
 {
@@ -355,12 +358,12 @@ __device__ inline void raise(Rows<D, RT>& r, float (&top)[RT])
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         top[rt] = row_max(top[rt]);
-        above |= top[rt] > r.m[rt] + kLazy;
+        above |= top[rt] > r.m[rt] + (kLazy + kRoom);
     }
     if (!__any(above)) return;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        const float m = top[rt] > r.m[rt] + kLazy ? top[rt] : r.m[rt];
+        const float m = top[rt] > r.m[rt] + (kLazy + kRoom) ? top[rt] - kRoom : r.m[rt];
         const float old = m == r.m[rt] ? 1.0f : __builtin_amdgcn_exp2f(r.m[rt] - m);
         r.m[rt] = m;
         r.l[rt] *= old;
