@@ -50,7 +50,8 @@ def rope_frequencies(rotary: int, base: float = 10000.0, *, scaling: str | None 
     elif scaling == "yarn":
         def number(turns):                                   # of the pair that makes so many turns
             return half * math.log(original / (turns * 2 * math.pi)) / math.log(base)
-        first, last = max(math.floor(number(high)), 0), min(math.ceil(number(low)), half - 1)
+        # (the end of the ramp may lie behind the last pair, which then keeps a part)
+        first, last = max(math.floor(number(high)), 0), min(math.ceil(number(low)), rotary - 1)
         keep = 1.0 - ((pair - first) / max(last - first, 0.001)).clamp(0.0, 1.0)
         freqs = freqs * (keep + (1 - keep) / factor)
         scale = 0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0
