@@ -32,3 +32,10 @@ def test_yarn_over_contexts(rotary, base, original):
     plain = rope_frequencies(rotary, base, device="cpu")[0]
     if number(1.0) > rotary / 2 - 1:                         # every pair makes more than `low` turns
         assert (f > plain / 8 * 1.0001).all()
+
+
+def test_yarn_by_default_blends_from_32_turns_to_1():
+    want = yarn(128, 10000.0, 4.0, 4096, 1.0, 32.0)[0]
+    assert torch.allclose(rope_frequencies(128, scaling="yarn", factor=4.0, device="cpu")[0], want, rtol=1e-13)
+    by_wavelength = rope_frequencies(128, scaling="wavelength", factor=4.0, device="cpu")[0]       # as before: from 4
+    assert torch.equal(by_wavelength, rope_frequencies(128, scaling="wavelength", factor=4.0, high=4.0, device="cpu")[0])

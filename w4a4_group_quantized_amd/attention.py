@@ -21,20 +21,22 @@ from .linear import LlamaLayerW4A4
 
 
 def rope_frequencies(rotary: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
-                     original: int = 4096, low: float = 1.0, high: float = 4.0, device="cuda"):
+                     original: int = 4096, low: float = 1.0, high: float | None = None, device="cuda"):
     """(frequencies float64 [rotary / 2], the factor that goes with them) of rotary positions,
     base^(-2 i / rotary) with
 
     scaling None: as they are; "linear": divided by `factor`; "ntk": a base grown so that the
     slowest turns `factor` times slower and the fastest stays; "wavelength": divided by `factor`
     where a turn takes more than original / low positions, as they are where it takes less than
-    original / high, and blended between; "yarn": divided by `factor` where there are fewer than
-    `low` turns in `original` positions, as they are from `high` on, blended by the pair's
-    number between (usual: low 1, high 32), with a factor 0.1 ln(factor) + 1 for queries and
+    original / high, and blended between (high 4 when None); "yarn": divided by `factor` where there
+    are fewer than `low` turns in `original` positions, as they are from `high` on (32 when None),
+    blended by the pair's number between, with a factor 0.1 ln(factor) + 1 for queries and
     keys (1 otherwise): the `scale` of apex4.rope, the `rope_scale` of apex4.kv4_append.
     """
     if rotary < 16 or rotary % 16 or factor < 1.0:
         raise ValueError(f"rotary must be a multiple of 16 and factor at least 1, got {rotary, factor}")
+    if high is None:
+        high = 32.0 if scaling == "yarn" else 4.0
     half = rotary // 2
     pair = torch.arange(half, dtype=torch.float64)
     scale = 1.0
