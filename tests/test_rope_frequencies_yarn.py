@@ -39,3 +39,13 @@ def test_yarn_by_default_blends_from_32_turns_to_1():
     assert torch.allclose(rope_frequencies(128, scaling="yarn", factor=4.0, device="cpu")[0], want, rtol=1e-13)
     by_wavelength = rope_frequencies(128, scaling="wavelength", factor=4.0, device="cpu")[0]       # as before: from 4
     assert torch.equal(by_wavelength, rope_frequencies(128, scaling="wavelength", factor=4.0, high=4.0, device="cpu")[0])
+
+
+def test_refusals():
+    for scaling in ("wavelength", "yarn"):
+        for bad in (dict(low=4.0, high=4.0), dict(low=4.0, high=1.0), dict(low=0.0), dict(low=-1.0), dict(original=0)):
+            with pytest.raises(ValueError):
+                rope_frequencies(128, scaling=scaling, factor=2.0, device="cpu", **bad)
+    for base in (1.0, 0.0, -10.0, float("nan")):
+        with pytest.raises(ValueError):
+            rope_frequencies(128, base, scaling="yarn", factor=2.0, device="cpu")

@@ -33,10 +33,14 @@ def rope_frequencies(rotary: int, base: float = 10000.0, *, scaling: str | None 
     blended by the pair's number between, with a factor 0.1 ln(factor) + 1 for queries and
     keys (1 otherwise): the `scale` of apex4.rope, the `rope_scale` of apex4.kv4_append.
     """
-    if rotary < 16 or rotary % 16 or factor < 1.0:
+    if rotary < 16 or rotary % 16 or not factor >= 1.0:
         raise ValueError(f"rotary must be a multiple of 16 and factor at least 1, got {rotary, factor}")
     if high is None:
         high = 32.0 if scaling == "yarn" else 4.0
+    if not base > (1.0 if scaling == "yarn" else 0.0):
+        raise ValueError(f"base must be above 0 (yarn: above 1), got {base}")
+    if scaling in ("wavelength", "yarn") and not (0.0 < low < high and original > 0):
+        raise ValueError(f"0 < low < high and original > 0 are needed, got {low, high, original}")
     half = rotary // 2
     pair = torch.arange(half, dtype=torch.float64)
     scale = 1.0
