@@ -31,9 +31,10 @@ class W4A4Linear(torch.nn.Module):
     (apex4_pack_weight's outputs), group_a: activation group size used by the
     on-the-fly quantization (group_w == group_a, or group_w == K for
     per-channel weight scales with activation groups).  Inputs: fp16
-    [..., K] on the GPU; output fp16 [..., N].  The call's workspace (the
-    activation codes and scales, and the GEMM's K-split partials) is kept per
-    row count, so repeated calls at one shape allocate only the output.
+    [..., K] on the GPU; output fp16 [..., N].  Every call takes its workspace
+    (the activation codes and scales, and the GEMM's K-split partials) from
+    torch's caching allocator, so calls on different streams, or in several
+    captured graphs, do not share one.
     """
 
     def __init__(self, qw: torch.Tensor, sw: torch.Tensor, group_w: int, group_a: int | None = None):
@@ -46,21 +47,12 @@ class W4A4Linear(torch.nn.Module):
         self.group_a = group_w if group_a is None else group_a
         self.register_buffer("qw", qw)
         self.register_buffer("sw", sw)
-        self._ws = {}
 
     @classmethod
     def from_weight(cls, w: torch.Tensor, group_w: int = 128, group_a: int | None = None) -> "W4A4Linear":
         """Quantize and pack an fp16 [N, K] GPU weight (the offline step)."""
         qw, sw = apex4.pack_weight(w.contiguous(), group_w)
         return cls(qw, sw, group_w, group_a)
-
-    def _workspace(self, M: int, device):
-        ws = self._ws.get(M)
-        if ws is None:
-            need = apex4.linear_workspace_size(M, self.out_features, self.in_features, self.group_a, self.group_w)
-            ws = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
-            self._ws[M] = ws
-        return ws
 
     def forward(self, x: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
         if x.shape[-1] != self.in_features:
@@ -78,8 +70,7 @@ class W4A4Linear(torch.nn.Module):
                 raise ValueError(f"out must be a contiguous {(*lead, self.out_features)} tensor, "
                                  f"got {tuple(out.shape)} (contiguous: {out.is_contiguous()})")
             y16 = out.view(M, self.out_features)
-        y = apex4.linear(x2, self.group_a, self.qw, self.sw, self.group_w, y16=y16,
-                         workspace=self._workspace(M, x2.device))
+        y = apex4.linear(x2, self.group_a, self.qw, self.sw, self.group_w, y16=y16)
         return y.reshape(*lead, self.out_features)
 
     def extra_repr(self) -> str:
