@@ -152,8 +152,7 @@ def pack_weight(w, group: int):
     N, K = w.shape
     qw = torch.empty((N, K // 2), dtype=torch.uint8, device=w.device)
     sw = torch.empty((N, _cols(K, group)), dtype=torch.float32, device=w.device)
-    _check("apex4_pack_weight", lib().apex4_pack_weight(
-        _ptr(w), N, K, group, _ptr(qw), _ptr(sw), _stream(torch, w.device)))
+    _call("apex4_pack_weight", w.device, _ptr(w), N, K, group, _ptr(qw), _ptr(sw))
     return qw, sw
 
 
@@ -252,15 +251,14 @@ def linear(x, ga: int, qw, sw, gw: int, *, want_y32: bool = False, y16=None, y32
         y16 = torch.empty((M, N), dtype=torch.float16, device=dev)
     if want_y32 and y32 is None:
         y32 = torch.empty((M, N), dtype=torch.float32, device=dev)
-    need = linear_workspace_size(M, N, K, ga, gw)
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace is None:
+        need = _size("apex4_linear_workspace_size", dev, M, N, K, ga, gw)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     if workspace is not None:
         _need_gpu(workspace, "workspace", torch.uint8, None, dev)
     nbytes = 0 if workspace is None else workspace.numel()
-    _check("apex4_linear_w4a4", lib().apex4_linear_w4a4(
-        _ptr(x), ga, _ptr(qw), _ptr(sw), gw, M, N, K, _ptr(y16), _ptr(y32), _ptr(workspace), nbytes,
-        _stream(torch, dev)))
+    _call("apex4_linear_w4a4", dev, _ptr(x), ga, _ptr(qw), _ptr(sw), gw, M, N, K, _ptr(y16), _ptr(y32),
+          _ptr(workspace), nbytes)
     return (y16, y32) if want_y32 else y16
 
 
