@@ -146,6 +146,18 @@ class CachedLayerW4A4(LlamaLayerW4A4):
         self.turn = dict(interleaved=interleaved, rope_scale=rope_scale)
         self.register_buffer("inv_freq", inv_freq)
 
+    @classmethod
+    def random(cls, hidden: int = 4096, intermediate: int = 11008, group: int = 128, seed: int = 0, device="cuda", *,
+               heads: int = 32, kv_heads: int | None = None, head_dim: int = 128,
+               base: float = 10000.0) -> "CachedLayerW4A4":
+        """Random weights as LlamaLayerW4A4.random's, `kv_heads` key heads (as many as query heads when
+        None), positions turned over the whole head."""
+        kv_heads = heads if kv_heads is None else kv_heads
+        shapes = {"qkv": ((heads + 2 * kv_heads) * head_dim, hidden), "o": (hidden, heads * head_dim),
+                  "gate_up": (2 * intermediate, hidden), "down": (hidden, intermediate)}
+        return cls(cls._random_weights(shapes, seed, device), heads, kv_heads, head_dim,
+                   rope_frequencies(head_dim, base, device=device)[0], group)
+
     def forward(self, x: torch.Tensor, cache: KVCache4, plan: BatchPlan, window: int = 0) -> torch.Tensor:
         """x: fp16 [tokens, h], the plan's new tokens; their keys and values are added to the cache.
         Rows that no sequence owns come out as the layer's other parts make them (no attention)."""

@@ -101,14 +101,17 @@ class LlamaLayerW4A4(torch.nn.Module):
                device="cuda") -> "LlamaLayerW4A4":
         """Random N(0, 0.02) fp16 weights from the seeded generator of
         w4a4_group_quantized_amd.inputs (numpy PCG64, seed `seed`)."""
+        shapes = {"qkv": (3 * hidden, hidden), "o": (hidden, hidden),
+                  "gate_up": (2 * intermediate, hidden), "down": (hidden, intermediate)}
+        return cls(cls._random_weights(shapes, seed, device), group)
+
+    @classmethod
+    def _random_weights(cls, shapes: dict, seed: int, device) -> dict:
         import numpy as np
 
         from . import inputs
         rng = np.random.default_rng(seed)
-        shapes = {"qkv": (3 * hidden, hidden), "o": (hidden, hidden),
-                  "gate_up": (2 * intermediate, hidden), "down": (hidden, intermediate)}
-        w = {n: torch.from_numpy(inputs.weights(rng, *shapes[n])).to(device) for n in cls.NAMES}
-        return cls(w, group)
+        return {n: torch.from_numpy(inputs.weights(rng, *shapes[n])).to(device) for n in cls.NAMES}
 
     def linear_shapes(self):
         """(K, N) of the four W4A4 GEMMs, in call order."""
