@@ -47,6 +47,7 @@
 #include <algorithm>
 
 #include "attention.h"
+#include "kv4_cut.h"
 #include "layers.h"
 #include "rotary.h"
 
@@ -58,8 +59,6 @@ typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef float float2v __attribute__((ext_vector_type(2)));
 typedef float float4v __attribute__((ext_vector_type(4)));
 
-constexpr int kWaves = 4;
-constexpr int64_t kMaxBlocks = (1 << 24) - 1;
 constexpr float kTiny = 0x1p-80f;      // the least scale of values: 2^15 / kTiny, 2^30 times, stays finite
 constexpr float kLazy = 8.0f, kRoom = 7.0f;     // (fp16 holds weights of 2^(kLazy + kRoom))
 
@@ -451,51 +450,47 @@ __device__ inline void attend(const Kv4AttentionProblem& p, const Sequence& s, i
     const float factor = p.scale * kLog2e * 0x1p20f;
     const int key_at = (lane & 15) * (D / 2) + quad * (D == 64 ? 8 : 16), value_at = lane * (D / 8);
 
-    // Tiles in flight besides the one at hand: with one, a wave's 9 KB do not cover
-    // the memory's latency; two do not fit the registers of the larger rows.
-    constexpr int DEPTH = 1;
-    // lane's token of the tile at t: its row in the cache (row 0 where there is none)
+    // The tile ahead, and the row in the cache of the lane's token of it (row 0 where there
+    // is none).  (Two tiles ahead do not fit the registers of the larger rows, and gained
+    // nothing for the smaller ones.)
     struct Ahead {
         Codes<D> k, v;
         float ks, vs;
         int64_t row;
         bool valid;
-    } ahead[DEPTH];
+    } a;
     int page = 0;
     const auto look = [&](int t) { page = table[min((t + lane) >> c.shift, last)]; };
-    const auto locate = [&](int t, Ahead& a) {
+    const auto locate = [&](int t) {
         a.valid = t + lane < to && page >= 0 && page < c.pages;
         a.row = a.valid ? (((int64_t)page * c.Hkv + g) << c.shift) + ((t + lane) & (c.page - 1)) : 0;
     };
-    const auto base = [&](const Ahead& a, int sub) {
+    const auto base = [&](int sub) {
         const uint32_t low = __builtin_amdgcn_readlane((uint32_t)a.row, 16 * sub);
         const uint32_t high = __builtin_amdgcn_readlane((uint32_t)(a.row >> 32), 16 * sub);
         return (int64_t)((uint64_t)high << 32 | low) * (D / 2);
     };
-    const auto load_k = [&](Ahead& a) {
+    const auto load_k = [&]() {
         a.ks = c.k_scales[a.row];
 #pragma unroll
-        for (int sub = 0; sub < 4; ++sub) load_codes<D, ONCE>(a.k, sub, c.k_codes + base(a, sub) + key_at);
+        for (int sub = 0; sub < 4; ++sub) load_codes<D, ONCE>(a.k, sub, c.k_codes + base(sub) + key_at);
     };
-    const auto load_v = [&](Ahead& a) {
+    const auto load_v = [&]() {
         a.vs = c.v_scales[a.row];
 #pragma unroll
-        for (int sub = 0; sub < 4; ++sub) load_values<D, ONCE>(a.v, sub, c.v_codes + base(a, sub) + value_at);
+        for (int sub = 0; sub < 4; ++sub) load_values<D, ONCE>(a.v, sub, c.v_codes + base(sub) + value_at);
     };
     RawRows<D, RT> raw;
     look(from);
     fetch_rows<D, RT>(p, s, g, row0, raw);
-#pragma unroll
-    for (int i = 0; i < DEPTH; ++i) {
-        locate(from + i * step, ahead[i]);
-        look(from + (i + 1) * step);
-        load_k(ahead[i]);
-        load_v(ahead[i]);
-    }
+    locate(from);
+    look(from + step);
+    load_k();
+    load_v();
     make_rows<BF16, D, RT>(p, s, row0, raw, r);
     const bool scaled = any_scaled(r.unit);
 
-    const auto tile = [&](int t0, Ahead& a) {
+    for (int t0 = from; t0 < to; t0 += step) {
         factors[lane] = key_factor(a.valid, a.ks, factor);
         put_value_factors<64>(factors, lane, a.valid, a.vs);
         const bool edge = t0 + 64 > hi_min || t0 < lo_max || !__all(a.valid);
@@ -511,9 +506,9 @@ __device__ inline void attend(const Kv4AttentionProblem& p, const Sequence& s, i
                 for (int rt = 0; rt < RT; ++rt) x[rt][sub] = mfma(key, r.q[rt][f], f == 0 ? r.bias[rt] : x[rt][sub]);
             }
         }
-        locate(t0 + DEPTH * step, a);
-        look(t0 + (DEPTH + 1) * step);
-        load_k(a);
+        locate(t0 + step);
+        look(t0 + 2 * step);
+        load_k();
         if (scaled) unscale<D, RT>(r, x);
         float top[RT];
         exponents<D, RT>(x, factors, top);
@@ -537,12 +532,7 @@ __device__ inline void attend(const Kv4AttentionProblem& p, const Sequence& s, i
                 }
             }
         }
-        load_v(a);
-    };
-    for (int t0 = from; t0 < to; t0 += DEPTH * step) {
-#pragma unroll
-        for (int i = 0; i < DEPTH; ++i)
-            if (t0 + i * step < to) tile(t0 + i * step, ahead[i]);
+        load_v();
     }
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) r.l[rt] = row_sum(r.l[rt]);
@@ -714,10 +704,7 @@ __device__ inline Place place(const Kv4AttentionProblem& p, int tiles, int x)
 }
 
 // Few rows: the waves of a workgroup have the same rows and every fourth 64
-// tokens; their sums meet in LDS.  256 tokens of a row tile are a unit.
-constexpr int kUnit = 64 * kWaves;
-constexpr int kSorted = 256;     // sequences that a workgroup sorts: one a thread
-
+// tokens; their sums meet in LDS.  256 tokens of a row tile are a unit (kUnit).
 template <int D, int RT>
 struct Meeting {
     float factors[kWaves][192];
@@ -1027,62 +1014,22 @@ __global__ __launch_bounds__(64 * WAVES) void join_kernel(Kv4AttentionProblem p,
     }
 }
 
-// How a call of these sizes is cut.
-struct Cut {
-    bool rows;                  // waves have rows of their own
-    bool share, sorted;
-    int rt, tiles;
-    int64_t blocks;
-    bool deep;                  // a row tile may be in many parts
-};
-
 Cut cut(const Kv4AttentionProblem& p)
 {
-    const int64_t all = (int64_t)p.max_q * p.share, pairs = (int64_t)p.B * p.cache.Hkv;
-    const int cus = compute_units() > 0 ? compute_units() : 256;
-    Cut c{};
-    c.rt = p.cache.D == 256 || all <= 16 ? 1 : 2;
-    // Row tiles of R rows: max_q's for every sequence, or fewer places where the
-    // tokens can fill no more (63 decoding sequences and a prompt of 4096: 373 us
-    // against 889, a prompt of 512: 64 against 566).  Workgroups stride over what passes the grid's 2^32 threads.
-    const auto tile = [&](int64_t R) {
-        const int64_t each = (all + R - 1) / R, places = (p.T * p.share / R + p.B) * p.cache.Hkv;
-        const bool uneven = places < pairs * each && places <= kMaxBlocks;
-        c.tiles = uneven ? 0 : (int)std::max<int64_t>(1, std::min<int64_t>(each, kMaxBlocks / pairs));
-        c.blocks = uneven ? places : pairs * c.tiles;
-    };
-    tile(16 * c.rt * kWaves);
-    c.rows = all > 16 * c.rt && 2 * c.blocks >= 3 * cus;
-    if (!c.rows) tile(16 * c.rt);
-    if (c.rows) return c;
-    // Row tiles of more than 5 units are shared where whole ones leave room for two
-    // workgroups a compute unit: 1 x 2048 tokens of 32 heads 11.5 us against 14, 1 x
-    // 131071 of 8 heads 34.5 against 675; up to 5 units the second launch costs more
-    // (1 x 517 of 32 heads 11.6 us against 8.7), and where the chip is full without it
-    // the starts of the parts do (64 x 4096 of 8 heads 54 us against 50).
-    // (The tokens that a tile sees count, with a window fewer than those cached.)
-    const int64_t seen = p.window ? std::min<int64_t>(p.max_kv, (int64_t)p.window + 16 * c.rt / p.share) : p.max_kv;
-    const int64_t units = (seen + kUnit - 1) / kUnit, total = c.blocks * units;
-    if (units > 5 && c.blocks < 2 * cus) {
-        c.share = true;
-        c.blocks = std::min<int64_t>(total, 2 * cus);
-        // (16 waves for each row where a tile is in more than 8 parts)
-        c.deep = units * c.blocks > 8 * total;
-    }
-    // Whole ones of uneven sequences: the longest first (64 x up to 8192 tokens of 8
-    // heads 77 us to 66; not for few units, 64 x up to 512 10 us to 12).
-    c.sorted = !c.share && c.tiles && units > 5 && p.B > 1 && p.B <= kSorted;
-    return c;
+    const int cus = compute_units();
+    return kv4_cut(p.T, p.B, p.cache.Hkv, p.share, p.cache.D, p.max_q, p.max_kv, p.window, cus > 0 ? cus : 256);
 }
 
 template <bool BF16, int D, int RT>
 hipError_t launch(const Kv4AttentionProblem& p, const Cut& c, const Plan& plan, hipStream_t stream)
 {
     const unsigned blocks = (unsigned)c.blocks;
-    if (c.rows) {
-        if (c.tiles) rows_kernel<BF16, D, RT, false><<<blocks, 256, 0, stream>>>(p, plan);
-        else rows_kernel<BF16, D, RT, true><<<blocks, 256, 0, stream>>>(p, plan);
-        return hipGetLastError();
+    if constexpr (RT == row_tiles(D)) {
+        if (c.rows) {
+            if (c.tiles) rows_kernel<BF16, D, RT, false><<<blocks, 256, 0, stream>>>(p, plan);
+            else rows_kernel<BF16, D, RT, true><<<blocks, 256, 0, stream>>>(p, plan);
+            return hipGetLastError();
+        }
     }
     few_kernel<BF16, D, RT><<<blocks, 256, 0, stream>>>(p, plan);
     if (c.share) {
