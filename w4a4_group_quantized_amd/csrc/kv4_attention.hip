@@ -356,13 +356,13 @@ __device__ inline void raise(Rows<D, RT>& r, float (&top)[RT])
     bool above = false;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        top[rt] = row_max(top[rt]);
-        above |= top[rt] > r.m[rt] + (kLazy + kRoom);
+        top[rt] = row_max(top[rt]) - (kLazy + kRoom);
+        above |= top[rt] > r.m[rt];
     }
     if (!__any(above)) return;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        const float m = top[rt] > r.m[rt] + (kLazy + kRoom) ? top[rt] - kRoom : r.m[rt];
+        const float m = top[rt] > r.m[rt] ? top[rt] + kLazy : r.m[rt];
         const float old = m == r.m[rt] ? 1.0f : __builtin_amdgcn_exp2f(r.m[rt] - m);
         r.m[rt] = m;
         r.l[rt] *= old;
@@ -659,12 +659,11 @@ __device__ inline void attend_shared(const Kv4AttentionProblem& p, const Sequenc
     for (int rt = 0; rt < RT; ++rt) r.l[rt] = row_sum(r.l[rt]);
 }
 
-// numbers 16 t + 4 quad .. + 3 of a lane's row, times `by` (last: with values' scales
-// of 2^108 and more, 1 / l times 2^20 is beyond fp32)
+// numbers 16 t + 4 quad .. + 3 of a lane's row, held in units of 2^-20, times `by`
 template <int D, int RT>
 __device__ inline float4v row_values(const Rows<D, RT>& r, int rt, int t, float by)
 {
-    return (r.o[rt][t] - r.w[rt][0]) * 0x1p20f * by;
+    return (r.o[rt][t] - r.w[rt][0]) * by;
 }
 
 template <bool BF16>
@@ -739,7 +738,7 @@ __device__ inline void few_rows(const Kv4AttentionProblem& p, const Plan& plan, 
         float m = lds.tops[0][row].x;
 #pragma unroll
         for (int v = 1; v < kWaves; ++v) m = fmaxf(m, lds.tops[v][row].x);
-        const float by = r.m[rt] == m ? 1.0f : __builtin_amdgcn_exp2f(r.m[rt] - m);
+        const float by = (r.m[rt] == m ? 1.0f : __builtin_amdgcn_exp2f(r.m[rt] - m)) * 0x1p20f;
 #pragma unroll
         for (int t = 0; t < D / 16; ++t)
             *reinterpret_cast<float4v*>(&lds.sums[wave][row][16 * t + 4 * (lane >> 4)]) = row_values(r, rt, t, by);
@@ -825,8 +824,8 @@ __global__ __launch_bounds__(256, 2) void rows_kernel(Kv4AttentionProblem p, Pla
             const int64_t at = (s.q0 + i) * p.Hq + g * share + (row - i * share);
             const float by = r.l[rt] == 0.0f ? 0.0f : 1.0f / r.l[rt];
 #pragma unroll
-            for (int t = 0; t < D / 16; ++t)
-                store4<BF16>(p.out, at * D + 16 * t + 4 * (lane >> 4), row_values(r, rt, t, by));
+            for (int t = 0; t < D / 16; ++t)           // (1 / l may be so large that 2^20 times it is beyond fp32)
+                store4<BF16>(p.out, at * D + 16 * t + 4 * (lane >> 4), row_values(r, rt, t, 0x1p20f) * by);
             if (p.lse && lane < 16) p.lse[at] = log_sum(r.m[rt], r.l[rt]);
         }
     }
