@@ -80,6 +80,11 @@ class BatchPlan:
             if cu_q is not None:
                 raise ValueError("tokens has to be given with cu_q (it is in device memory)")
             tokens = B
+        if cu_q is None and tokens != B:
+            if tokens < B:
+                raise ValueError(f"{tokens} rows do not hold one token of each of {B} sequences")
+            cu_q = torch.arange(B + 1, dtype=torch.int32, device=table.device)
+            max_q = 1 if max_q is None else max_q
         row = torch.arange(tokens, device=table.device)
         if cu_q is None:
             sequence, new = row, torch.ones_like(row)
