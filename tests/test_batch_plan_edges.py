@@ -22,3 +22,14 @@ def test_one_token_a_sequence_and_padding_behind():
 def test_fewer_rows_than_sequences():
     with pytest.raises(ValueError):
         BatchPlan(i32([[4, -1], [2, 7]]), i32([5, 18]), page=16, tokens=1)
+
+
+@pytest.mark.parametrize("cu", [None, [0], [2]])
+def test_no_sequences(cu):
+    """An idle step: rows of padding only."""
+    none = torch.zeros((0, 3), dtype=torch.int32)
+    for tokens in (0, 4):
+        plan = BatchPlan(none, i32([]), None if cu is None else i32(cu), page=16, tokens=tokens)
+        assert plan.positions.tolist() == [0] * tokens and plan.slots.tolist() == [-1] * tokens
+        assert plan.positions.dtype == plan.slots.dtype == torch.int64
+        assert tokens == 0 or plan.cu_q is not None

@@ -39,3 +39,12 @@ def test_decoding_with_rows_behind_the_batch(dev, layer):
         assert torch.equal(a, b)
     # (fp32 sums in another order: at most a step of fp16 and of a code of the next linear's input)
     assert ((y[:3] - want).float().norm(dim=-1) <= 0.1 * want.float().norm(dim=-1)).all()
+
+
+def test_step_without_sequences(dev, layer):
+    """Rows of padding only: nothing is stored, every row comes out."""
+    cache = KVCache4(2, 2, 64, 16, dev)
+    none = torch.zeros((0, 3), dtype=torch.int32, device=dev)
+    x = torch.randn((4, 256), generator=torch.Generator().manual_seed(2)).half().to(dev)
+    y = layer(x, cache, BatchPlan(none, i32([], dev), page=16, tokens=4))
+    assert torch.isfinite(y).all() and all((t == 0).all() for t in cache.tensors)

@@ -85,7 +85,16 @@ class BatchPlan:
                 raise ValueError(f"{tokens} rows do not hold one token of each of {B} sequences")
             cu_q = torch.arange(B + 1, dtype=torch.int32, device=table.device)
             max_q = 1 if max_q is None else max_q
+        self.positions, self.slots = self._places(table, kv_lens, cu_q, page, tokens)
+        self.table, self.kv_lens, self.cu_q = table, kv_lens, cu_q
+        self.page, self.tokens, self.max_q, self.max_kv = page, tokens, max_q, max_kv
+
+    @staticmethod
+    def _places(table, kv_lens, cu_q, page: int, tokens: int):
+        B, cols = table.shape
         row = torch.arange(tokens, device=table.device)
+        if B == 0:
+            return torch.zeros_like(row), torch.full_like(row, -1)
         if cu_q is None:
             sequence, new = row, torch.ones_like(row)
         else:
@@ -98,10 +107,8 @@ class BatchPlan:
             live &= row >= cu_q[0]
         held = position.clamp(0, cols * page - 1)
         at = table.long()[owner, held // page]
-        self.positions = torch.where(live, position, torch.zeros_like(position))
-        self.slots = torch.where(live & (at >= 0), at * page + held % page, torch.full_like(position, -1))
-        self.table, self.kv_lens, self.cu_q = table, kv_lens, cu_q
-        self.page, self.tokens, self.max_q, self.max_kv = page, tokens, max_q, max_kv
+        return (torch.where(live, position, torch.zeros_like(position)),
+                torch.where(live & (at >= 0), at * page + held % page, torch.full_like(position, -1)))
 
 
 class KVCache4:
