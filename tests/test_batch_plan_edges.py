@@ -33,3 +33,13 @@ def test_no_sequences(cu):
         assert plan.positions.tolist() == [0] * tokens and plan.slots.tolist() == [-1] * tokens
         assert plan.positions.dtype == plan.slots.dtype == torch.int64
         assert tokens == 0 or plan.cu_q is not None
+
+
+def test_refusals():
+    """What the cache or the attention would refuse only after the tokens are stored, or index out of range."""
+    table, lens, cu = i32([[4, -1], [2, 7]]), i32([5, 18]), i32([0, 1, 2])
+    for bad in (dict(page=0), dict(page=8), dict(page=24), dict(page=2048), dict(table=table[0]), dict(table=table.long()),
+                dict(table=table[:, :0]), dict(kv_lens=lens[:1]), dict(kv_lens=lens.long()), dict(cu_q=cu[:2]),
+                dict(cu_q=cu.long()), dict(tokens=-1), dict(kv_lens=lens.to("meta")), dict(table=table.t())):
+        with pytest.raises(ValueError):
+            BatchPlan(**{**dict(table=table, kv_lens=lens, cu_q=cu, page=16, tokens=2), **bad})

@@ -75,7 +75,18 @@ class BatchPlan:
 
     def __init__(self, table, kv_lens, cu_q=None, *, page: int, tokens: int | None = None, max_q: int | None = None,
                  max_kv: int | None = None):
-        B, cols = table.shape
+        if page < 16 or page > 1024 or page & (page - 1):
+            raise ValueError(f"page must be a power of two from 16 to 1024, got {page}")
+        if table.dim() != 2 or table.shape[1] < 1:
+            raise ValueError(f"table must be [B, cols] with a column at least, got {tuple(table.shape)}")
+        B = table.shape[0]
+        for name, t, shape in (("table", table, table.shape), ("kv_lens", kv_lens, (B,)), ("cu_q", cu_q, (B + 1,))):
+            if t is not None and (t.dtype != torch.int32 or t.shape != shape or t.device != table.device
+                                  or not t.is_contiguous()):
+                raise ValueError(f"{name} must be contiguous int32 {tuple(shape)} on {table.device}, "
+                                 f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+        if tokens is not None and tokens < 0:
+            raise ValueError(f"tokens must not be negative, got {tokens}")
         if tokens is None:
             if cu_q is not None:
                 raise ValueError("tokens has to be given with cu_q (it is in device memory)")
