@@ -701,8 +701,10 @@ def kv4_cache(pages: int, kv_heads: int, head_dim: int, page: int = 64, device="
     """An empty 4-bit cache of `pages` pages of `page` tokens: (k_codes, k_scales, v_codes,
     v_scales), the tensors that kv4_append, kv4_read and kv4_attention take as `cache`."""
     import torch
-    if head_dim % 32 or page % 16:
-        raise ValueError(f"head_dim must be 64, 128 or 256 and page a power of two from 16, got {head_dim, page}")
+    if head_dim not in (64, 128, 256) or page < 16 or page > 1024 or page & (page - 1):
+        raise ValueError(f"head_dim must be 64, 128 or 256 and page a power of two from 16 to 1024, got {head_dim, page}")
+    if pages < 1 or kv_heads < 1 or kv_heads > 1024:
+        raise ValueError(f"a page and 1 to 1024 heads are needed, got {pages, kv_heads}")
     codes = {"dtype": torch.uint8, "device": device}
     return (torch.zeros((pages, kv_heads, page, head_dim // 2), **codes),
             torch.zeros((pages, kv_heads, page), device=device),
