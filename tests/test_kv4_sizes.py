@@ -1,4 +1,4 @@
-"""Sizes that the 4-bit cache's calls refuse are refused where the cache is made (CPU)."""
+"""Sizes that the 4-bit cache's calls refuse are refused where the cache is made and the workspace asked for (CPU)."""
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -23,3 +23,21 @@ def test_cache_sizes():
             k, ks, v, vs = apex4.kv4_cache(3, 2, D, page, "cpu")
             assert k.shape == (3, 2, page, D // 2) and v.shape == (3, 2, page // 16, 8 * D)
             assert ks.shape == vs.shape == (3, 2, page)
+
+
+@pytest.mark.parametrize("at", range(1, 7))
+@pytest.mark.parametrize("by", [2 ** 32, -2 ** 32, 2 ** 31])
+def test_workspace_of_numbers_that_do_not_fit_the_library(monkeypatch, at, by):
+    """Taken modulo 2^32 most of them are right arguments; kv4_attention refuses them too."""
+    called = []
+
+    class Lib:
+        apex4_kv4_attention_workspace_size = staticmethod(lambda *args: called.append(args) or 64)
+
+    monkeypatch.setattr(apex4, "_lib", Lib)
+    args = [1, 1, 4, 1, 64, 1, 5000]
+    assert apex4.kv4_attention_workspace_size(*args) == 64
+    args[at] += by
+    with pytest.raises(ValueError):
+        apex4.kv4_attention_workspace_size(*args)
+    assert len(called) == 1

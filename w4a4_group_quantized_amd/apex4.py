@@ -795,6 +795,8 @@ def kv4_read(cache, slots, dtype=None, out=None):
 
 def kv4_attention_workspace_size(T: int, B: int, Hq: int, Hkv: int, D: int, max_q: int, max_kv: int) -> int:
     """Bytes that `kv4_attention` takes on the current device."""
+    if (B | Hq | Hkv | D | max_q | max_kv) >> 31:
+        raise ValueError(f"sizes must fit 31 bits, got {B, Hq, Hkv, D, max_q, max_kv}")
     return int(lib().apex4_kv4_attention_workspace_size(T, B, Hq, Hkv, D, max_q, max_kv))
 
 
