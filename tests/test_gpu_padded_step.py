@@ -48,3 +48,11 @@ def test_step_without_sequences(dev, layer):
     x = torch.randn((4, 256), generator=torch.Generator().manual_seed(2)).half().to(dev)
     y = layer(x, cache, BatchPlan(none, i32([], dev), page=16, tokens=4))
     assert torch.isfinite(y).all() and all((t == 0).all() for t in cache.tensors)
+
+
+def test_step_without_rows(dev, layer):
+    cache = KVCache4(2, 2, 64, 16, dev)
+    x = torch.zeros((0, 256), dtype=torch.float16, device=dev)
+    assert layer(x, cache, BatchPlan(torch.zeros((0, 3), dtype=torch.int32, device=dev), i32([], dev), page=16)).shape == x.shape
+    plan = BatchPlan(i32([[0, 1]], dev), i32([3], dev), i32([0, 0], dev), page=16, tokens=0)
+    assert layer(x, cache, plan).shape == x.shape and all((t == 0).all() for t in cache.tensors)

@@ -189,7 +189,7 @@ class CachedLayerW4A4(LlamaLayerW4A4):
         q = cache.append(rows[:, h:h + k], rows[:, h + k:], plan, self.inv_freq, rows[:, :h], **self.turn)
         out = torch.zeros_like(q) if plan.cu_q is not None else None      # (rows behind the last sequence stay zero)
         o = cache.attend(q, plan, window=window, out=out)
-        x = x + self.o(o.view(x.shape[0], -1))
+        x = x + self.o(o.flatten(1))
         gu = self.gate_up(x)
         i = self.intermediate
         return x + self.down(torch.nn.functional.silu(gu[:, :i]) * gu[:, i:])
