@@ -562,7 +562,8 @@ apex4_status apex4_kv4_read(const void* k_codes, const float* k_scales, const vo
  *   matrix units and sum in fp32; a weight p_j times the scale of v_j is rounded to
  *   fp16 for the product with the codes (2^-11 of itself, or 2^-32 of the largest so
  *   far), and counts unrounded in the sum below it.  A value's scale below 2^-80 counts as
- *   2^-80; |scale| times a key's scale has to stay below 2^100.
+ *   2^-80; the values' scales that a query sees have to lie within 2^100 of each
+ *   other (those below 2^-80 as that), and |scale| times a key's scale below 2^100.
  *   Queries and scales that are not finite show in the rows that see them only.
  *   workspace: at least apex4_kv4_attention_workspace_size() bytes (NULL allowed
  *   when that is 0; 0 for invalid or empty sizes), 16-byte aligned, caller-owned,

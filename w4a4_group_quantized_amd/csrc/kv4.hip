@@ -8,8 +8,10 @@
 // find the head's largest number by lane moves.  Measured: 4096 tokens x 64 heads
 // x 128 bf16 turned in 22 us (6.0 TB/s, the last-level cache holds part of it);
 // 4096 tokens of 64 query and 8 key heads appended in 30 us (160 MB, 5.3 TB/s);
-// 65521 tokens of 8 heads read in 55 us again and again, 63 with other work between
-// (340 MB, 5.4-6.2 TB/s).
+// 65521 tokens of 8 heads read in 49 to 58 us one call after the other (340 MB, 5.8-7.0
+// TB/s), in 77 where other work's lines are in the caches (4.4 TB/s).  fp32 heads of 128
+// and all of 256 keep to the caches (see read): 65521 tokens of 8 heads of 128 in
+// fp32 165 us (3.7 TB/s).
 #include "attention.h"
 #include "quant_rule.h"
 #include "rotary.h"
