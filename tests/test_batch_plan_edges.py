@@ -40,6 +40,16 @@ def test_refusals():
     table, lens, cu = i32([[4, -1], [2, 7]]), i32([5, 18]), i32([0, 1, 2])
     for bad in (dict(page=0), dict(page=8), dict(page=24), dict(page=2048), dict(table=table[0]), dict(table=table.long()),
                 dict(table=table[:, :0]), dict(kv_lens=lens[:1]), dict(kv_lens=lens.long()), dict(cu_q=cu[:2]),
-                dict(cu_q=cu.long()), dict(tokens=-1), dict(kv_lens=lens.to("meta")), dict(table=table.t())):
+                dict(cu_q=cu.long()), dict(tokens=-1), dict(kv_lens=lens.to("meta"))):
         with pytest.raises(ValueError):
             BatchPlan(**{**dict(table=table, kv_lens=lens, cu_q=cu, page=16, tokens=2), **bad})
+
+
+def test_parts_of_wider_tables():
+    """The first columns of a table with room for more, every other length: as copies of them."""
+    wide = i32([[4, -1, 9], [2, 7, 9]])
+    lens, cu = i32([5, 0, 18, 0]), i32([0, 9, 1, 9, 2])
+    plan = BatchPlan(wide[:, :2], lens[::2], cu[::2], page=16, tokens=2)
+    want = BatchPlan(wide[:, :2].contiguous(), i32([5, 18]), i32([0, 1, 2]), page=16, tokens=2)
+    for name in ("table", "kv_lens", "cu_q", "positions", "slots"):
+        assert torch.equal(getattr(plan, name), getattr(want, name)) and getattr(plan, name).is_contiguous()

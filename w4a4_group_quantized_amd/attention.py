@@ -81,9 +81,8 @@ class BatchPlan:
             raise ValueError(f"table must be [B, cols] with a column at least, got {tuple(table.shape)}")
         B = table.shape[0]
         for name, t, shape in (("table", table, table.shape), ("kv_lens", kv_lens, (B,)), ("cu_q", cu_q, (B + 1,))):
-            if t is not None and (t.dtype != torch.int32 or t.shape != shape or t.device != table.device
-                                  or not t.is_contiguous()):
-                raise ValueError(f"{name} must be contiguous int32 {tuple(shape)} on {table.device}, "
+            if t is not None and (t.dtype != torch.int32 or t.shape != shape or t.device != table.device):
+                raise ValueError(f"{name} must be int32 {tuple(shape)} on {table.device}, "
                                  f"got {t.dtype} {tuple(t.shape)} on {t.device}")
         if tokens is not None and tokens < 0:
             raise ValueError(f"tokens must not be negative, got {tokens}")
@@ -97,7 +96,9 @@ class BatchPlan:
             cu_q = torch.arange(B + 1, dtype=torch.int32, device=table.device)
             max_q = 1 if max_q is None else max_q
         self.positions, self.slots = self._places(table, kv_lens, cu_q, page, tokens)
-        self.table, self.kv_lens, self.cu_q = table, kv_lens, cu_q
+        # (the attention takes them contiguous: parts of wider tables are copied)
+        self.table, self.kv_lens = table.contiguous(), kv_lens.contiguous()
+        self.cu_q = None if cu_q is None else cu_q.contiguous()
         self.page, self.tokens, self.max_q, self.max_kv = page, tokens, max_q, max_kv
 
     @staticmethod

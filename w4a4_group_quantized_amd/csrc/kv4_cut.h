@@ -17,7 +17,7 @@ constexpr int row_tiles(int D) { return D == 256 ? 1 : 2; }
 
 struct Cut {
     bool rows;                  // waves have rows of their own
-    bool share, sorted;         // (see Plan)
+    bool share, sorted;         // (see Plan in kv4_attention.hip)
     int rt, tiles;              // row tiles of 16 a wave; places of a sequence and key head (0: numbered over the batch)
     int64_t blocks;
     bool deep;                  // a row tile may be in many parts
