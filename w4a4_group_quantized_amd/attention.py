@@ -144,6 +144,8 @@ class KVCache4:
     def attend(self, q, plan: BatchPlan, **args):
         """Attention of the plan's tokens over their sequences (apex4.kv4_attention's arguments)."""
         self._fits(plan)
+        if q.shape[0] != plan.tokens:
+            raise ValueError(f"q has {q.shape[0]} rows, the plan {plan.tokens}")
         return apex4.kv4_attention(q, self.tensors, plan.table, plan.kv_lens, plan.cu_q, max_q=plan.max_q,
                                    max_kv=plan.max_kv, **args)
 
