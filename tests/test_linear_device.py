@@ -31,6 +31,9 @@ class Host:
     def is_contiguous(self):
         return True
 
+    def dim(self):
+        return len(self.shape)
+
     def numel(self):
         return self.shape.numel()
 
@@ -72,3 +75,27 @@ def test_a_linear_layer_runs_and_packs_on_its_device(calls):
     assert [c[0] for c in calls] == ["apex4_pack_weight", "size", "apex4_linear_w4a4"]
     assert all(c[1] == 1 for c in calls) and Device.current == 0
     assert all(c[2] == 1001 for c in calls if c[0] != "size")            # the device's own stream
+
+
+def test_the_linear_layers_parts_run_on_their_device(calls, monkeypatch):
+    """The quantizers and products that the layer's call is made of, and their forms of other codes."""
+    f16, f32 = torch.float16, torch.float32
+    for name in ("apex4_quantize_act", "apex4_gemm_w4a4", "apex4_gemm_w4a4_debug", "apex4_gemm_w4a4_noalloc",
+                 "apex4_quantize_f8", "apex4_gemm_w4a4_f8", "apex4_quantize_f6", "apex4_gemm_w4a4_f6",
+                 "apex4_gemm_workspace_size"):
+        value = 0 if "workspace" not in name else 64
+        setattr(apex4._lib, name, staticmethod(
+            lambda *args, name=name, value=value: calls.append((name, Device.current, args[-1])) or value))
+    x, w = Host(3, 256, dtype=f16), Host(256, 256, dtype=f16)
+    qa, sa = apex4.quantize_act(x, 128)
+    qw, sw = apex4.pack_weight(w, 128)
+    y = Host(3, 256, dtype=f16)
+    apex4.gemm(qa, sa, 128, qw, sw, 128)
+    apex4.gemm(qa, sa, 128, qw, sw, 128, want_psum=True, psum_rows=(0, 1, 2))
+    apex4.gemm_noalloc(qa, sa, 128, qw, sw, 128, y16=y)
+    a8, w8 = apex4.quantize_f8(x), apex4.quantize_f8(w)
+    apex4.gemm_f8(*a8, *w8)
+    a6, w6 = apex4.quantize_f6(x), apex4.quantize_f6(w)
+    apex4.gemm_f6(*a6, *w6)
+    assert len(calls) == 14 and all(c[1] == 1 for c in calls), calls
+    assert all(c[2] == 1001 for c in calls if "workspace" not in c[0])

@@ -140,8 +140,7 @@ def quantize_act(x, group: int, out=None):
         qa, sa = out
         _need_gpu(qa, "qa", torch.uint8, (M, K // 2), x.device)
         _need_gpu(sa, "s_a", torch.float32, (M, _cols(K, group)), x.device)
-    _check("apex4_quantize_act", lib().apex4_quantize_act(
-        _ptr(x), M, K, group, _ptr(qa), _ptr(sa), _stream(torch, x.device)))
+    _call("apex4_quantize_act", x.device, _ptr(x), M, K, group, _ptr(qa), _ptr(sa))
     return qa, sa
 
 
@@ -191,17 +190,14 @@ def gemm(qa, sa, ga: int, qw, sw, gw: int, K: int | None = None, *, want_y32: bo
     row0, step, count = psum_rows if psum_rows is not None else (0, 1, M)
     if want_psum:
         psum = torch.empty((count, N, G), dtype=torch.int32, device=dev)
-    ws_bytes = workspace_size(M, N, K, ga, gw)
+    ws_bytes = _size("apex4_gemm_workspace_size", dev, M, N, K, ga, gw)
     ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
     if psum_rows is None:
-        _check("apex4_gemm_w4a4", lib().apex4_gemm_w4a4(
-            _ptr(qa), _ptr(sa), ga, _ptr(qw), _ptr(sw), gw, M, N, K,
-            _ptr(y16), _ptr(y32), _ptr(psum), _ptr(ws), ws_bytes, _stream(torch, dev)))
+        _call("apex4_gemm_w4a4", dev, _ptr(qa), _ptr(sa), ga, _ptr(qw), _ptr(sw), gw, M, N, K, _ptr(y16),
+              _ptr(y32), _ptr(psum), _ptr(ws), ws_bytes)
     else:
-        _check("apex4_gemm_w4a4_debug", lib().apex4_gemm_w4a4_debug(
-            _ptr(qa), _ptr(sa), ga, _ptr(qw), _ptr(sw), gw, M, N, K,
-            _ptr(y16), _ptr(y32), row0, step, count if want_psum else 0, _ptr(psum),
-            _ptr(ws), ws_bytes, _stream(torch, dev)))
+        _call("apex4_gemm_w4a4_debug", dev, _ptr(qa), _ptr(sa), ga, _ptr(qw), _ptr(sw), gw, M, N, K, _ptr(y16),
+              _ptr(y32), row0, step, count if want_psum else 0, _ptr(psum), _ptr(ws), ws_bytes)
     if want_y32 or want_psum:
         return y16, y32, psum
     return y16
@@ -221,8 +217,8 @@ def gemm_noalloc(qa, sa, ga: int, qw, sw, gw: int, K: int | None = None, *, y16,
     _need_gpu(y16, "y16", torch.float16, (M, N), dev)
     if y32 is not None:
         _need_gpu(y32, "y32", torch.float32, (M, N), dev)
-    _check("apex4_gemm_w4a4_noalloc", lib().apex4_gemm_w4a4_noalloc(
-        _ptr(qa), _ptr(sa), ga, _ptr(qw), _ptr(sw), gw, M, N, K, _ptr(y16), _ptr(y32), _stream(torch, dev)))
+    _call("apex4_gemm_w4a4_noalloc", dev, _ptr(qa), _ptr(sa), ga, _ptr(qw), _ptr(sw), gw, M, N, K, _ptr(y16),
+          _ptr(y32))
     return y16
 
 
@@ -276,8 +272,7 @@ def quantize_f8(x, group: int = 128, out=None):
         q8, s = out
         _need_gpu(q8, "q8", torch.uint8, (rows, K), x.device)
         _need_gpu(s, "s", torch.float32, (rows, _cols(K, group)), x.device)
-    _check("apex4_quantize_f8", lib().apex4_quantize_f8(
-        _ptr(x), rows, K, group, _ptr(q8), _ptr(s), _stream(torch, x.device)))
+    _call("apex4_quantize_f8", x.device, _ptr(x), rows, K, group, _ptr(q8), _ptr(s))
     return q8, s
 
 
@@ -306,9 +301,8 @@ def gemm_f8(qa8, sa, qw8, sw, group: int | None = None, *, want_y32: bool = Fals
     if want_y32 and y32 is None:
         y32 = torch.empty((M, N), dtype=torch.float32, device=dev)
     psum = torch.empty((M, N, _cols(K, group)), dtype=torch.int32, device=dev) if want_psum else None
-    _check("apex4_gemm_w4a4_f8", lib().apex4_gemm_w4a4_f8(
-        _ptr(qa8), _ptr(sa), _ptr(qw8), _ptr(sw), group, M, N, K, _ptr(y16), _ptr(y32), _ptr(psum),
-        _stream(torch, dev)))
+    _call("apex4_gemm_w4a4_f8", dev, _ptr(qa8), _ptr(sa), _ptr(qw8), _ptr(sw), group, M, N, K, _ptr(y16),
+          _ptr(y32), _ptr(psum))
     if want_y32 or want_psum:
         return y16, y32, psum
     return y16
@@ -332,8 +326,7 @@ def quantize_f6(x, group: int = 128, out=None):
         q6, s = out
         _need_gpu(q6, "q6", torch.uint8, (f6_rows(rows), K * 3 // 4), x.device)
         _need_gpu(s, "s", torch.float32, (rows, _cols(K, group)), x.device)
-    _check("apex4_quantize_f6", lib().apex4_quantize_f6(
-        _ptr(x), rows, K, group, _ptr(q6), _ptr(s), _stream(torch, x.device)))
+    _call("apex4_quantize_f6", x.device, _ptr(x), rows, K, group, _ptr(q6), _ptr(s))
     return q6, s
 
 
@@ -357,11 +350,10 @@ def gemm_f6(qa6, sa, qw6, sw, *, want_y32: bool = False, want_psum: bool = False
     if want_y32 and y32 is None:
         y32 = torch.empty((M, N), dtype=torch.float32, device=dev)
     psum = torch.empty((M, N, K // 128), dtype=torch.int32, device=dev) if want_psum else None
-    ws_bytes = workspace_size(M, N, K, 128, 128)
+    ws_bytes = _size("apex4_gemm_workspace_size", dev, M, N, K, 128, 128)
     ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev) if ws_bytes else None
-    _check("apex4_gemm_w4a4_f6", lib().apex4_gemm_w4a4_f6(
-        _ptr(qa6), _ptr(sa), _ptr(qw6), _ptr(sw), M, N, K, _ptr(y16), _ptr(y32), _ptr(psum),
-        _ptr(ws), ws_bytes, _stream(torch, dev)))
+    _call("apex4_gemm_w4a4_f6", dev, _ptr(qa6), _ptr(sa), _ptr(qw6), _ptr(sw), M, N, K, _ptr(y16), _ptr(y32),
+          _ptr(psum), _ptr(ws), ws_bytes)
     if want_y32 or want_psum:
         return y16, y32, psum
     return y16
