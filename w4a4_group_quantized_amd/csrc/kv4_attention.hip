@@ -206,7 +206,9 @@ __device__ inline void make_rows(const Kv4AttentionProblem& p, const Sequence& s
             }
         }
         most = row_max(most);
-        // rows outside fp16's comfortable range are brought to 16..32 by a power of two
+        // rows outside fp16's comfortable range are brought to 16..32 by a power of two (a bf16
+        // number is exact in fp16 down to 2^-16, here 2^-10 of the row's largest at the least; smaller
+        // ones are off by up to 2^-25, 2^-19 of the largest)
         int e = 0;
         if (!(most >= 0x1p-6f && most < 0x1p14f) && most > 0.0f && most < INFINITY) e = 5 - __builtin_amdgcn_frexp_expf(most);
         r.unit[rt] = __builtin_amdgcn_ldexpf(1.0f, -e);
@@ -372,7 +374,10 @@ __device__ inline void raise(Rows<D, RT>& r, float (&top)[RT])
     }
 }
 
-// Exponents to weights, the operands of the second product.
+// Exponents to weights, the operands of the second product.  fp16, because the codes
+// are exact beside it (a bf16 operand has no subnormals of that size, and 3 bits
+// less): a weight is off by 2^-11 of itself, which over a row's tokens makes 2.6 to 2.8
+// 10^-4 of the largest output of what is 2.0 to 2.1 with weights in fp32 (fp16's own rounding).
 template <int D, int RT, int NS>
 __device__ inline void weights(Rows<D, RT>& r, const float4v (&x)[RT][NS], const float* factors, half8 (&w)[RT][NS / 2])
 {
