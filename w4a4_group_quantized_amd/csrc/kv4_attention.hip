@@ -375,9 +375,9 @@ __device__ inline void raise(Rows<D, RT>& r, float (&top)[RT])
 }
 
 // Exponents to weights, the operands of the second product.  fp16, because the codes
-// are exact beside it (a bf16 operand has no subnormals of that size, and 3 bits
-// less): a weight is off by 2^-11 of itself, which over a row's tokens makes 2.6 to 2.8
-// 10^-4 of the largest output of what is 2.0 to 2.1 with weights in fp32 (fp16's own rounding).
+// are exact beside it and bf16 would hold 3 bits less: a weight is off by 2^-11 of
+// itself.  Outputs in fp16 are 2.6 to 2.8 10^-4 of the largest off for it, and 2.0 to
+// 2.1 with weights in fp32 (the outputs' own rounding).
 template <int D, int RT, int NS>
 __device__ inline void weights(Rows<D, RT>& r, const float4v (&x)[RT][NS], const float* factors, half8 (&w)[RT][NS / 2])
 {
