@@ -69,7 +69,7 @@ def rope_frequencies(rotary: int, base: float = 10000.0, *, scaling: str | None 
 class BatchPlan:
     """Where the newest tokens of a batch stand: table int32 [B, cols] of pages, kv_lens int32 [B]
     cached tokens with the new ones, cu_q int32 [B + 1] where each sequence's new tokens begin
-    (None: one a sequence).  `tokens` is the number of rows of a step, with the padding before the
+    (None: one a sequence, its first B rows).  `tokens` is the number of rows of a step, with the padding before the
     first sequence and behind the last.  From them, on the GPU and without a copy to the host: positions and slots
     int64 [tokens] (slot -1: nothing is stored).  max_q, max_kv: see apex4.kv4_attention."""
 
